@@ -1,0 +1,341 @@
+// Host side of libctcpb_lm.so: argument checks and launches (C ABI in
+// include/ctcpb_lm.h).
+#include "ctcpb_lm.h"
+
+#include <climits>
+#include <exception>
+#include <string>
+
+#include "attention.h"
+#include "cache.h"
+#include "ctcpb.h"
+
+using namespace ctcpb_lm;
+
+namespace {
+
+thread_local std::string g_err;
+
+int ok() {
+  g_err.clear();
+  return CTCPB_OK;
+}
+
+int fail(int code, const char* msg) {
+  g_err = msg;
+  return code;
+}
+
+int launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) return ok();
+  g_err = std::string(what) + " launch failed: " + hipGetErrorString(e);
+  return CTCPB_ERR_DEVICE;
+}
+
+// No C++ exception leaves a C entry point (the only ones possible here are
+// allocation failures of the error text).
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return CTCPB_ERR_DEVICE;
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int log2_of(int32_t v) {
+  int n = 0;
+  while ((1 << n) < v) ++n;
+  return n;
+}
+
+bool page_size_ok(int32_t ps) { return ps >= 4 && ps <= 256 && (ps & (ps - 1)) == 0; }
+
+int elem_size(int32_t dtype) {
+  return dtype == CTCPB_LM_BF16 || dtype == CTCPB_LM_F16 ? 2 : dtype == CTCPB_LM_F32 ? 4 : 0;
+}
+
+constexpr const char* kBadPage = "page_size must be a power of two in 4..256";
+constexpr const char* kBadType = "dtype must be CTCPB_LM_BF16, CTCPB_LM_F16 or CTCPB_LM_F32";
+constexpr const char* kNull = "a required pointer is NULL";
+
+int check_table(int32_t rows, int64_t stride, int32_t width, int32_t page_size) {
+  if (rows < 0 || width < 0) return fail(CTCPB_ERR_INVALID, "rows and table_width must be >= 0");
+  if (!page_size_ok(page_size)) return fail(CTCPB_ERR_INVALID, kBadPage);
+  if (stride < width) return fail(CTCPB_ERR_INVALID, "table_stride must be >= table_width");
+  if ((int64_t)width * page_size > (1 << 30))
+    return fail(CTCPB_ERR_INVALID, "table_width * page_size must be at most 2^30");
+  return CTCPB_OK;
+}
+
+int check_pages(int32_t num_pages, int32_t page_size) {
+  if (!page_size_ok(page_size)) return fail(CTCPB_ERR_INVALID, kBadPage);
+  if (num_pages < 1 || (int64_t)num_pages * page_size > INT_MAX)
+    return fail(CTCPB_ERR_INVALID, "num_pages must be >= 1 and num_pages * page_size below 2^31");
+  return CTCPB_OK;
+}
+
+int check_cache(const ctcpb_lm_cache* c) {
+  if (!c || !c->data) return fail(CTCPB_ERR_INVALID, kNull);
+  if (c->stride_page < 0 || c->stride_token < 0 || c->stride_head < 0)
+    return fail(CTCPB_ERR_INVALID, "cache strides must be >= 0");
+  return CTCPB_OK;
+}
+
+CacheView view(const ctcpb_lm_cache* c, int es) {
+  return CacheView{static_cast<char*>(c->data), c->stride_page * es, c->stride_token * es,
+                   c->stride_head * es};
+}
+
+bool wide_cache(const CacheView& v) {
+  return aligned(v.data, 16) && v.page % 16 == 0 && v.token % 16 == 0 && v.head % 16 == 0;
+}
+
+// ------------------------------------------------------------- attention --
+
+// The launch plan of an attention call, a function of sizes only (the lengths
+// stay on the device).
+struct AttnPlan {
+  int32_t head_tiles, chunk, splits, max_len, tile;
+  size_t bytes;
+};
+
+AttnPlan plan_attention(int32_t dtype, int32_t rows, int32_t heads, int32_t kv_heads, int32_t D,
+                        int32_t max_len, int32_t window) {
+  AttnPlan p;
+  p.tile = dtype == CTCPB_LM_F32 ? 16 : 32;
+  p.head_tiles = (heads / kv_heads + 15) / 16;
+  p.max_len = max_len;
+  // tokens a row can have in its range (a window starts at a tile's edge)
+  int64_t span = max_len;
+  if (window > 0 && (int64_t)window + p.tile < span) span = (int64_t)window + p.tile;
+  const int64_t blocks = (int64_t)rows * kv_heads * p.head_tiles;
+  const int64_t step = kAttnWaves * p.tile;
+  int64_t want = blocks ? (1024 + blocks - 1) / blocks : 1;
+  int64_t chunk = (span + want - 1) / want;
+  chunk = (chunk + step - 1) / step * step;
+  if (chunk < 2 * step) chunk = 2 * step;
+  p.chunk = (int32_t)(chunk < INT_MAX / 2 ? chunk : INT_MAX / 2);
+  p.splits = (int32_t)((span + p.chunk - 1) / p.chunk);
+  if (p.splits < 1) p.splits = 1;
+  p.bytes = p.splits > 1 ? (size_t)rows * heads * p.splits * (D + 2) * sizeof(float) : 0;
+  return p;
+}
+
+int check_attention(int32_t dtype, int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t D,
+                    int32_t max_len, int32_t window) {
+  if (!elem_size(dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
+  if (rows < 0) return fail(CTCPB_ERR_INVALID, "rows must be >= 0");
+  if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads)
+    return fail(CTCPB_ERR_INVALID, "q_heads must be a multiple of kv_heads >= 1");
+  if (D < 8 || D % 8) return fail(CTCPB_ERR_INVALID, "head_dim must be a multiple of 8");
+  if (D > 256) return fail(CTCPB_ERR_UNSUPPORTED, "head_dim above 256");
+  if (max_len < 0 || max_len > (1 << 30) || window < 0)
+    return fail(CTCPB_ERR_INVALID, "need 0 <= max_len <= 2^30 and window >= 0");
+  return CTCPB_OK;
+}
+
+template <typename T>
+void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  const unsigned blocks = (unsigned)((int64_t)a.rows * a.kv_heads * p.head_tiles * p.splits);
+  const dim3 block(64 * kAttnWaves);
+  if (a.D <= 64)
+    attn_kernel<T, 64><<<blocks, block, 0, st>>>(a);
+  else if (a.D <= 128)
+    attn_kernel<T, 128><<<blocks, block, 0, st>>>(a);
+  else
+    attn_kernel<T, 256><<<blocks, block, 0, st>>>(a);
+  if (p.splits > 1)
+    join_kernel<T><<<(unsigned)(a.rows * a.heads), 256, 0, st>>>(a, p.tile);
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* ctcpb_lm_last_error(void) { return g_err.c_str(); }
+
+int ctcpb_lm_cache_plan(const int32_t* lengths, const int32_t* counts, int32_t rows,
+                        int32_t* tables, int64_t table_stride, int32_t table_width,
+                        const int32_t* pool, int32_t pool_size, const int32_t* taken,
+                        int32_t page_size, int32_t* slots, int32_t* positions, int32_t capacity,
+                        int32_t* starts, int32_t* out_lengths, int32_t* out_taken,
+                        int32_t* status, void* stream) {
+  return guarded([&] {
+    if (int rc = check_table(rows, table_stride, table_width, page_size)) return rc;
+    if (pool_size < 0 || capacity < 0 || capacity > (1 << 30))
+      return fail(CTCPB_ERR_INVALID, "need pool_size >= 0 and 0 <= capacity <= 2^30");
+    if ((rows && (!lengths || !counts || !out_lengths || !status || (!tables && table_width))) ||
+        (!pool && pool_size) || !taken || (capacity && (!slots || !positions)) || !starts ||
+        !out_taken)
+      return fail(CTCPB_ERR_INVALID, kNull);
+    PlanArgs a{lengths, counts,    pool,        taken,     tables,     slots,
+               positions, starts,  out_lengths, out_taken, status,     table_stride,
+               rows,    table_width, pool_size, log2_of(page_size), capacity, 0};
+    const int threads = rows <= 256 ? 256 : kPlanThreads;
+    // a workgroup's part of the slot map: a few tokens per thread
+    a.per_block = 4 * threads;
+    const int blocks = capacity ? (capacity + a.per_block - 1) / a.per_block : 1;
+    plan_kernel<<<blocks, threads, 0, static_cast<hipStream_t>(stream)>>>(a);
+    return launched("plan_kernel");
+  });
+}
+
+int ctcpb_lm_cache_release(const uint8_t* finished, const int32_t* lengths, int32_t rows,
+                           const int32_t* tables, int64_t table_stride, int32_t table_width,
+                           int32_t* pool, int32_t pool_size, const int32_t* taken,
+                           int32_t page_size, int32_t* out_lengths, int32_t* out_taken,
+                           void* stream) {
+  return guarded([&] {
+    if (int rc = check_table(rows, table_stride, table_width, page_size)) return rc;
+    if (pool_size < 0) return fail(CTCPB_ERR_INVALID, "pool_size must be >= 0");
+    if ((rows && (!finished || !lengths || !out_lengths || (!tables && table_width))) ||
+        (!pool && pool_size) || !taken || !out_taken)
+      return fail(CTCPB_ERR_INVALID, kNull);
+    const ReleaseArgs a{finished, lengths,      tables, taken,       pool,      out_lengths,
+                        out_taken, table_stride, rows,   table_width, pool_size, log2_of(page_size)};
+    release_kernel<<<1, kPlanThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+    return launched("release_kernel");
+  });
+}
+
+int ctcpb_lm_cache_store(int32_t dtype, const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                         const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                         const int32_t* slots, int32_t tokens, const ctcpb_lm_cache* k_cache,
+                         const ctcpb_lm_cache* v_cache, int32_t num_pages, int32_t page_size,
+                         int32_t kv_heads, int32_t head_dim, void* stream) {
+  return guarded([&] {
+    const int es = elem_size(dtype);
+    if (!es) return fail(CTCPB_ERR_INVALID, kBadType);
+    if (int rc = check_pages(num_pages, page_size)) return rc;
+    if (tokens < 0 || kv_heads < 1 || head_dim < 1)
+      return fail(CTCPB_ERR_INVALID, "need tokens >= 0, kv_heads >= 1 and head_dim >= 1");
+    if ((int64_t)kv_heads * head_dim > INT_MAX)
+      return fail(CTCPB_ERR_INVALID, "kv_heads * head_dim must be below 2^31");
+    if (k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0)
+      return fail(CTCPB_ERR_INVALID, "strides must be >= 0");
+    if (int rc = check_cache(k_cache)) return rc;
+    if (int rc = check_cache(v_cache)) return rc;
+    if (tokens == 0) return ok();
+    if (!k || !v || !slots) return fail(CTCPB_ERR_INVALID, kNull);
+    StoreArgs a{};
+    a.k = static_cast<const char*>(k);
+    a.v = static_cast<const char*>(v);
+    a.k_t = k_stride_t * es;
+    a.k_h = k_stride_h * es;
+    a.v_t = v_stride_t * es;
+    a.v_h = v_stride_h * es;
+    a.slots = slots;
+    a.kc = view(k_cache, es);
+    a.vc = view(v_cache, es);
+    a.heads = kv_heads;
+    a.page_log = log2_of(page_size);
+    a.num_slots = num_pages * page_size;
+    const bool wide = head_dim * es % 16 == 0 && aligned(k, 16) && aligned(v, 16) &&
+                      a.k_t % 16 == 0 && a.k_h % 16 == 0 && a.v_t % 16 == 0 && a.v_h % 16 == 0 &&
+                      wide_cache(a.kc) && wide_cache(a.vc);
+    const int size = wide ? 16 : es;
+    a.per_head = head_dim * es / size;
+    a.pieces = (int64_t)tokens * kv_heads * a.per_head;
+    int64_t blocks = (a.pieces + 255) / 256;
+    if (blocks > 1 << 20) blocks = 1 << 20;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (wide)
+      store_kernel<u32x4><<<(unsigned)blocks, 256, 0, st>>>(a);
+    else if (es == 4)
+      store_kernel<uint32_t><<<(unsigned)blocks, 256, 0, st>>>(a);
+    else
+      store_kernel<uint16_t><<<(unsigned)blocks, 256, 0, st>>>(a);
+    return launched("store_kernel");
+  });
+}
+
+int ctcpb_lm_attention_workspace(int32_t dtype, int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int32_t max_len, int32_t window,
+                                 size_t* out_bytes) {
+  return guarded([&] {
+    if (int rc = check_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window))
+      return rc;
+    if (!out_bytes) return fail(CTCPB_ERR_INVALID, "out_bytes is NULL");
+    *out_bytes = plan_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window).bytes;
+    return ok();
+  });
+}
+
+int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t q_stride_h,
+                       const ctcpb_lm_cache* k_cache, const ctcpb_lm_cache* v_cache,
+                       int32_t num_pages, int32_t page_size, const int32_t* tables,
+                       int64_t table_stride, int32_t table_width, const int32_t* lengths,
+                       int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                       int32_t max_len, int32_t window, float scale, void* out,
+                       int64_t out_stride_r, int64_t out_stride_h, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    if (int rc = check_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window))
+      return rc;
+    if (int rc = check_pages(num_pages, page_size)) return rc;
+    if (int rc = check_table(rows, table_stride, table_width, page_size)) return rc;
+    if (q_stride_r < 0 || q_stride_h < 0 || out_stride_r < 0 || out_stride_h < 0)
+      return fail(CTCPB_ERR_INVALID, "strides must be >= 0");
+    if (int rc = check_cache(k_cache)) return rc;
+    if (int rc = check_cache(v_cache)) return rc;
+    const int es = elem_size(dtype);
+    AttnArgs a{};
+    a.kc = view(k_cache, es);
+    a.vc = view(v_cache, es);
+    if (!wide_cache(a.kc) || !wide_cache(a.vc))
+      return fail(CTCPB_ERR_INVALID,
+                  "caches must be 16-byte aligned, with strides that are multiples of 16 bytes");
+    if (rows == 0) return ok();
+    const int32_t held = table_width * page_size;
+    if (max_len == 0 || max_len > held) max_len = held;
+    if (!q || !out || !lengths || (!tables && max_len)) return fail(CTCPB_ERR_INVALID, kNull);
+    const AttnPlan p =
+        plan_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window);
+    if (p.bytes && (!workspace || !aligned(workspace, 16)))
+      return fail(CTCPB_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
+    if (workspace_bytes < p.bytes)
+      return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_attention_workspace");
+    if ((int64_t)rows * kv_heads * p.head_tiles * p.splits > INT_MAX ||
+        (int64_t)rows * q_heads > INT_MAX)
+      return fail(CTCPB_ERR_UNSUPPORTED, "too many rows for one launch");
+    a.q = static_cast<const char*>(q);
+    a.out = static_cast<char*>(out);
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.tables = tables;
+    a.lengths = lengths;
+    a.q_r = q_stride_r;
+    a.q_h = q_stride_h;
+    a.out_r = out_stride_r;
+    a.out_h = out_stride_h;
+    a.table_stride = table_stride;
+    a.rows = rows;
+    a.heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.group = q_heads / kv_heads;
+    a.head_tiles = p.head_tiles;
+    a.D = head_dim;
+    a.width = table_width;
+    a.page_log = log2_of(page_size);
+    a.num_pages = num_pages;
+    a.max_len = p.max_len;
+    a.window = window;
+    a.chunk = p.chunk;
+    a.splits = p.splits;
+    a.scale = scale;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (dtype == CTCPB_LM_BF16)
+      launch_attention<__bf16>(a, p, st);
+    else if (dtype == CTCPB_LM_F16)
+      launch_attention<_Float16>(a, p, st);
+    else
+      launch_attention<float>(a, p, st);
+    return launched("attn_kernel");
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,141 @@
+/*
+ * ctcpb_lm.h -- C ABI of libctcpb_lm.so: the operators a language model needs
+ * to rescore the decoder's N-best lists on AMD Instinct MI355X (gfx950).
+ *
+ *   cache_plan / cache_release   page tables and slot maps of a paged
+ *                                key/value cache, from device-resident lengths
+ *   cache_store                  new tokens' keys and values to their slots
+ *   attention                    one new token per request over the cache
+ *
+ * Conventions are those of ctcpb.h: device pointers are the caller's, the
+ * library allocates no device memory and keeps no state between calls, every
+ * call only enqueues work on `stream` (a hipStream_t, NULL = the default
+ * stream) and may be captured into a HIP graph.  The return value is CTCPB_OK
+ * or an error code (the values of ctcpb.h), described by
+ * ctcpb_lm_last_error().  On error nothing was enqueued, except
+ * CTCPB_ERR_DEVICE, reported when a launch fails.  Strides are in elements.
+ * Results do not depend on the order in which workgroups run: two calls on the
+ * same inputs give the same bits.
+ */
+#ifndef CTCPB_LM_H
+#define CTCPB_LM_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of the tensors documented "typed". */
+enum { CTCPB_LM_BF16 = 0, CTCPB_LM_F16 = 1, CTCPB_LM_F32 = 2 };
+
+/* Status bits of ctcpb_lm_cache_plan. */
+enum {
+  CTCPB_LM_NO_PAGE = 1,   /* the pool ran out before the row had its pages */
+  CTCPB_LM_NO_ENTRY = 2,  /* the row's table is full */
+  CTCPB_LM_NO_SLOT = 4    /* the slot map is full: the row's last tokens were left out */
+};
+
+/* Hand out pages for counts[r] new tokens of every request r that already
+ * holds lengths[r] tokens, and list the slots of the new tokens.
+ *   lengths, counts  device int32 [rows]; negative values count as 0, lengths
+ *                    are clamped to table_width * page_size
+ *   tables           device int32 [rows][table_width] with row stride
+ *                    table_stride: entry p of row r is the page of the row's
+ *                    tokens p*page_size ..; entries of pages the row holds are
+ *                    read, the entries of new pages are written (-1 where the
+ *                    pool has none left), the others are left alone
+ *   pool, taken      device int32 [pool_size] free page ids (distinct, >= 0)
+ *                    and int32 [1], how many of them are in use: pages are
+ *                    taken from pool[taken] on, in row order, then page order
+ *   page_size        a power of two in 4..256
+ *   slots, positions device int32 [capacity]: for the new tokens, rows in
+ *                    order, the slot (page * page_size + offset; -1 if the
+ *                    token has no page) and the position in its request;
+ *                    entries past the last token are -1
+ *   starts           device int32 [rows + 1]: row r's new tokens are
+ *                    slots[starts[r]] ..; a sum above 2^30 counts as 2^30.
+ *                    A row's tokens past `capacity` are not appended.
+ *   out_lengths      device int32 [rows]: tokens with a slot, old and new
+ *   out_taken        device int32 [1]
+ *   status           device int32 [rows]: CTCPB_LM_NO_* bits, 0 = complete
+ * slots, positions, starts, out_lengths, out_taken and status must not overlap
+ * the inputs, so a repeated call on the same inputs gives the same result.
+ * num_pages * page_size, with num_pages the largest page id + 1, must be below
+ * 2^31. */
+int ctcpb_lm_cache_plan(const int32_t* lengths, const int32_t* counts, int32_t rows,
+                        int32_t* tables, int64_t table_stride, int32_t table_width,
+                        const int32_t* pool, int32_t pool_size, const int32_t* taken,
+                        int32_t page_size, int32_t* slots, int32_t* positions, int32_t capacity,
+                        int32_t* starts, int32_t* out_lengths, int32_t* out_taken,
+                        int32_t* status, void* stream);
+
+/* Give back the pages of the rows with finished[r] != 0 (device uint8 [rows]):
+ * they go to pool[out_taken ..] in row order, then page order, and
+ * out_taken = taken - (their number).  out_lengths is 0 for these rows,
+ * lengths[r] for the others.  Other arguments as ctcpb_lm_cache_plan; out_*
+ * must not overlap the inputs. */
+int ctcpb_lm_cache_release(const uint8_t* finished, const int32_t* lengths, int32_t rows,
+                           const int32_t* tables, int64_t table_stride, int32_t table_width,
+                           int32_t* pool, int32_t pool_size, const int32_t* taken,
+                           int32_t page_size, int32_t* out_lengths, int32_t* out_taken,
+                           void* stream);
+
+/* A paged cache tensor: element (page, offset, head, d) at
+ * data[page*stride_page + offset*stride_token + head*stride_head + d].  The
+ * order of the axes in memory is free (token by token or head by head). */
+typedef struct {
+  void* data;            /* device, typed */
+  int64_t stride_page, stride_token, stride_head;
+} ctcpb_lm_cache;
+
+/* Write the keys and values of `tokens` tokens to their slots.
+ *   k, v     device, typed: element (t, head, d) at t*stride_t + head*stride_h + d
+ *   slots    device int32 [tokens]; tokens whose slot is outside
+ *            [0, num_pages*page_size) are left out.  Slots are distinct.
+ * 16-byte accesses are used where pointers and strides allow, else single
+ * elements. */
+int ctcpb_lm_cache_store(int32_t dtype, const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                         const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                         const int32_t* slots, int32_t tokens, const ctcpb_lm_cache* k_cache,
+                         const ctcpb_lm_cache* v_cache, int32_t num_pages, int32_t page_size,
+                         int32_t kv_heads, int32_t head_dim, void* stream);
+
+/* Attention of one token per request over its pages (the token's own key and
+ * value stored before).  With t over the last `window` of the request's
+ * lengths[r] tokens (window 0: all of them), kv = head / (q_heads / kv_heads):
+ *   s_t = scale * q[r, head] . k[t, kv]      m = max s_t     l = sum exp(s_t - m)
+ *   out[r, head] = sum exp(s_t - m) v[t, kv] / l        lse[r, head] = m + log l
+ * A row with no token, or with every s_t = -inf, gives zeros and lse = -inf.
+ * Slots past a row's length are never used, whatever they hold.
+ *   q, out   device, typed, element (r, head, d) at r*stride_r + head*stride_h + d
+ *   lse      device float32 [rows][q_heads], or NULL
+ *   tables   as ctcpb_lm_cache_plan leaves them; entries are clamped to the cache
+ *   lengths  device int32 [rows], clamped to [0, min(max_len, table_width*page_size)]
+ *   max_len  an upper bound of the lengths that the caller knows (it sizes the
+ *            launch), 0: table_width * page_size
+ *   head_dim a multiple of 8, at most 256; caches 16-byte aligned, with strides
+ *            that are multiples of 16 bytes
+ *   workspace  device, >= ctcpb_lm_attention_workspace bytes, 16-byte aligned;
+ *            its contents on entry do not matter; calls that share it must not
+ *            overlap.  */
+int ctcpb_lm_attention_workspace(int32_t dtype, int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int32_t max_len, int32_t window,
+                                 size_t* out_bytes);
+int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t q_stride_h,
+                       const ctcpb_lm_cache* k_cache, const ctcpb_lm_cache* v_cache,
+                       int32_t num_pages, int32_t page_size, const int32_t* tables,
+                       int64_t table_stride, int32_t table_width, const int32_t* lengths,
+                       int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                       int32_t max_len, int32_t window, float scale, void* out,
+                       int64_t out_stride_r, int64_t out_stride_h, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Human-readable description of the last error on this thread ("" if none). */
+const char* ctcpb_lm_last_error(void);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* CTCPB_LM_H */
