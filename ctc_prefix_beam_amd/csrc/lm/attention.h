@@ -47,14 +47,6 @@ struct AttnArgs {
   float scale;
 };
 
-// exp(x) for x <= 0: 2^(x log2 e) is off by |x| 2^-24, below what 16-bit outputs
-// show; f32 takes the library's exponential.
-template <typename T>
-__device__ inline float exp_of(float x) {
-  if constexpr (sizeof(T) == 4) return expf(x);
-  return exp_fast(x);
-}
-
 template <typename T>
 struct Elem;
 

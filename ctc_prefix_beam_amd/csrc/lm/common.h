@@ -20,6 +20,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ inline float neg_inf() { return -__builtin_huge_valf(); }
 __device__ inline float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// exp(x) for x <= 0: 2^(x log2 e) is off by |x| 2^-24, below what 16-bit outputs
+// show; f32 takes the library's exponential.
+template <typename T>
+__device__ inline float exp_of(float x) {
+  if constexpr (sizeof(T) == 4) return expf(x);
+  return exp_fast(x);
+}
+
 // Maximum / sum over the four lanes l, l^16, l^32, l^48.
 __device__ inline float max_over_groups(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));

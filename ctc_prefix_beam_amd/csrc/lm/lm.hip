@@ -5,10 +5,12 @@
 #include <climits>
 #include <exception>
 #include <string>
+#include <type_traits>
 
 #include "attention.h"
 #include "cache.h"
 #include "ctcpb.h"
+#include "loss.h"
 
 using namespace ctcpb_lm;
 
@@ -150,6 +152,158 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     attn_kernel<T, 256><<<blocks, block, 0, st>>>(a);
   if (p.splits > 1)
     join_kernel<T><<<(unsigned)(a.rows * a.heads), 256, 0, st>>>(a, p.tile);
+}
+
+// ------------------------------------------------------------------ loss --
+
+constexpr size_t kPieceBytes = (size_t)256 << 20;   // workspace for d at a time
+constexpr int kTile = 128;                          // tokens and vocabulary rows of a tile
+
+size_t up(size_t v, size_t n) { return (v + n - 1) / n * n; }
+
+// Sizes and workspace offsets of a loss or gradient call.
+struct LossPlan {
+  int es, padded;          // padded: hidden up to 16 bytes
+  bool pad_x, pad_w;       // rows to be copied to aligned ones
+  int32_t tiles_v, tiles_n;
+  int32_t piece, pieces;   // gradient: vocabulary rows at a time
+  size_t o_x, o_w, o_part, o_hit, o_d, o_sums, o_bias, o_scale, bytes;
+};
+
+bool row_aligned(const void* p, int64_t stride, int es) {
+  // within a tile, rows are addressed with 31 bits
+  return aligned(p, 16) && stride * es % 16 == 0 && stride * es <= (1 << 23);
+}
+
+LossPlan plan_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
+                   int32_t rows, int32_t vocab, int32_t hidden, bool grad) {
+  LossPlan p{};
+  p.es = elem_size(dtype);
+  p.padded = (int)up(hidden, 16 / p.es);
+  // a row is read up to its last 16 bytes
+  p.pad_x = p.padded != hidden || !row_aligned(x, stride_x, p.es);
+  p.pad_w = p.padded != hidden || !row_aligned(w, stride_w, p.es);
+  p.tiles_v = (vocab + kTile - 1) / kTile;
+  p.tiles_n = (rows + kTile - 1) / kTile;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = up(at + bytes, 256);
+    return o;
+  };
+  if (p.pad_x) p.o_x = take((size_t)rows * p.padded * p.es);
+  if (p.pad_w) p.o_w = take((size_t)vocab * p.padded * p.es);
+  if (!grad) {
+    p.o_part = take((size_t)p.tiles_v * rows * sizeof(float2));
+    p.o_hit = take((size_t)rows * sizeof(float));
+  } else {
+    const size_t most = kPieceBytes / ((size_t)(rows ? rows : 1) * p.es) / kTile * kTile;
+    const size_t all = up(vocab, kTile);
+    size_t piece = most < kTile ? kTile : most < all ? most : all;
+    p.pieces = (int32_t)((all + piece - 1) / piece);
+    p.piece = (int32_t)up((all + p.pieces - 1) / p.pieces, kTile);   // of about the same size
+    p.o_d = take((size_t)rows * p.piece * p.es);
+    if (p.pieces > 1) p.o_sums = take((size_t)rows * hidden * sizeof(float));
+    p.o_bias = take((size_t)p.tiles_n * 2 * vocab * sizeof(float));
+    p.o_scale = take(2 * sizeof(float));
+  }
+  p.bytes = at;
+  return p;
+}
+
+int check_loss(int32_t dtype, int64_t stride_x, int64_t stride_w, int32_t rows, int32_t vocab,
+               int32_t hidden) {
+  if (!elem_size(dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
+  if (rows < 0 || vocab < 1 || hidden < 1)
+    return fail(CTCPB_ERR_INVALID, "need rows >= 0, vocab >= 1 and hidden >= 1");
+  if (stride_x < hidden || stride_w < hidden)
+    return fail(CTCPB_ERR_INVALID, "stride_x and stride_w must be >= hidden");
+  if (hidden > 1 << 20 || vocab > 1 << 30 || rows > 1 << 30)
+    return fail(CTCPB_ERR_UNSUPPORTED, "hidden above 2^20, or vocab or rows above 2^30");
+  const int64_t tiles = ((int64_t)vocab + kTile - 1) / kTile * ((rows + kTile - 1) / kTile);
+  if (tiles > INT_MAX) return fail(CTCPB_ERR_UNSUPPORTED, "too many tiles for one launch");
+  return CTCPB_OK;
+}
+
+// x or w as the kernels read it: in place, or its copy with aligned rows.
+template <typename T>
+Operand aligned_rows(const void* data, int64_t stride, int32_t rows, int32_t hidden,
+                     const LossPlan& p, bool pad, char* copy, hipStream_t st) {
+  if (!pad)
+    return Operand{static_cast<const char*>(data), stride * (int)sizeof(T), rows};
+  typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type U;
+  const int64_t all = (int64_t)rows * p.padded;
+  if (all == 0) return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows};
+  const int64_t blocks = (all + 255) / 256 < 8192 ? (all + 255) / 256 : 8192;
+  pad_kernel<U><<<(unsigned)blocks, 256, 0, st>>>(static_cast<const U*>(data), stride,
+                                                  reinterpret_cast<U*>(copy), rows, hidden,
+                                                  p.padded);
+  return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows};
+}
+
+template <typename T, bool AKC, bool BKC, typename Epilogue>
+void launch_gemm(const Operand& a, const Operand& b, int32_t m, int32_t n, int32_t K,
+                 const Epilogue& ep, hipStream_t st) {
+  const GemmArgs g{a, b, K, (m + kTile - 1) / kTile, (n + kTile - 1) / kTile};
+  gemm_kernel<T, kTile, kTile, 2, 2, AKC, BKC, Epilogue>
+      <<<(unsigned)(g.tiles_m * g.tiles_n), 256, 0, st>>>(g, ep);
+}
+
+template <typename T>
+void run_loss(const LossPlan& p, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
+              const float* bias, const int32_t* targets, int32_t rows, int32_t vocab,
+              int32_t hidden, float* loss, float* lse, char* ws, hipStream_t st) {
+  const Operand ox = aligned_rows<T>(x, stride_x, rows, hidden, p, p.pad_x, ws + p.o_x, st);
+  const Operand ow = aligned_rows<T>(w, stride_w, vocab, hidden, p, p.pad_w, ws + p.o_w, st);
+  float2* part = reinterpret_cast<float2*>(ws + p.o_part);
+  float* hit = reinterpret_cast<float*>(ws + p.o_hit);
+  const ForwardEpilogue ep{Logits{bias, targets, rows, vocab, 0}, part, hit};
+  launch_gemm<T, true, true>(ow, ox, vocab, rows, p.padded, ep, st);
+  loss_join_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, st>>>(part, hit, targets, rows, vocab,
+                                                                  p.tiles_v, loss, lse);
+}
+
+template <typename T>
+void run_grad(const LossPlan& p, const float* grad, const void* x, int64_t stride_x, const void* w,
+              int64_t stride_w, const float* bias, const int32_t* targets, const float* lse,
+              int32_t rows, int32_t vocab, int32_t hidden, void* dx, void* dw, float* dbias,
+              char* ws, hipStream_t st) {
+  const Operand ox = aligned_rows<T>(x, stride_x, rows, hidden, p, p.pad_x, ws + p.o_x, st);
+  const Operand ow = aligned_rows<T>(w, stride_w, vocab, hidden, p, p.pad_w, ws + p.o_w, st);
+  T* d = reinterpret_cast<T*>(ws + p.o_d);
+  float* sums = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.o_sums) : nullptr;
+  float* part = dbias ? reinterpret_cast<float*>(ws + p.o_bias) : nullptr;
+  float* scale = nullptr;
+  if (sizeof(T) == 2 && std::is_same<T, _Float16>::value) {
+    scale = reinterpret_cast<float*>(ws + p.o_scale);
+    scale_kernel<<<1, 1024, 0, st>>>(grad, targets, rows, vocab, scale);
+  }
+  const int64_t ldd = (int64_t)p.piece * (int)sizeof(T);
+  for (int32_t k = 0; k < p.pieces; ++k) {
+    const int32_t v0 = k * p.piece;
+    const int32_t nv = vocab - v0 < p.piece ? vocab - v0 : p.piece;
+    const Operand wp{ow.data + v0 * ow.ld, ow.ld, nv};
+    const GradEpilogue<T> ge{Logits{bias, targets, rows, vocab, v0}, grad, lse, scale, d, p.piece,
+                             part};
+    if (rows) launch_gemm<T, true, true>(wp, ox, nv, rows, p.padded, ge, st);
+    if (dx && rows) {
+      // out[token, h]: m = h, n = token, k = vocabulary
+      const Operand a{wp.data, wp.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, rows};
+      const OutEpilogue<T> oe{static_cast<T*>(dx), sums, scale, hidden, rows, k == 0,
+                              k == p.pieces - 1};
+      launch_gemm<T, false, true>(a, b, hidden, rows, nv, oe, st);
+    }
+    if (dw) {
+      // out[v, h]: m = h, n = v, k = token
+      const Operand a{ox.data, ox.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, nv};
+      const OutEpilogue<T> oe{static_cast<T*>(dw) + (int64_t)v0 * hidden, nullptr, scale, hidden,
+                              nv, true, true};
+      launch_gemm<T, false, false>(a, b, hidden, nv, rows, oe, st);
+    }
+  }
+  if (dbias)
+    dbias_kernel<<<(unsigned)((vocab + 255) / 256), 256, 0, st>>>(part, p.tiles_n * 2, vocab,
+                                                                  dbias);
 }
 
 }  // namespace
@@ -335,6 +489,74 @@ int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t
     else
       launch_attention<float>(a, p, st);
     return launched("attn_kernel");
+  });
+}
+
+int ctcpb_lm_loss_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
+                            int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
+                            size_t* out_bytes) {
+  return guarded([&] {
+    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
+    if (!out_bytes) return fail(CTCPB_ERR_INVALID, "out_bytes is NULL");
+    *out_bytes = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, false).bytes;
+    return ok();
+  });
+}
+
+int ctcpb_lm_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
+                  const float* bias, const int32_t* targets, int32_t rows, int32_t vocab,
+                  int32_t hidden, float* loss, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
+    if (rows == 0) return ok();
+    if (!x || !w || !targets || !loss || !lse || !workspace) return fail(CTCPB_ERR_INVALID, kNull);
+    if (!aligned(workspace, 256))
+      return fail(CTCPB_ERR_INVALID, "workspace must be 256-byte aligned");
+    const LossPlan p = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, false);
+    if (workspace_bytes < p.bytes)
+      return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_loss_workspace");
+    const auto f = dtype == CTCPB_LM_BF16  ? run_loss<__bf16>
+                   : dtype == CTCPB_LM_F16 ? run_loss<_Float16>
+                                           : run_loss<float>;
+    f(p, x, stride_x, w, stride_w, bias, targets, rows, vocab, hidden, loss, lse,
+      static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+    return launched("loss kernels");
+  });
+}
+
+int ctcpb_lm_loss_grad_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
+                                 int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
+                                 size_t* out_bytes) {
+  return guarded([&] {
+    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
+    if (!out_bytes) return fail(CTCPB_ERR_INVALID, "out_bytes is NULL");
+    *out_bytes = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, true).bytes;
+    return ok();
+  });
+}
+
+int ctcpb_lm_loss_grad(int32_t dtype, const float* grad, const void* x, int64_t stride_x,
+                       const void* w, int64_t stride_w, const float* bias,
+                       const int32_t* targets, const float* lse, int32_t rows, int32_t vocab,
+                       int32_t hidden, void* dx, void* dw, float* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
+    if (!dx && !dw && !dbias) return ok();
+    if (!w || !workspace || (rows && (!grad || !x || !targets || !lse)))
+      return fail(CTCPB_ERR_INVALID, kNull);
+    if (!aligned(workspace, 256) || (dx && !aligned(dx, 16)) || (dw && !aligned(dw, 16)))
+      return fail(CTCPB_ERR_INVALID, "workspace must be 256-byte aligned, dx and dw 16-byte");
+    const LossPlan p = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, true);
+    if (workspace_bytes < p.bytes)
+      return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_loss_grad_workspace");
+    const auto f = dtype == CTCPB_LM_BF16  ? run_grad<__bf16>
+                   : dtype == CTCPB_LM_F16 ? run_grad<_Float16>
+                                           : run_grad<float>;
+    f(p, grad, x, stride_x, w, stride_w, bias, targets, lse, rows, vocab, hidden, dx, dw, dbias,
+      static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+    return launched("loss gradient kernels");
   });
 }
 

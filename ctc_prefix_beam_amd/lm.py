@@ -3,8 +3,10 @@
 Thin Python binding of ``libctcpb_lm.so`` (C ABI in ``include/ctcpb_lm.h``):
 the pages and slots of a paged key/value cache from device-resident lengths
 (``cache_plan``, ``cache_release``), the store of new tokens' keys and values
-(``cache_store``) and the attention of one new token per request over the cache
-(``attention``).  ``PagedCache`` holds the tensors these work on.  Every step
+(``cache_store``), the attention of one new token per request over the cache
+(``attention``), and token losses over a large vocabulary without keeping the
+logits, with their gradients (``token_loss``).  ``PagedCache`` holds the tensors
+of a cache.  Every step
 runs in the library's HIP kernels; PyTorch provides device memory and the
 current stream.  If the library is missing the calls raise; there is no CPU
 fallback.
@@ -24,7 +26,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libctcpb_lm.so")
 
 EXPORTS = ("ctcpb_lm_cache_plan", "ctcpb_lm_cache_release", "ctcpb_lm_cache_store",
-           "ctcpb_lm_attention_workspace", "ctcpb_lm_attention", "ctcpb_lm_last_error")
+           "ctcpb_lm_attention_workspace", "ctcpb_lm_attention", "ctcpb_lm_loss_workspace",
+           "ctcpb_lm_loss", "ctcpb_lm_loss_grad_workspace", "ctcpb_lm_loss_grad",
+           "ctcpb_lm_last_error")
 NO_PAGE, NO_ENTRY, NO_SLOT = 1, 2, 4   # status bits of cache_plan
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -55,6 +59,11 @@ def lib():
         L.ctcpb_lm_attention.argtypes = [i32, p, i64, i64, cachep, cachep, i32, i32, p, i64, i32,
                                          p, i32, i32, i32, i32, i32, i32, f32, p, i64, i64, p, p,
                                          sz, p]
+        L.ctcpb_lm_loss_workspace.argtypes = [i32, p, i64, p, i64, i32, i32, i32, szp]
+        L.ctcpb_lm_loss.argtypes = [i32, p, i64, p, i64, p, p, i32, i32, i32, p, p, p, sz, p]
+        L.ctcpb_lm_loss_grad_workspace.argtypes = [i32, p, i64, p, i64, i32, i32, i32, szp]
+        L.ctcpb_lm_loss_grad.argtypes = [i32, p, p, i64, p, i64, p, p, p, i32, i32, i32, p, p, p,
+                                         p, sz, p]
         for name in EXPORTS[:-1]:   # all but the string getter
             getattr(L, name).restype = ctypes.c_int
         L.ctcpb_lm_last_error.restype = ctypes.c_char_p
@@ -258,6 +267,92 @@ def attention(q, k_cache, v_cache, tables, lengths, scale: float | None = None, 
         window, scale, out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(),
         ws.data_ptr() if ws is not None else None, need.value, on.ptr))
     return out, lse
+
+
+def _loss_args(x, w, targets, bias):
+    dev = _gpu(x, "x")
+    dt = _type(x, "x")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be (rows, hidden) with unit stride over hidden")
+    N, H = x.shape
+    _check_dev(w, dev, "w", x.dtype)
+    if w.dim() != 2 or w.shape[1] != H or (H > 1 and w.stride(1) != 1):
+        raise ValueError(f"w must be (vocab, {H}) with unit stride over hidden")
+    V = w.shape[0]
+    _i32(targets, dev, "targets", (N,))
+    if bias is not None:
+        _check_dev(bias, dev, "bias", torch.float32, (V,), contiguous=True)
+    # a single row's stride is of no account, and may be anything
+    sx = x.stride(0) if N > 1 else H
+    sw = w.stride(0) if V > 1 else H
+    return dev, dt, N, V, H, sx, sw
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def token_loss_forward(x, w, targets, bias=None, stream=None):
+    """(loss, lse), both (rows,) float32, of an output layer: x (rows, hidden), w
+    (vocab, hidden) of one type, bias float32 (vocab,) or None, targets int32
+    (rows,).  loss = lse - logit of the target, 0 where the target is outside
+    the vocabulary (the decoder's -1 padding)."""
+    dev, dt, N, V, H, sx, sw = _loss_args(x, w, targets, bias)
+    L = lib()
+    need = ctypes.c_size_t()
+    _check(L.ctcpb_lm_loss_workspace(dt, x.data_ptr(), sx, w.data_ptr(), sw, N, V, H,
+                                     ctypes.byref(need)))
+    on = _On(stream, dev)
+    out = on.empty((2, N), torch.float32)
+    ws = on.empty((need.value,), torch.uint8)
+    _check(L.ctcpb_lm_loss(dt, x.data_ptr(), sx, w.data_ptr(), sw, _ptr(bias), targets.data_ptr(),
+                           N, V, H, out.data_ptr(), out.data_ptr() + 4 * N, ws.data_ptr(),
+                           need.value, on.ptr))
+    return out[0], out[1]
+
+
+def token_loss_backward(grad, x, w, targets, lse, bias=None, need=(True, True, True), stream=None):
+    """Gradients (dx, dw, dbias) of sum(grad * loss) for ``token_loss_forward``
+    with its lse; grad (rows,) float32.  dx and dw have x's and w's type, dbias
+    is float32 (None without a bias).  `need` says which of them to compute."""
+    dev, dt, N, V, H, sx, sw = _loss_args(x, w, targets, bias)
+    _check_dev(grad, dev, "grad", torch.float32, (N,), contiguous=True)
+    _check_dev(lse, dev, "lse", torch.float32, (N,), contiguous=True)
+    L = lib()
+    size = ctypes.c_size_t()
+    _check(L.ctcpb_lm_loss_grad_workspace(dt, x.data_ptr(), sx, w.data_ptr(), sw, N, V, H,
+                                          ctypes.byref(size)))
+    on = _On(stream, dev)
+    dx = on.empty((N, H), x.dtype) if need[0] else None
+    dw = on.empty((V, H), w.dtype) if need[1] else None
+    db = on.empty((V,), torch.float32) if need[2] and bias is not None else None
+    ws = on.empty((size.value,), torch.uint8)
+    _check(L.ctcpb_lm_loss_grad(dt, grad.data_ptr(), x.data_ptr(), sx, w.data_ptr(), sw,
+                                _ptr(bias), targets.data_ptr(), lse.data_ptr(), N, V, H, _ptr(dx),
+                                _ptr(dw), _ptr(db), ws.data_ptr(), size.value, on.ptr))
+    return dx, dw, db
+
+
+class _TokenLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, targets, bias):
+        loss, lse = token_loss_forward(x, w, targets, bias)
+        ctx.save_for_backward(x, w, targets, bias, lse)
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, w, targets, bias, lse = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = token_loss_backward(grad.contiguous(), x, w, targets, lse, bias,
+                                         (need[0], need[1], need[3]))
+        return dx, dw, None, db
+
+
+def token_loss(x, w, targets, bias=None):
+    """The losses of ``token_loss_forward`` as a torch function: gradients flow
+    to x, w and bias."""
+    return _TokenLoss.apply(x, w, targets, bias)
 
 
 class PagedCache:

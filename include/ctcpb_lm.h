@@ -6,6 +6,8 @@
  *                                key/value cache, from device-resident lengths
  *   cache_store                  new tokens' keys and values to their slots
  *   attention                    one new token per request over the cache
+ *   loss / loss_grad             token losses over a large vocabulary without
+ *                                keeping the logits, and their gradients
  *
  * Conventions are those of ctcpb.h: device pointers are the caller's, the
  * library allocates no device memory and keeps no state between calls, every
@@ -130,6 +132,47 @@ int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t
                        int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                        int32_t max_len, int32_t window, float scale, void* out,
                        int64_t out_stride_r, int64_t out_stride_h, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Token losses of an output layer, the vocabulary taken in pieces:
+ *   logit[n, v] = x[n] . w[v] + bias[v]     lse[n] = log sum_v exp(logit[n, v])
+ *   loss[n] = lse[n] - logit[n, targets[n]]
+ * A target outside [0, vocab) (the decoder's -1 padding) gives loss 0.
+ *   x, w     device, typed, row strides stride_x / stride_w >= hidden, unit
+ *            stride over `hidden`
+ *   bias     device float32 [vocab], or NULL
+ *   targets  device int32 [rows];  loss, lse: device float32 [rows]
+ * Products of 16-bit types are summed in float32; float32 inputs are
+ * multiplied in float32.  workspace: device, 256-byte aligned, contents on
+ * entry do not matter; calls that share it must not overlap.  Its size depends
+ * on the addresses and strides of x and w (rows that are not 16-byte aligned
+ * are copied to aligned ones there); the size query does not read them. */
+int ctcpb_lm_loss_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
+                            int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
+                            size_t* out_bytes);
+int ctcpb_lm_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
+                  const float* bias, const int32_t* targets, int32_t rows, int32_t vocab,
+                  int32_t hidden, float* loss, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_n grad[n] * loss[n], recomputing the probabilities piece by
+ * piece from lse:
+ *   d[n, v] = grad[n] * (exp(logit[n, v] - lse[n]) - (v == targets[n]))
+ *   dx = d w     dw = d^T x     dbias[v] = sum_n d[n, v]
+ * Rows without a target have no part in any of them.
+ *   grad     device float32 [rows];  lse: as ctcpb_lm_loss left it
+ *   dx       device, typed [rows][hidden], contiguous;  dw: device, typed
+ *            [vocab][hidden], contiguous;  dbias: device float32 [vocab].  Any
+ *            of them may be NULL and is then not computed.
+ * With 16-bit types d is rounded to that type before the products (for f16
+ * after a power-of-two scaling that keeps it in range); sums are float32. */
+int ctcpb_lm_loss_grad_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
+                                 int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
+                                 size_t* out_bytes);
+int ctcpb_lm_loss_grad(int32_t dtype, const float* grad, const void* x, int64_t stride_x,
+                       const void* w, int64_t stride_w, const float* bias,
+                       const int32_t* targets, const float* lse, int32_t rows, int32_t vocab,
+                       int32_t hidden, void* dx, void* dw, float* dbias, void* workspace,
                        size_t workspace_bytes, void* stream);
 
 /* Human-readable description of the last error on this thread ("" if none). */

@@ -97,3 +97,43 @@ def attention(q, k_cache, v_cache, tables, lengths, scale, window, page):
             tol_l[r, h] = e + 2.0 ** -22 * (1 + abs(float(lse[r, h])))
             tol_o[r, h] = (e + 2.0 ** -16) * float(vv.abs().max()) + u * out[r, h].abs() + tiny
     return out, lse, tol_o, tol_l
+
+
+def loss(x, w, targets, bias, grad):
+    """(loss, lse, dx, dw, dbias) in float64 on the CPU, and tolerances.
+
+    A logit of H float32 products is off by at most e = (H + 4) 2^-24 of the sum
+    of their magnitudes; loss and lse by 2e and their own rounding.  A
+    probability is off by a factor 1 + 2e + 2^-17 (its exponential), d also by
+    its rounding to the inputs' type (u), and the sums over n terms by n 2^-24:
+    dx is off by at most |d| |w| times that, plus its own rounding; dw and dbias
+    alike.  Numbers below 2^-126, the smallest normal float32 and bfloat16, may
+    come out as zero."""
+    u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}[x.dtype]
+    tiny = 2.0 ** -25 if x.dtype == torch.float16 else 2.0 ** -126
+    X, W, t = x.cpu().double(), w.cpu().double(), targets.cpu().long()
+    b = torch.zeros(W.shape[0], dtype=torch.float64) if bias is None else bias.cpu().double()
+    N, H = X.shape
+    V = W.shape[0]
+    z = X @ W.t() + b
+    e = (H + 4) * 2.0 ** -24 * (X.abs() @ W.abs().t() + b.abs()).amax(1)
+    lse = torch.logsumexp(z, 1)
+    ok = (t >= 0) & (t < V)
+    at = torch.where(ok, t, 0)
+    nll = torch.where(ok, lse - z[torch.arange(N), at], 0.0)
+    tol_lse = e + 2.0 ** -21 * (1 + lse.abs())
+    tol_loss = 2 * e + 2.0 ** -20 * (1 + lse.abs())
+    g = torch.where(ok, grad.cpu().double(), 0.0)
+    p = torch.exp(z - lse[:, None])
+    hot = torch.zeros_like(p)
+    hot[torch.arange(N)[ok], at[ok]] = 1
+    d = g[:, None] * (p - hot)
+    # the error of d: of the probability, and of rounding d to the type
+    r = 2 * e + 2.0 ** -17
+    de = g.abs()[:, None] * p * r[:, None] + u * d.abs()
+    de += (2.0 ** -36 if x.dtype == torch.float16 else 2.0 ** -126) * g.abs().max()
+    dx, dw, db = d @ W, d.t() @ X, d.sum(0)
+    tol_dx = (de + V * 2.0 ** -24 * d.abs()) @ W.abs() + u * dx.abs() + tiny
+    tol_dw = (de + N * 2.0 ** -24 * d.abs()).t() @ X.abs() + u * dw.abs() + tiny
+    tol_db = (g.abs()[:, None] * p * r[:, None] + (N + 4) * 2.0 ** -24 * d.abs()).sum(0)
+    return (nll, lse, dx, dw, db), (tol_loss, tol_lse, tol_dx, tol_dw, tol_db)

@@ -106,3 +106,53 @@ def test_attention_workspace(L):
     assert ws(1, 32, 8, 128, 131072, window=64)[1] < one   # a window bounds the length
     assert ws(1, 3, 2, 64, 100)[0] == 1
     assert attend(L, rows=0, q=N, out=N, lengths=N, tables=N) == 0
+
+
+def loss(L, dtype=0, x=P, sx=64, w=P, sw=64, targets=P, rows=3, V=100, H=64, out=P, lse=P, ws=P,
+         ws_bytes=1 << 40):
+    return L.ctcpb_lm_loss(dtype, x, sx, w, sw, N, targets, rows, V, H, out, lse, ws, ws_bytes, N)
+
+
+def grad(L, dtype=0, g=P, x=P, sx=64, w=P, sw=64, targets=P, lse=P, rows=3, V=100, H=64, dx=P, dw=P,
+         ws=P, ws_bytes=1 << 40):
+    return L.ctcpb_lm_loss_grad(dtype, g, x, sx, w, sw, N, targets, lse, rows, V, H, dx, dw, N, ws,
+                                ws_bytes, N)
+
+
+SIZES = [(dict(dtype=9), 1), (dict(rows=-1), 1), (dict(V=0), 1), (dict(H=0), 1), (dict(sx=63), 1),
+         (dict(sw=63), 1), (dict(H=(1 << 20) + 8, sx=1 << 21, sw=1 << 21), 3),
+         (dict(rows=1 << 30, V=1 << 30), 3), (dict(x=N), 1), (dict(w=N), 1), (dict(targets=N), 1),
+         (dict(lse=N), 1), (dict(ws=N), 1), (dict(ws=ctypes.c_void_p(264)), 1),
+         (dict(ws_bytes=8), 2)]
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [(dict(out=N), 1)])
+def test_loss_refusals(L, kw, code):
+    assert loss(L, **kw) == code
+    assert L.ctcpb_lm_last_error().decode() != ""
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [(dict(g=N), 1), (dict(dx=ctypes.c_void_p(8)), 1),
+                                             (dict(dw=ctypes.c_void_p(8)), 1)])
+def test_loss_grad_refusals(L, kw, code):
+    assert grad(L, **kw) == code
+    assert L.ctcpb_lm_last_error().decode() != ""
+
+
+def test_loss_workspaces(L):
+    def size(f, x=256, sx=64, H=64, rows=1000, V=5000, dtype=0):
+        out = ctypes.c_size_t(3)
+        rc = f(dtype, x, sx, 256, max(H, 64), rows, V, H, ctypes.byref(out))
+        assert rc == 0
+        return out.value
+    for f in (L.ctcpb_lm_loss_workspace, L.ctcpb_lm_loss_grad_workspace):
+        one = size(f)
+        assert one > 0 and one % 256 == 0
+        # rows that are not 16-byte aligned are copied: x of 1000 x 64 16-bit values
+        assert size(f, x=258) == size(f, sx=65) == one + 128000
+        assert f(0, 256, 64, 256, 64, 3, 9, 64, None) == 1
+    # the gradient's workspace holds a piece of the vocabulary, not all of it
+    many = size(L.ctcpb_lm_loss_grad_workspace, rows=100000, V=50000)
+    assert many < 100000 * 50000 * 2 / 4
+    assert loss(L, rows=0, x=N, w=N, targets=N, out=N, lse=N, ws=N) == 0
+    assert grad(L, dx=N, dw=N, x=N, w=N) == 0
