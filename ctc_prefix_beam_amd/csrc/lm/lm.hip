@@ -63,6 +63,7 @@ int elem_size(int32_t dtype) {
 constexpr const char* kBadPage = "page_size must be a power of two in 4..256";
 constexpr const char* kBadType = "dtype must be CTCPB_LM_BF16, CTCPB_LM_F16 or CTCPB_LM_F32";
 constexpr const char* kNull = "a required pointer is NULL";
+constexpr const char* kNoArgs = "args is NULL";
 
 int check_table(int32_t rows, int64_t stride, int32_t width, int32_t page_size) {
   if (rows < 0 || width < 0) return fail(CTCPB_ERR_INVALID, "rows and table_width must be >= 0");
@@ -80,16 +81,16 @@ int check_pages(int32_t num_pages, int32_t page_size) {
   return CTCPB_OK;
 }
 
-int check_cache(const ctcpb_lm_cache* c) {
-  if (!c || !c->data) return fail(CTCPB_ERR_INVALID, kNull);
-  if (c->stride_page < 0 || c->stride_token < 0 || c->stride_head < 0)
+int check_cache(const ctcpb_lm_cache& c) {
+  if (!c.data) return fail(CTCPB_ERR_INVALID, kNull);
+  if (c.stride_page < 0 || c.stride_token < 0 || c.stride_head < 0)
     return fail(CTCPB_ERR_INVALID, "cache strides must be >= 0");
   return CTCPB_OK;
 }
 
-CacheView view(const ctcpb_lm_cache* c, int es) {
-  return CacheView{static_cast<char*>(c->data), c->stride_page * es, c->stride_token * es,
-                   c->stride_head * es};
+CacheView view(const ctcpb_lm_cache& c, int es) {
+  return CacheView{static_cast<char*>(c.data), c.stride_page * es, c.stride_token * es,
+                   c.stride_head * es};
 }
 
 bool wide_cache(const CacheView& v) {
@@ -105,10 +106,16 @@ struct AttnPlan {
   size_t bytes;
 };
 
-AttnPlan plan_attention(int32_t dtype, int32_t rows, int32_t heads, int32_t kv_heads, int32_t D,
-                        int32_t max_len, int32_t window) {
+int32_t length_bound(const ctcpb_lm_attention_args& g) {
+  const int32_t held = g.table_width * g.page_size;
+  return g.max_len == 0 || g.max_len > held ? held : g.max_len;
+}
+
+AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
+  const int32_t rows = g.rows, heads = g.q_heads, kv_heads = g.kv_heads, window = g.window;
+  const int32_t max_len = length_bound(g);
   AttnPlan p;
-  p.tile = dtype == CTCPB_LM_F32 ? 16 : 32;
+  p.tile = g.dtype == CTCPB_LM_F32 ? 16 : 32;
   p.head_tiles = (heads / kv_heads + 15) / 16;
   p.max_len = max_len;
   // tokens a row can have in its range (a window starts at a tile's edge)
@@ -123,21 +130,20 @@ AttnPlan plan_attention(int32_t dtype, int32_t rows, int32_t heads, int32_t kv_h
   p.chunk = (int32_t)(chunk < INT_MAX / 2 ? chunk : INT_MAX / 2);
   p.splits = (int32_t)((span + p.chunk - 1) / p.chunk);
   if (p.splits < 1) p.splits = 1;
-  p.bytes = p.splits > 1 ? (size_t)rows * heads * p.splits * (D + 2) * sizeof(float) : 0;
+  p.bytes = p.splits > 1 ? (size_t)rows * heads * p.splits * (g.head_dim + 2) * sizeof(float) : 0;
   return p;
 }
 
-int check_attention(int32_t dtype, int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t D,
-                    int32_t max_len, int32_t window) {
-  if (!elem_size(dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
-  if (rows < 0) return fail(CTCPB_ERR_INVALID, "rows must be >= 0");
-  if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads)
+int check_attention(const ctcpb_lm_attention_args& g) {
+  if (!elem_size(g.dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
+  if (g.kv_heads < 1 || g.q_heads < g.kv_heads || g.q_heads % g.kv_heads)
     return fail(CTCPB_ERR_INVALID, "q_heads must be a multiple of kv_heads >= 1");
-  if (D < 8 || D % 8) return fail(CTCPB_ERR_INVALID, "head_dim must be a multiple of 8");
-  if (D > 256) return fail(CTCPB_ERR_UNSUPPORTED, "head_dim above 256");
-  if (max_len < 0 || max_len > (1 << 30) || window < 0)
-    return fail(CTCPB_ERR_INVALID, "need 0 <= max_len <= 2^30 and window >= 0");
-  return CTCPB_OK;
+  if (g.head_dim < 8 || g.head_dim % 8)
+    return fail(CTCPB_ERR_INVALID, "head_dim must be a multiple of 8");
+  if (g.head_dim > 256) return fail(CTCPB_ERR_UNSUPPORTED, "head_dim above 256");
+  if (g.max_len < 0 || g.window < 0)
+    return fail(CTCPB_ERR_INVALID, "max_len and window must be >= 0");
+  return check_table(g.rows, g.table_stride, g.table_width, g.page_size);
 }
 
 template <typename T>
@@ -175,14 +181,15 @@ bool row_aligned(const void* p, int64_t stride, int es) {
   return aligned(p, 16) && stride * es % 16 == 0 && stride * es <= (1 << 23);
 }
 
-LossPlan plan_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
-                   int32_t rows, int32_t vocab, int32_t hidden, bool grad) {
+template <typename Args>
+LossPlan plan_loss(const Args& g, bool grad) {
+  const int32_t rows = g.rows, vocab = g.vocab, hidden = g.hidden;
   LossPlan p{};
-  p.es = elem_size(dtype);
+  p.es = elem_size(g.dtype);
   p.padded = (int)up(hidden, 16 / p.es);
   // a row is read up to its last 16 bytes
-  p.pad_x = p.padded != hidden || !row_aligned(x, stride_x, p.es);
-  p.pad_w = p.padded != hidden || !row_aligned(w, stride_w, p.es);
+  p.pad_x = p.padded != hidden || !row_aligned(g.x, g.stride_x, p.es);
+  p.pad_w = p.padded != hidden || !row_aligned(g.w, g.stride_w, p.es);
   p.tiles_v = (vocab + kTile - 1) / kTile;
   p.tiles_n = (rows + kTile - 1) / kTile;
   size_t at = 0;
@@ -202,6 +209,7 @@ LossPlan plan_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w
     size_t piece = most < kTile ? kTile : most < all ? most : all;
     p.pieces = (int32_t)((all + piece - 1) / piece);
     p.piece = (int32_t)up((all + p.pieces - 1) / p.pieces, kTile);   // of about the same size
+    p.pieces = (int32_t)((all + p.piece - 1) / p.piece);             // none empty
     p.o_d = take((size_t)rows * p.piece * p.es);
     if (p.pieces > 1) p.o_sums = take((size_t)rows * hidden * sizeof(float));
     p.o_bias = take((size_t)p.tiles_n * 2 * vocab * sizeof(float));
@@ -211,16 +219,16 @@ LossPlan plan_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w
   return p;
 }
 
-int check_loss(int32_t dtype, int64_t stride_x, int64_t stride_w, int32_t rows, int32_t vocab,
-               int32_t hidden) {
-  if (!elem_size(dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
-  if (rows < 0 || vocab < 1 || hidden < 1)
+template <typename Args>
+int check_loss(const Args& g) {
+  if (!elem_size(g.dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
+  if (g.rows < 0 || g.vocab < 1 || g.hidden < 1)
     return fail(CTCPB_ERR_INVALID, "need rows >= 0, vocab >= 1 and hidden >= 1");
-  if (stride_x < hidden || stride_w < hidden)
+  if (g.stride_x < g.hidden || g.stride_w < g.hidden)
     return fail(CTCPB_ERR_INVALID, "stride_x and stride_w must be >= hidden");
-  if (hidden > 1 << 20 || vocab > 1 << 30 || rows > 1 << 30)
+  if (g.hidden > 1 << 20 || g.vocab > 1 << 30 || g.rows > 1 << 30)
     return fail(CTCPB_ERR_UNSUPPORTED, "hidden above 2^20, or vocab or rows above 2^30");
-  const int64_t tiles = ((int64_t)vocab + kTile - 1) / kTile * ((rows + kTile - 1) / kTile);
+  const int64_t tiles = ((int64_t)g.vocab + kTile - 1) / kTile * ((g.rows + kTile - 1) / kTile);
   if (tiles > INT_MAX) return fail(CTCPB_ERR_UNSUPPORTED, "too many tiles for one launch");
   return CTCPB_OK;
 }
@@ -250,60 +258,59 @@ void launch_gemm(const Operand& a, const Operand& b, int32_t m, int32_t n, int32
 }
 
 template <typename T>
-void run_loss(const LossPlan& p, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
-              const float* bias, const int32_t* targets, int32_t rows, int32_t vocab,
-              int32_t hidden, float* loss, float* lse, char* ws, hipStream_t st) {
-  const Operand ox = aligned_rows<T>(x, stride_x, rows, hidden, p, p.pad_x, ws + p.o_x, st);
-  const Operand ow = aligned_rows<T>(w, stride_w, vocab, hidden, p, p.pad_w, ws + p.o_w, st);
+void run_loss(const LossPlan& p, const ctcpb_lm_loss_args& g, char* ws, hipStream_t st) {
+  const Operand x =
+      aligned_rows<T>(g.x, g.stride_x, g.rows, g.hidden, p, p.pad_x, ws + p.o_x, st);
+  const Operand w =
+      aligned_rows<T>(g.w, g.stride_w, g.vocab, g.hidden, p, p.pad_w, ws + p.o_w, st);
   float2* part = reinterpret_cast<float2*>(ws + p.o_part);
   float* hit = reinterpret_cast<float*>(ws + p.o_hit);
-  const ForwardEpilogue ep{Logits{bias, targets, rows, vocab, 0}, part, hit};
-  launch_gemm<T, true, true>(ow, ox, vocab, rows, p.padded, ep, st);
-  loss_join_kernel<<<(unsigned)((rows + 31) / 32), 256, 0, st>>>(part, hit, targets, rows, vocab,
-                                                                  p.tiles_v, loss, lse);
+  const ForwardEpilogue ep{Logits{g.bias, g.targets, g.rows, g.vocab, 0}, part, hit};
+  launch_gemm<T, true, true>(w, x, g.vocab, g.rows, p.padded, ep, st);
+  loss_join_kernel<<<(unsigned)((g.rows + 31) / 32), 256, 0, st>>>(
+      part, hit, g.targets, g.rows, g.vocab, p.tiles_v, g.loss, g.lse);
 }
 
 template <typename T>
-void run_grad(const LossPlan& p, const float* grad, const void* x, int64_t stride_x, const void* w,
-              int64_t stride_w, const float* bias, const int32_t* targets, const float* lse,
-              int32_t rows, int32_t vocab, int32_t hidden, void* dx, void* dw, float* dbias,
-              char* ws, hipStream_t st) {
-  const Operand ox = aligned_rows<T>(x, stride_x, rows, hidden, p, p.pad_x, ws + p.o_x, st);
-  const Operand ow = aligned_rows<T>(w, stride_w, vocab, hidden, p, p.pad_w, ws + p.o_w, st);
+void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStream_t st) {
+  const Operand x =
+      aligned_rows<T>(g.x, g.stride_x, g.rows, g.hidden, p, p.pad_x, ws + p.o_x, st);
+  const Operand w =
+      aligned_rows<T>(g.w, g.stride_w, g.vocab, g.hidden, p, p.pad_w, ws + p.o_w, st);
   T* d = reinterpret_cast<T*>(ws + p.o_d);
   float* sums = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.o_sums) : nullptr;
-  float* part = dbias ? reinterpret_cast<float*>(ws + p.o_bias) : nullptr;
+  float* part = g.dbias ? reinterpret_cast<float*>(ws + p.o_bias) : nullptr;
   float* scale = nullptr;
-  if (sizeof(T) == 2 && std::is_same<T, _Float16>::value) {
+  if (std::is_same<T, _Float16>::value) {
     scale = reinterpret_cast<float*>(ws + p.o_scale);
-    scale_kernel<<<1, 1024, 0, st>>>(grad, targets, rows, vocab, scale);
+    scale_kernel<<<1, 1024, 0, st>>>(g.grad, g.targets, g.rows, g.vocab, scale);
   }
   const int64_t ldd = (int64_t)p.piece * (int)sizeof(T);
   for (int32_t k = 0; k < p.pieces; ++k) {
     const int32_t v0 = k * p.piece;
-    const int32_t nv = vocab - v0 < p.piece ? vocab - v0 : p.piece;
-    const Operand wp{ow.data + v0 * ow.ld, ow.ld, nv};
-    const GradEpilogue<T> ge{Logits{bias, targets, rows, vocab, v0}, grad, lse, scale, d, p.piece,
-                             part};
-    if (rows) launch_gemm<T, true, true>(wp, ox, nv, rows, p.padded, ge, st);
-    if (dx && rows) {
+    const int32_t nv = g.vocab - v0 < p.piece ? g.vocab - v0 : p.piece;
+    const Operand wp{w.data + v0 * w.ld, w.ld, nv};
+    const GradEpilogue<T> ge{Logits{g.bias, g.targets, g.rows, g.vocab, v0}, g.grad, g.lse, scale,
+                             d, p.piece, part};
+    if (g.rows) launch_gemm<T, true, true>(wp, x, nv, g.rows, p.padded, ge, st);
+    if (g.dx && g.rows) {
       // out[token, h]: m = h, n = token, k = vocabulary
-      const Operand a{wp.data, wp.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, rows};
-      const OutEpilogue<T> oe{static_cast<T*>(dx), sums, scale, hidden, rows, k == 0,
+      const Operand a{wp.data, wp.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, g.rows};
+      const OutEpilogue<T> oe{static_cast<T*>(g.dx), sums, scale, g.hidden, g.rows, k == 0,
                               k == p.pieces - 1};
-      launch_gemm<T, false, true>(a, b, hidden, rows, nv, oe, st);
+      launch_gemm<T, false, true>(a, b, g.hidden, g.rows, nv, oe, st);
     }
-    if (dw) {
+    if (g.dw) {
       // out[v, h]: m = h, n = v, k = token
-      const Operand a{ox.data, ox.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, nv};
-      const OutEpilogue<T> oe{static_cast<T*>(dw) + (int64_t)v0 * hidden, nullptr, scale, hidden,
-                              nv, true, true};
-      launch_gemm<T, false, false>(a, b, hidden, nv, rows, oe, st);
+      const Operand a{x.data, x.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, nv};
+      const OutEpilogue<T> oe{static_cast<T*>(g.dw) + (int64_t)v0 * g.hidden, nullptr, scale,
+                              g.hidden, nv, true, true};
+      launch_gemm<T, false, false>(a, b, g.hidden, nv, g.rows, oe, st);
     }
   }
-  if (dbias)
-    dbias_kernel<<<(unsigned)((vocab + 255) / 256), 256, 0, st>>>(part, p.tiles_n * 2, vocab,
-                                                                  dbias);
+  if (g.dbias)
+    dbias_kernel<<<(unsigned)((g.vocab + 255) / 256), 256, 0, st>>>(part, p.tiles_n * 2, g.vocab,
+                                                                    g.dbias);
 }
 
 }  // namespace
@@ -312,88 +319,84 @@ extern "C" {
 
 const char* ctcpb_lm_last_error(void) { return g_err.c_str(); }
 
-int ctcpb_lm_cache_plan(const int32_t* lengths, const int32_t* counts, int32_t rows,
-                        int32_t* tables, int64_t table_stride, int32_t table_width,
-                        const int32_t* pool, int32_t pool_size, const int32_t* taken,
-                        int32_t page_size, int32_t* slots, int32_t* positions, int32_t capacity,
-                        int32_t* starts, int32_t* out_lengths, int32_t* out_taken,
-                        int32_t* status, void* stream) {
+int ctcpb_lm_cache_plan(const ctcpb_lm_plan_args* args, void* stream) {
   return guarded([&] {
-    if (int rc = check_table(rows, table_stride, table_width, page_size)) return rc;
-    if (pool_size < 0 || capacity < 0 || capacity > (1 << 30))
+    if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    const ctcpb_lm_plan_args& g = *args;
+    if (int rc = check_table(g.rows, g.table_stride, g.table_width, g.page_size)) return rc;
+    if (g.pool_size < 0 || g.capacity < 0 || g.capacity > (1 << 30))
       return fail(CTCPB_ERR_INVALID, "need pool_size >= 0 and 0 <= capacity <= 2^30");
-    if ((rows && (!lengths || !counts || !out_lengths || !status || (!tables && table_width))) ||
-        (!pool && pool_size) || !taken || (capacity && (!slots || !positions)) || !starts ||
-        !out_taken)
+    if ((g.rows && (!g.lengths || !g.counts || !g.out_lengths || !g.status ||
+                    (!g.tables && g.table_width))) ||
+        (!g.pool && g.pool_size) || !g.taken || (g.capacity && (!g.slots || !g.positions)) ||
+        !g.starts || !g.out_taken)
       return fail(CTCPB_ERR_INVALID, kNull);
-    PlanArgs a{lengths, counts,    pool,        taken,     tables,     slots,
-               positions, starts,  out_lengths, out_taken, status,     table_stride,
-               rows,    table_width, pool_size, log2_of(page_size), capacity, 0};
-    const int threads = rows <= 256 ? 256 : kPlanThreads;
+    PlanArgs a{g.lengths,   g.counts, g.pool,        g.taken,     g.tables, g.slots,
+               g.positions, g.starts, g.out_lengths, g.out_taken, g.status, g.table_stride,
+               g.rows,      g.table_width, g.pool_size, log2_of(g.page_size), g.capacity, 0};
+    const int threads = g.rows <= 256 ? 256 : kPlanThreads;
     // a workgroup's part of the slot map: a few tokens per thread
     a.per_block = 4 * threads;
-    const int blocks = capacity ? (capacity + a.per_block - 1) / a.per_block : 1;
+    const int blocks = g.capacity ? (g.capacity + a.per_block - 1) / a.per_block : 1;
     plan_kernel<<<blocks, threads, 0, static_cast<hipStream_t>(stream)>>>(a);
     return launched("plan_kernel");
   });
 }
 
-int ctcpb_lm_cache_release(const uint8_t* finished, const int32_t* lengths, int32_t rows,
-                           const int32_t* tables, int64_t table_stride, int32_t table_width,
-                           int32_t* pool, int32_t pool_size, const int32_t* taken,
-                           int32_t page_size, int32_t* out_lengths, int32_t* out_taken,
-                           void* stream) {
+int ctcpb_lm_cache_release(const ctcpb_lm_release_args* args, void* stream) {
   return guarded([&] {
-    if (int rc = check_table(rows, table_stride, table_width, page_size)) return rc;
-    if (pool_size < 0) return fail(CTCPB_ERR_INVALID, "pool_size must be >= 0");
-    if ((rows && (!finished || !lengths || !out_lengths || (!tables && table_width))) ||
-        (!pool && pool_size) || !taken || !out_taken)
+    if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    const ctcpb_lm_release_args& g = *args;
+    if (int rc = check_table(g.rows, g.table_stride, g.table_width, g.page_size)) return rc;
+    if (g.pool_size < 0) return fail(CTCPB_ERR_INVALID, "pool_size must be >= 0");
+    if ((g.rows &&
+         (!g.finished || !g.lengths || !g.out_lengths || (!g.tables && g.table_width))) ||
+        (!g.pool && g.pool_size) || !g.taken || !g.out_taken)
       return fail(CTCPB_ERR_INVALID, kNull);
-    const ReleaseArgs a{finished, lengths,      tables, taken,       pool,      out_lengths,
-                        out_taken, table_stride, rows,   table_width, pool_size, log2_of(page_size)};
+    const ReleaseArgs a{g.finished,  g.lengths,      g.tables, g.taken,       g.pool,
+                        g.out_lengths, g.out_taken, g.table_stride, g.rows, g.table_width,
+                        g.pool_size, log2_of(g.page_size)};
     release_kernel<<<1, kPlanThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
     return launched("release_kernel");
   });
 }
 
-int ctcpb_lm_cache_store(int32_t dtype, const void* k, int64_t k_stride_t, int64_t k_stride_h,
-                         const void* v, int64_t v_stride_t, int64_t v_stride_h,
-                         const int32_t* slots, int32_t tokens, const ctcpb_lm_cache* k_cache,
-                         const ctcpb_lm_cache* v_cache, int32_t num_pages, int32_t page_size,
-                         int32_t kv_heads, int32_t head_dim, void* stream) {
+int ctcpb_lm_cache_store(const ctcpb_lm_store_args* args, void* stream) {
   return guarded([&] {
-    const int es = elem_size(dtype);
+    if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    const ctcpb_lm_store_args& g = *args;
+    const int es = elem_size(g.dtype);
     if (!es) return fail(CTCPB_ERR_INVALID, kBadType);
-    if (int rc = check_pages(num_pages, page_size)) return rc;
-    if (tokens < 0 || kv_heads < 1 || head_dim < 1)
+    if (int rc = check_pages(g.num_pages, g.page_size)) return rc;
+    if (g.tokens < 0 || g.kv_heads < 1 || g.head_dim < 1)
       return fail(CTCPB_ERR_INVALID, "need tokens >= 0, kv_heads >= 1 and head_dim >= 1");
-    if ((int64_t)kv_heads * head_dim > INT_MAX)
+    if ((int64_t)g.kv_heads * g.head_dim > INT_MAX)
       return fail(CTCPB_ERR_INVALID, "kv_heads * head_dim must be below 2^31");
-    if (k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0)
+    if (g.k_stride_t < 0 || g.k_stride_h < 0 || g.v_stride_t < 0 || g.v_stride_h < 0)
       return fail(CTCPB_ERR_INVALID, "strides must be >= 0");
-    if (int rc = check_cache(k_cache)) return rc;
-    if (int rc = check_cache(v_cache)) return rc;
-    if (tokens == 0) return ok();
-    if (!k || !v || !slots) return fail(CTCPB_ERR_INVALID, kNull);
+    if (int rc = check_cache(g.k_cache)) return rc;
+    if (int rc = check_cache(g.v_cache)) return rc;
+    if (g.tokens == 0) return ok();
+    if (!g.k || !g.v || !g.slots) return fail(CTCPB_ERR_INVALID, kNull);
     StoreArgs a{};
-    a.k = static_cast<const char*>(k);
-    a.v = static_cast<const char*>(v);
-    a.k_t = k_stride_t * es;
-    a.k_h = k_stride_h * es;
-    a.v_t = v_stride_t * es;
-    a.v_h = v_stride_h * es;
-    a.slots = slots;
-    a.kc = view(k_cache, es);
-    a.vc = view(v_cache, es);
-    a.heads = kv_heads;
-    a.page_log = log2_of(page_size);
-    a.num_slots = num_pages * page_size;
-    const bool wide = head_dim * es % 16 == 0 && aligned(k, 16) && aligned(v, 16) &&
+    a.k = static_cast<const char*>(g.k);
+    a.v = static_cast<const char*>(g.v);
+    a.k_t = g.k_stride_t * es;
+    a.k_h = g.k_stride_h * es;
+    a.v_t = g.v_stride_t * es;
+    a.v_h = g.v_stride_h * es;
+    a.slots = g.slots;
+    a.kc = view(g.k_cache, es);
+    a.vc = view(g.v_cache, es);
+    a.heads = g.kv_heads;
+    a.page_log = log2_of(g.page_size);
+    a.num_slots = g.num_pages * g.page_size;
+    const bool wide = g.head_dim * es % 16 == 0 && aligned(g.k, 16) && aligned(g.v, 16) &&
                       a.k_t % 16 == 0 && a.k_h % 16 == 0 && a.v_t % 16 == 0 && a.v_h % 16 == 0 &&
                       wide_cache(a.kc) && wide_cache(a.vc);
     const int size = wide ? 16 : es;
-    a.per_head = head_dim * es / size;
-    a.pieces = (int64_t)tokens * kv_heads * a.per_head;
+    a.per_head = g.head_dim * es / size;
+    a.pieces = (int64_t)g.tokens * g.kv_heads * a.per_head;
     int64_t blocks = (a.pieces + 255) / 256;
     if (blocks > 1 << 20) blocks = 1 << 20;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -407,84 +410,73 @@ int ctcpb_lm_cache_store(int32_t dtype, const void* k, int64_t k_stride_t, int64
   });
 }
 
-int ctcpb_lm_attention_workspace(int32_t dtype, int32_t rows, int32_t q_heads, int32_t kv_heads,
-                                 int32_t head_dim, int32_t max_len, int32_t window,
-                                 size_t* out_bytes) {
+int ctcpb_lm_attention_workspace(const ctcpb_lm_attention_args* args, size_t* out_bytes) {
   return guarded([&] {
-    if (int rc = check_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window))
-      return rc;
-    if (!out_bytes) return fail(CTCPB_ERR_INVALID, "out_bytes is NULL");
-    *out_bytes = plan_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window).bytes;
+    if (!args || !out_bytes) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    if (int rc = check_attention(*args)) return rc;
+    *out_bytes = plan_attention(*args).bytes;
     return ok();
   });
 }
 
-int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t q_stride_h,
-                       const ctcpb_lm_cache* k_cache, const ctcpb_lm_cache* v_cache,
-                       int32_t num_pages, int32_t page_size, const int32_t* tables,
-                       int64_t table_stride, int32_t table_width, const int32_t* lengths,
-                       int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                       int32_t max_len, int32_t window, float scale, void* out,
-                       int64_t out_stride_r, int64_t out_stride_h, float* lse, void* workspace,
+int ctcpb_lm_attention(const ctcpb_lm_attention_args* args, void* workspace,
                        size_t workspace_bytes, void* stream) {
   return guarded([&] {
-    if (int rc = check_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window))
-      return rc;
-    if (int rc = check_pages(num_pages, page_size)) return rc;
-    if (int rc = check_table(rows, table_stride, table_width, page_size)) return rc;
-    if (q_stride_r < 0 || q_stride_h < 0 || out_stride_r < 0 || out_stride_h < 0)
+    if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    const ctcpb_lm_attention_args& g = *args;
+    if (int rc = check_attention(g)) return rc;
+    if (int rc = check_pages(g.num_pages, g.page_size)) return rc;
+    if (g.q_stride_r < 0 || g.q_stride_h < 0 || g.out_stride_r < 0 || g.out_stride_h < 0)
       return fail(CTCPB_ERR_INVALID, "strides must be >= 0");
-    if (int rc = check_cache(k_cache)) return rc;
-    if (int rc = check_cache(v_cache)) return rc;
-    const int es = elem_size(dtype);
+    if (int rc = check_cache(g.k_cache)) return rc;
+    if (int rc = check_cache(g.v_cache)) return rc;
+    const int es = elem_size(g.dtype);
     AttnArgs a{};
-    a.kc = view(k_cache, es);
-    a.vc = view(v_cache, es);
+    a.kc = view(g.k_cache, es);
+    a.vc = view(g.v_cache, es);
     if (!wide_cache(a.kc) || !wide_cache(a.vc))
       return fail(CTCPB_ERR_INVALID,
                   "caches must be 16-byte aligned, with strides that are multiples of 16 bytes");
-    if (rows == 0) return ok();
-    const int32_t held = table_width * page_size;
-    if (max_len == 0 || max_len > held) max_len = held;
-    if (!q || !out || !lengths || (!tables && max_len)) return fail(CTCPB_ERR_INVALID, kNull);
-    const AttnPlan p =
-        plan_attention(dtype, rows, q_heads, kv_heads, head_dim, max_len, window);
+    if (g.rows == 0) return ok();
+    if (!g.q || !g.out || !g.lengths || (!g.tables && g.table_width))
+      return fail(CTCPB_ERR_INVALID, kNull);
+    const AttnPlan p = plan_attention(g);
     if (p.bytes && (!workspace || !aligned(workspace, 16)))
       return fail(CTCPB_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
     if (workspace_bytes < p.bytes)
       return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_attention_workspace");
-    if ((int64_t)rows * kv_heads * p.head_tiles * p.splits > INT_MAX ||
-        (int64_t)rows * q_heads > INT_MAX)
+    if ((int64_t)g.rows * g.kv_heads * p.head_tiles * p.splits > INT_MAX ||
+        (int64_t)g.rows * g.q_heads > INT_MAX)
       return fail(CTCPB_ERR_UNSUPPORTED, "too many rows for one launch");
-    a.q = static_cast<const char*>(q);
-    a.out = static_cast<char*>(out);
-    a.lse = lse;
+    a.q = static_cast<const char*>(g.q);
+    a.out = static_cast<char*>(g.out);
+    a.lse = g.lse;
     a.part = static_cast<float*>(workspace);
-    a.tables = tables;
-    a.lengths = lengths;
-    a.q_r = q_stride_r;
-    a.q_h = q_stride_h;
-    a.out_r = out_stride_r;
-    a.out_h = out_stride_h;
-    a.table_stride = table_stride;
-    a.rows = rows;
-    a.heads = q_heads;
-    a.kv_heads = kv_heads;
-    a.group = q_heads / kv_heads;
+    a.tables = g.tables;
+    a.lengths = g.lengths;
+    a.q_r = g.q_stride_r;
+    a.q_h = g.q_stride_h;
+    a.out_r = g.out_stride_r;
+    a.out_h = g.out_stride_h;
+    a.table_stride = g.table_stride;
+    a.rows = g.rows;
+    a.heads = g.q_heads;
+    a.kv_heads = g.kv_heads;
+    a.group = g.q_heads / g.kv_heads;
     a.head_tiles = p.head_tiles;
-    a.D = head_dim;
-    a.width = table_width;
-    a.page_log = log2_of(page_size);
-    a.num_pages = num_pages;
+    a.D = g.head_dim;
+    a.width = g.table_width;
+    a.page_log = log2_of(g.page_size);
+    a.num_pages = g.num_pages;
     a.max_len = p.max_len;
-    a.window = window;
+    a.window = g.window;
     a.chunk = p.chunk;
     a.splits = p.splits;
-    a.scale = scale;
+    a.scale = g.scale;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (dtype == CTCPB_LM_BF16)
+    if (g.dtype == CTCPB_LM_BF16)
       launch_attention<__bf16>(a, p, st);
-    else if (dtype == CTCPB_LM_F16)
+    else if (g.dtype == CTCPB_LM_F16)
       launch_attention<_Float16>(a, p, st);
     else
       launch_attention<float>(a, p, st);
@@ -492,70 +484,64 @@ int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t
   });
 }
 
-int ctcpb_lm_loss_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
-                            int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
-                            size_t* out_bytes) {
+int ctcpb_lm_loss_workspace(const ctcpb_lm_loss_args* args, size_t* out_bytes) {
   return guarded([&] {
-    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
-    if (!out_bytes) return fail(CTCPB_ERR_INVALID, "out_bytes is NULL");
-    *out_bytes = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, false).bytes;
+    if (!args || !out_bytes) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    if (int rc = check_loss(*args)) return rc;
+    *out_bytes = plan_loss(*args, false).bytes;
     return ok();
   });
 }
 
-int ctcpb_lm_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
-                  const float* bias, const int32_t* targets, int32_t rows, int32_t vocab,
-                  int32_t hidden, float* loss, float* lse, void* workspace,
-                  size_t workspace_bytes, void* stream) {
+int ctcpb_lm_loss(const ctcpb_lm_loss_args* args, void* workspace, size_t workspace_bytes,
+                  void* stream) {
   return guarded([&] {
-    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
-    if (rows == 0) return ok();
-    if (!x || !w || !targets || !loss || !lse || !workspace) return fail(CTCPB_ERR_INVALID, kNull);
+    if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    const ctcpb_lm_loss_args& g = *args;
+    if (int rc = check_loss(g)) return rc;
+    if (g.rows == 0) return ok();
+    if (!g.x || !g.w || !g.targets || !g.loss || !g.lse || !workspace)
+      return fail(CTCPB_ERR_INVALID, kNull);
     if (!aligned(workspace, 256))
       return fail(CTCPB_ERR_INVALID, "workspace must be 256-byte aligned");
-    const LossPlan p = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, false);
+    const LossPlan p = plan_loss(g, false);
     if (workspace_bytes < p.bytes)
       return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_loss_workspace");
-    const auto f = dtype == CTCPB_LM_BF16  ? run_loss<__bf16>
-                   : dtype == CTCPB_LM_F16 ? run_loss<_Float16>
-                                           : run_loss<float>;
-    f(p, x, stride_x, w, stride_w, bias, targets, rows, vocab, hidden, loss, lse,
-      static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+    const auto f = g.dtype == CTCPB_LM_BF16  ? run_loss<__bf16>
+                   : g.dtype == CTCPB_LM_F16 ? run_loss<_Float16>
+                                             : run_loss<float>;
+    f(p, g, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
     return launched("loss kernels");
   });
 }
 
-int ctcpb_lm_loss_grad_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
-                                 int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
-                                 size_t* out_bytes) {
+int ctcpb_lm_loss_grad_workspace(const ctcpb_lm_grad_args* args, size_t* out_bytes) {
   return guarded([&] {
-    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
-    if (!out_bytes) return fail(CTCPB_ERR_INVALID, "out_bytes is NULL");
-    *out_bytes = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, true).bytes;
+    if (!args || !out_bytes) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    if (int rc = check_loss(*args)) return rc;
+    *out_bytes = plan_loss(*args, true).bytes;
     return ok();
   });
 }
 
-int ctcpb_lm_loss_grad(int32_t dtype, const float* grad, const void* x, int64_t stride_x,
-                       const void* w, int64_t stride_w, const float* bias,
-                       const int32_t* targets, const float* lse, int32_t rows, int32_t vocab,
-                       int32_t hidden, void* dx, void* dw, float* dbias, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+int ctcpb_lm_loss_grad(const ctcpb_lm_grad_args* args, void* workspace, size_t workspace_bytes,
+                       void* stream) {
   return guarded([&] {
-    if (int rc = check_loss(dtype, stride_x, stride_w, rows, vocab, hidden)) return rc;
-    if (!dx && !dw && !dbias) return ok();
-    if (!w || !workspace || (rows && (!grad || !x || !targets || !lse)))
+    if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
+    const ctcpb_lm_grad_args& g = *args;
+    if (int rc = check_loss(g)) return rc;
+    if (!g.dx && !g.dw && !g.dbias) return ok();
+    if (!g.w || !workspace || (g.rows && (!g.grad || !g.x || !g.targets || !g.lse)))
       return fail(CTCPB_ERR_INVALID, kNull);
-    if (!aligned(workspace, 256) || (dx && !aligned(dx, 16)) || (dw && !aligned(dw, 16)))
+    if (!aligned(workspace, 256) || !aligned(g.dx, 16) || !aligned(g.dw, 16))
       return fail(CTCPB_ERR_INVALID, "workspace must be 256-byte aligned, dx and dw 16-byte");
-    const LossPlan p = plan_loss(dtype, x, stride_x, w, stride_w, rows, vocab, hidden, true);
+    const LossPlan p = plan_loss(g, true);
     if (workspace_bytes < p.bytes)
       return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_loss_grad_workspace");
-    const auto f = dtype == CTCPB_LM_BF16  ? run_grad<__bf16>
-                   : dtype == CTCPB_LM_F16 ? run_grad<_Float16>
-                                           : run_grad<float>;
-    f(p, grad, x, stride_x, w, stride_w, bias, targets, lse, rows, vocab, hidden, dx, dw, dbias,
-      static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+    const auto f = g.dtype == CTCPB_LM_BF16  ? run_grad<__bf16>
+                   : g.dtype == CTCPB_LM_F16 ? run_grad<_Float16>
+                                             : run_grad<float>;
+    f(p, g, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
     return launched("loss gradient kernels");
   });
 }

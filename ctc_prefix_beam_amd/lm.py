@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -32,11 +33,14 @@ EXPORTS = ("ctcpb_lm_cache_plan", "ctcpb_lm_cache_release", "ctcpb_lm_cache_stor
 NO_PAGE, NO_ENTRY, NO_SLOT = 1, 2, 4   # status bits of cache_plan
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-
-class CtcpbLmCache(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
-                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
-
+# The argument structures of include/ctcpb_lm.h, in order (native sizes and
+# alignment): a call packs them once instead of converting each argument.
+_PLAN = struct.Struct("11Pq5i4x")
+_RELEASE = struct.Struct("7Pq4i")
+_STORE = struct.Struct("3P4qP3qP3q6i")
+_ATTENTION = struct.Struct("5P5qP3qP3q10if4x")
+_LOSS = struct.Struct("6P2q4i")
+_GRAD = struct.Struct("9P2q4i")
 
 _lib = None
 
@@ -48,22 +52,13 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with ctc_prefix_beam_amd.build")
         L = ctypes.CDLL(LIB_PATH)
-        p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-        f32, cachep, szp = ctypes.c_float, ctypes.POINTER(CtcpbLmCache), ctypes.POINTER(sz)
-        L.ctcpb_lm_cache_plan.argtypes = [p, p, i32, p, i64, i32, p, i32, p, i32, p, p, i32, p, p,
-                                          p, p, p]
-        L.ctcpb_lm_cache_release.argtypes = [p, p, i32, p, i64, i32, p, i32, p, i32, p, p, p]
-        L.ctcpb_lm_cache_store.argtypes = [i32, p, i64, i64, p, i64, i64, p, i32, cachep, cachep,
-                                           i32, i32, i32, i32, p]
-        L.ctcpb_lm_attention_workspace.argtypes = [i32, i32, i32, i32, i32, i32, i32, szp]
-        L.ctcpb_lm_attention.argtypes = [i32, p, i64, i64, cachep, cachep, i32, i32, p, i64, i32,
-                                         p, i32, i32, i32, i32, i32, i32, f32, p, i64, i64, p, p,
-                                         sz, p]
-        L.ctcpb_lm_loss_workspace.argtypes = [i32, p, i64, p, i64, i32, i32, i32, szp]
-        L.ctcpb_lm_loss.argtypes = [i32, p, i64, p, i64, p, p, i32, i32, i32, p, p, p, sz, p]
-        L.ctcpb_lm_loss_grad_workspace.argtypes = [i32, p, i64, p, i64, i32, i32, i32, szp]
-        L.ctcpb_lm_loss_grad.argtypes = [i32, p, p, i64, p, i64, p, p, p, i32, i32, i32, p, p, p,
-                                         p, sz, p]
+        p, sz = ctypes.c_void_p, ctypes.c_size_t
+        args = ctypes.c_char_p   # the packed structure
+        for name in ("cache_plan", "cache_release", "cache_store"):
+            getattr(L, "ctcpb_lm_" + name).argtypes = [args, p]
+        for name in ("attention", "loss", "loss_grad"):
+            getattr(L, f"ctcpb_lm_{name}_workspace").argtypes = [args, ctypes.POINTER(sz)]
+            getattr(L, "ctcpb_lm_" + name).argtypes = [args, p, sz, p]
         for name in EXPORTS[:-1]:   # all but the string getter
             getattr(L, name).restype = ctypes.c_int
         L.ctcpb_lm_last_error.restype = ctypes.c_char_p
@@ -80,60 +75,92 @@ def _check(rc: int):
         raise RuntimeError(f"ctcpb_lm error {rc}: {msg}")
 
 
-class _On:
-    """The stream a call runs on, and the memory it allocates for itself: made
-    on the current stream, and marked as used by `stream` if that is another
-    one, so that it is not handed out again while the call still runs."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, stream, device):
-        if device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {device}, which is not the current device "
-                             f"({torch.cuda.current_device()})")
-        self.current = torch.cuda.current_stream(device)
-        self.stream = self.current if stream is None else stream
-        self.other = self.stream.cuda_stream != self.current.cuda_stream
-        self.device = device
-        self.ptr = self.stream.cuda_stream
 
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other:
-            # it may have been in use on the current stream until now
-            self.stream.wait_stream(self.current)
-            t.record_stream(self.stream)
+class _Other:
+    """Memory for a call on another stream than the current one: made on the
+    current stream, which the other one waits for (the memory may have been in
+    use there until now), and marked as used by the other one, so that it is not
+    handed out again while the call still runs."""
+
+    def __init__(self, stream, index):
+        self.stream, self.current = stream, torch.cuda.current_stream(index)
+
+    def __call__(self, shape, dtype, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+        self.stream.wait_stream(self.current)
+        t.record_stream(self.stream)
         return t
+
+
+def _on(stream, index):
+    """(hipStream_t, allocator) of a call on `stream` (None: the current one)
+    with tensors on GPU `index`, which has to be the current device."""
+    if index != _current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is "
+                         f"cuda:{_current_device()}")
+    raw = _raw_stream(index)
+    if stream is None or stream.cuda_stream == raw:
+        return raw, torch.empty
+    return stream.cuda_stream, _Other(stream, index)
 
 
 def _gpu(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    return t.device
+    return t.get_device()
 
 
-def _i32(t, device, name, shape):
-    _check_dev(t, device, name, torch.int32, shape, contiguous=True)
+def _i32(t, index, name, shape):
+    """Raise ValueError unless `t` is a contiguous int32 tensor of `shape` on GPU `index`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == index and
+            t.shape == shape and t.is_contiguous()):
+        _check_dev(t, torch.device("cuda", index), name, torch.int32, shape, contiguous=True)
 
 
-def _tables(tables, device, rows):
-    _check_dev(tables, device, "tables", torch.int32)
-    if tables.dim() != 2 or tables.shape[0] != rows or (tables.shape[1] > 1 and
-                                                        tables.stride(1) != 1):
-        raise ValueError("tables must be (rows, width) int32 with unit stride over the width")
-    return max(tables.stride(0), tables.shape[1]) if rows <= 1 else tables.stride(0)
+def _like(t, index, name, dtype, shape=None):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and
+            (shape is None or t.shape == shape)):
+        _check_dev(t, torch.device("cuda", index), name, dtype, shape)
 
 
-def _cache(t, device, name, dtype, shape=None):
-    _check_dev(t, device, name, dtype, shape)
-    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-        raise ValueError(f"{name} must be (pages, page_size, kv_heads, head_dim) with unit "
-                         "stride over head_dim")
-    return CtcpbLmCache(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+def _tables(tables, index, rows):
+    """(row stride, width) of page tables."""
+    _like(tables, index, "tables", torch.int32)
+    if tables.dim() == 2 and tables.shape[0] == rows:
+        stride, one = tables.stride()
+        width = tables.shape[1]
+        if one == 1 or width <= 1:
+            return (stride if rows > 1 else max(stride, width)), width
+    raise ValueError("tables must be (rows, width) int32 with unit stride over the width")
+
+
+def _cache(t, index, name, dtype, shape=None):
+    _like(t, index, name, dtype, shape)
+    if t.dim() == 4:
+        page, token, head, one = t.stride()
+        if one == 1 or t.shape[3] <= 1:
+            return t.data_ptr(), page, token, head
+    raise ValueError(f"{name} must be (pages, page_size, kv_heads, head_dim) with unit stride "
+                     "over head_dim")
+
+
+def _rows(t, name):
+    """(row stride, head stride, shape) of a (rows, heads, head_dim) tensor."""
+    if t.dim() == 3:
+        row, head, one = t.stride()
+        if one == 1 or t.shape[2] <= 1:
+            return row, head, t.shape
+    raise ValueError(f"{name} must have three axes, the last one with unit stride")
 
 
 def _type(t, name):
-    if t.dtype not in _TYPES:
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    return _TYPES[t.dtype]
+    return dt
 
 
 class CachePlan(NamedTuple):
@@ -157,23 +184,22 @@ def cache_plan(lengths, counts, tables, pool, taken, page_size: int, total: int,
     rows = lengths.numel()
     _i32(lengths, dev, "lengths", (rows,))
     _i32(counts, dev, "counts", (rows,))
-    stride = _tables(tables, dev, rows)
+    stride, width = _tables(tables, dev, rows)
     _i32(pool, dev, "pool", (pool.numel(),))
     _i32(taken, dev, "taken", (1,))
     if total < 0:
         raise ValueError("total must be >= 0")
-    on = _On(stream, dev)
+    raw, empty = _on(stream, dev)
     # one allocation for all outputs
-    buf = on.empty((2 * total + 3 * rows + 2,), torch.int32)
-    slots, positions, starts, after, now, status = buf.split(
-        (total, total, rows + 1, rows, 1, rows))
+    buf = empty((2 * total + 3 * rows + 2,), dtype=torch.int32, device=lengths.device)
     base = buf.data_ptr()
     at = base + 8 * total
-    _check(lib().ctcpb_lm_cache_plan(
-        lengths.data_ptr(), counts.data_ptr(), rows, tables.data_ptr(), stride, tables.shape[1],
-        pool.data_ptr(), pool.numel(), taken.data_ptr(), page_size, base, base + 4 * total, total,
-        at, at + 4 * (rows + 1), at + 4 * (2 * rows + 1), at + 4 * (2 * rows + 2), on.ptr))
-    return CachePlan(slots, positions, starts, after, now, status)
+    _check(lib().ctcpb_lm_cache_plan(_PLAN.pack(
+        lengths.data_ptr(), counts.data_ptr(), tables.data_ptr(), pool.data_ptr(),
+        taken.data_ptr(), base, base + 4 * total, at, at + 4 * (rows + 1),
+        at + 4 * (2 * rows + 1), at + 4 * (2 * rows + 2), stride, rows, width, pool.numel(),
+        page_size, total), raw))
+    return CachePlan._make(buf.split_with_sizes((total, total, rows + 1, rows, 1, rows)))
 
 
 def cache_release(finished, lengths, tables, pool, taken, page_size: int, stream=None):
@@ -182,17 +208,18 @@ def cache_release(finished, lengths, tables, pool, taken, page_size: int, stream
     `taken` only, so the call can be repeated on the same inputs."""
     dev = _gpu(lengths, "lengths")
     rows = lengths.numel()
-    _check_dev(finished, dev, "finished", torch.uint8, (rows,), contiguous=True)
+    _check_dev(finished, lengths.device, "finished", torch.uint8, (rows,), contiguous=True)
     _i32(lengths, dev, "lengths", (rows,))
-    stride = _tables(tables, dev, rows)
+    stride, width = _tables(tables, dev, rows)
     _i32(pool, dev, "pool", (pool.numel(),))
     _i32(taken, dev, "taken", (1,))
-    on = _On(stream, dev)
-    buf = on.empty((rows + 1,), torch.int32)
+    raw, empty = _on(stream, dev)
+    buf = empty((rows + 1,), dtype=torch.int32, device=lengths.device)
     base = buf.data_ptr()
-    _check(lib().ctcpb_lm_cache_release(
-        finished.data_ptr(), lengths.data_ptr(), rows, tables.data_ptr(), stride, tables.shape[1],
-        pool.data_ptr(), pool.numel(), taken.data_ptr(), page_size, base, base + 4 * rows, on.ptr))
+    _check(lib().ctcpb_lm_cache_release(_RELEASE.pack(
+        finished.data_ptr(), lengths.data_ptr(), tables.data_ptr(), pool.data_ptr(),
+        taken.data_ptr(), base, base + 4 * rows, stride, rows, width, pool.numel(), page_size),
+        raw))
     return buf[:rows], buf[rows:]
 
 
@@ -203,23 +230,21 @@ def cache_store(k, v, slots, k_cache, v_cache, stream=None):
     with head_dim innermost."""
     dev = _gpu(k, "k")
     dt = _type(k, "k")
-    if k.dim() != 3 or (k.shape[2] > 1 and k.stride(2) != 1):
-        raise ValueError("k must be (tokens, kv_heads, head_dim) with unit stride over head_dim")
-    T, H, D = k.shape
-    _check_dev(v, dev, "v", k.dtype, (T, H, D))
-    if D > 1 and v.stride(2) != 1:
-        raise ValueError("v must have unit stride over head_dim")
+    kt, kh, shape = _rows(k, "k")
+    _like(v, dev, "v", k.dtype, shape)
+    vt, vh, _ = _rows(v, "v")
+    T, H, D = shape
     _i32(slots, dev, "slots", (T,))
     kc = _cache(k_cache, dev, "k_cache", k.dtype)
-    vc = _cache(v_cache, dev, "v_cache", k.dtype, k_cache.shape)
-    if tuple(k_cache.shape[2:]) != (H, D):
-        raise ValueError(f"caches must have {H} heads of {D}, got {tuple(k_cache.shape[2:])}")
+    pages, page_size, heads, dim = cs = k_cache.shape
+    vc = _cache(v_cache, dev, "v_cache", k.dtype, cs)
+    if heads != H or dim != D:
+        raise ValueError(f"caches must have {H} heads of {D}, got {(heads, dim)}")
     if T == 0:
         return
-    _check(lib().ctcpb_lm_cache_store(
-        dt, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-        slots.data_ptr(), T, ctypes.byref(kc), ctypes.byref(vc), k_cache.shape[0],
-        k_cache.shape[1], H, D, _On(stream, dev).ptr))
+    _check(lib().ctcpb_lm_cache_store(_STORE.pack(
+        k.data_ptr(), v.data_ptr(), slots.data_ptr(), kt, kh, vt, vh, *kc, *vc, dt, T, pages,
+        page_size, H, D), _on(stream, dev)[0]))
 
 
 def attention(q, k_cache, v_cache, tables, lengths, scale: float | None = None, window: int = 0,
@@ -233,63 +258,63 @@ def attention(q, k_cache, v_cache, tables, lengths, scale: float | None = None, 
     without tokens gives zeros and -inf."""
     dev = _gpu(q, "q")
     dt = _type(q, "q")
-    if q.dim() != 3 or (q.shape[2] > 1 and q.stride(2) != 1):
-        raise ValueError("q must be (rows, q_heads, head_dim) with unit stride over head_dim")
-    R, Hq, D = q.shape
+    qr, qh, shape = _rows(q, "q")
+    R, Hq, D = shape
     kc = _cache(k_cache, dev, "k_cache", q.dtype)
-    vc = _cache(v_cache, dev, "v_cache", q.dtype, k_cache.shape)
-    pages, page_size, Hkv, Dk = k_cache.shape
+    pages, page_size, Hkv, Dk = cs = k_cache.shape
+    vc = _cache(v_cache, dev, "v_cache", q.dtype, cs)
     if Dk != D:
         raise ValueError(f"caches must have heads of {D}, got {Dk}")
-    stride = _tables(tables, dev, R)
+    stride, width = _tables(tables, dev, R)
     _i32(lengths, dev, "lengths", (R,))
-    if out is not None:
-        _check_dev(out, dev, "out", q.dtype, q.shape)
-        if D > 1 and out.stride(2) != 1:
-            raise ValueError("out must have unit stride over head_dim")
     L = lib()
-    width = tables.shape[1]
-    bound = width * page_size
-    if 0 < max_len < bound:
-        bound = max_len
-    need = ctypes.c_size_t()
-    _check(L.ctcpb_lm_attention_workspace(dt, R, Hq, Hkv, D, bound, window, ctypes.byref(need)))
-    on = _On(stream, dev)
+    raw, empty = _on(stream, dev)
     if out is None:
-        out = on.empty((R, Hq, D), q.dtype)
-    lse = on.empty((R, Hq), torch.float32)
-    ws = on.empty((need.value,), torch.uint8) if need.value else None
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    _check(L.ctcpb_lm_attention(
-        dt, q.data_ptr(), q.stride(0), q.stride(1), ctypes.byref(kc), ctypes.byref(vc), pages,
-        page_size, tables.data_ptr(), stride, width, lengths.data_ptr(), R, Hq, Hkv, D, bound,
-        window, scale, out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(),
-        ws.data_ptr() if ws is not None else None, need.value, on.ptr))
+        out = empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _like(out, dev, "out", q.dtype, shape)
+    outr, outh, _ = _rows(out, "out")
+    lse = empty((R, Hq), dtype=torch.float32, device=q.device)
+    args = _ATTENTION.pack(
+        q.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), qr, qh,
+        outr, outh, stride, *kc, *vc, dt, R, Hq, Hkv, D, pages, page_size, width, max_len, window,
+        1.0 / math.sqrt(D) if scale is None else scale)
+    need = ctypes.c_size_t()
+    _check(L.ctcpb_lm_attention_workspace(args, need))
+    size = need.value
+    # freed on return: the stream's later work may have it, after this call
+    ws = empty((size,), dtype=torch.uint8, device=q.device) if size else None
+    _check(L.ctcpb_lm_attention(args, ws.data_ptr() if size else None, size, raw))
     return out, lse
 
 
 def _loss_args(x, w, targets, bias):
     dev = _gpu(x, "x")
     dt = _type(x, "x")
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
         raise ValueError("x must be (rows, hidden) with unit stride over hidden")
     N, H = x.shape
-    _check_dev(w, dev, "w", x.dtype)
-    if w.dim() != 2 or w.shape[1] != H or (H > 1 and w.stride(1) != 1):
+    _like(w, dev, "w", x.dtype)
+    if w.dim() != 2 or w.shape[1] != H or (w.stride(1) != 1 and H > 1):
         raise ValueError(f"w must be (vocab, {H}) with unit stride over hidden")
     V = w.shape[0]
     _i32(targets, dev, "targets", (N,))
     if bias is not None:
-        _check_dev(bias, dev, "bias", torch.float32, (V,), contiguous=True)
+        _floats(bias, dev, "bias", V)
     # a single row's stride is of no account, and may be anything
     sx = x.stride(0) if N > 1 else H
     sw = w.stride(0) if V > 1 else H
-    return dev, dt, N, V, H, sx, sw
+    return dev, N, V, H, (sx, sw, dt, N, V, H)
+
+
+def _floats(t, index, name, n):
+    _like(t, index, name, torch.float32, (n,))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    return 0 if t is None else t.data_ptr()
 
 
 def token_loss_forward(x, w, targets, bias=None, stream=None):
@@ -297,39 +322,40 @@ def token_loss_forward(x, w, targets, bias=None, stream=None):
     (vocab, hidden) of one type, bias float32 (vocab,) or None, targets int32
     (rows,).  loss = lse - logit of the target, 0 where the target is outside
     the vocabulary (the decoder's -1 padding)."""
-    dev, dt, N, V, H, sx, sw = _loss_args(x, w, targets, bias)
+    dev, N, V, H, sizes = _loss_args(x, w, targets, bias)
     L = lib()
+    raw, empty = _on(stream, dev)
+    loss = empty((N,), dtype=torch.float32, device=x.device)
+    lse = empty((N,), dtype=torch.float32, device=x.device)
+    args = _LOSS.pack(x.data_ptr(), w.data_ptr(), _ptr(bias), targets.data_ptr(), loss.data_ptr(),
+                      lse.data_ptr(), *sizes)
     need = ctypes.c_size_t()
-    _check(L.ctcpb_lm_loss_workspace(dt, x.data_ptr(), sx, w.data_ptr(), sw, N, V, H,
-                                     ctypes.byref(need)))
-    on = _On(stream, dev)
-    out = on.empty((2, N), torch.float32)
-    ws = on.empty((need.value,), torch.uint8)
-    _check(L.ctcpb_lm_loss(dt, x.data_ptr(), sx, w.data_ptr(), sw, _ptr(bias), targets.data_ptr(),
-                           N, V, H, out.data_ptr(), out.data_ptr() + 4 * N, ws.data_ptr(),
-                           need.value, on.ptr))
-    return out[0], out[1]
+    _check(L.ctcpb_lm_loss_workspace(args, need))
+    ws = empty((need.value,), dtype=torch.uint8, device=x.device)
+    _check(L.ctcpb_lm_loss(args, ws.data_ptr(), need.value, raw))
+    return loss, lse
 
 
 def token_loss_backward(grad, x, w, targets, lse, bias=None, need=(True, True, True), stream=None):
     """Gradients (dx, dw, dbias) of sum(grad * loss) for ``token_loss_forward``
     with its lse; grad (rows,) float32.  dx and dw have x's and w's type, dbias
     is float32 (None without a bias).  `need` says which of them to compute."""
-    dev, dt, N, V, H, sx, sw = _loss_args(x, w, targets, bias)
-    _check_dev(grad, dev, "grad", torch.float32, (N,), contiguous=True)
-    _check_dev(lse, dev, "lse", torch.float32, (N,), contiguous=True)
+    dev, N, V, H, sizes = _loss_args(x, w, targets, bias)
+    _floats(grad, dev, "grad", N)
+    _floats(lse, dev, "lse", N)
     L = lib()
+    raw, empty = _on(stream, dev)
+    dx = empty((N, H), dtype=x.dtype, device=x.device) if need[0] else None
+    dw = empty((V, H), dtype=w.dtype, device=x.device) if need[1] else None
+    db = None
+    if need[2] and bias is not None:
+        db = empty((V,), dtype=torch.float32, device=x.device)
+    args = _GRAD.pack(x.data_ptr(), w.data_ptr(), _ptr(bias), targets.data_ptr(), grad.data_ptr(),
+                      lse.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), *sizes)
     size = ctypes.c_size_t()
-    _check(L.ctcpb_lm_loss_grad_workspace(dt, x.data_ptr(), sx, w.data_ptr(), sw, N, V, H,
-                                          ctypes.byref(size)))
-    on = _On(stream, dev)
-    dx = on.empty((N, H), x.dtype) if need[0] else None
-    dw = on.empty((V, H), w.dtype) if need[1] else None
-    db = on.empty((V,), torch.float32) if need[2] and bias is not None else None
-    ws = on.empty((size.value,), torch.uint8)
-    _check(L.ctcpb_lm_loss_grad(dt, grad.data_ptr(), x.data_ptr(), sx, w.data_ptr(), sw,
-                                _ptr(bias), targets.data_ptr(), lse.data_ptr(), N, V, H, _ptr(dx),
-                                _ptr(dw), _ptr(db), ws.data_ptr(), size.value, on.ptr))
+    _check(L.ctcpb_lm_loss_grad_workspace(args, size))
+    ws = empty((size.value,), dtype=torch.uint8, device=x.device)
+    _check(L.ctcpb_lm_loss_grad(args, ws.data_ptr(), size.value, raw))
     return dx, dw, db
 
 

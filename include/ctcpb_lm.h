@@ -15,7 +15,8 @@
  * stream) and may be captured into a HIP graph.  The return value is CTCPB_OK
  * or an error code (the values of ctcpb.h), described by
  * ctcpb_lm_last_error().  On error nothing was enqueued, except
- * CTCPB_ERR_DEVICE, reported when a launch fails.  Strides are in elements.
+ * CTCPB_ERR_DEVICE, reported when a launch fails.  Each call takes its operands
+ * in a structure that it reads before it returns.  Strides are in elements.
  * Results do not depend on the order in which workgroups run: two calls on the
  * same inputs give the same bits.
  */
@@ -66,23 +67,31 @@ enum {
  * the inputs, so a repeated call on the same inputs gives the same result.
  * num_pages * page_size, with num_pages the largest page id + 1, must be below
  * 2^31. */
-int ctcpb_lm_cache_plan(const int32_t* lengths, const int32_t* counts, int32_t rows,
-                        int32_t* tables, int64_t table_stride, int32_t table_width,
-                        const int32_t* pool, int32_t pool_size, const int32_t* taken,
-                        int32_t page_size, int32_t* slots, int32_t* positions, int32_t capacity,
-                        int32_t* starts, int32_t* out_lengths, int32_t* out_taken,
-                        int32_t* status, void* stream);
+typedef struct {
+  const int32_t *lengths, *counts;
+  int32_t* tables;
+  const int32_t *pool, *taken;
+  int32_t *slots, *positions, *starts, *out_lengths, *out_taken, *status;
+  int64_t table_stride;
+  int32_t rows, table_width, pool_size, page_size, capacity;
+} ctcpb_lm_plan_args;
+int ctcpb_lm_cache_plan(const ctcpb_lm_plan_args* args, void* stream);
 
 /* Give back the pages of the rows with finished[r] != 0 (device uint8 [rows]):
  * they go to pool[out_taken ..] in row order, then page order, and
  * out_taken = taken - (their number).  out_lengths is 0 for these rows,
  * lengths[r] for the others.  Other arguments as ctcpb_lm_cache_plan; out_*
  * must not overlap the inputs. */
-int ctcpb_lm_cache_release(const uint8_t* finished, const int32_t* lengths, int32_t rows,
-                           const int32_t* tables, int64_t table_stride, int32_t table_width,
-                           int32_t* pool, int32_t pool_size, const int32_t* taken,
-                           int32_t page_size, int32_t* out_lengths, int32_t* out_taken,
-                           void* stream);
+typedef struct {
+  const uint8_t* finished;
+  const int32_t *lengths, *tables;
+  int32_t* pool;
+  const int32_t* taken;
+  int32_t *out_lengths, *out_taken;
+  int64_t table_stride;
+  int32_t rows, table_width, pool_size, page_size;
+} ctcpb_lm_release_args;
+int ctcpb_lm_cache_release(const ctcpb_lm_release_args* args, void* stream);
 
 /* A paged cache tensor: element (page, offset, head, d) at
  * data[page*stride_page + offset*stride_token + head*stride_head + d].  The
@@ -98,11 +107,14 @@ typedef struct {
  *            [0, num_pages*page_size) are left out.  Slots are distinct.
  * 16-byte accesses are used where pointers and strides allow, else single
  * elements. */
-int ctcpb_lm_cache_store(int32_t dtype, const void* k, int64_t k_stride_t, int64_t k_stride_h,
-                         const void* v, int64_t v_stride_t, int64_t v_stride_h,
-                         const int32_t* slots, int32_t tokens, const ctcpb_lm_cache* k_cache,
-                         const ctcpb_lm_cache* v_cache, int32_t num_pages, int32_t page_size,
-                         int32_t kv_heads, int32_t head_dim, void* stream);
+typedef struct {
+  const void *k, *v;
+  const int32_t* slots;
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  ctcpb_lm_cache k_cache, v_cache;
+  int32_t dtype, tokens, num_pages, page_size, kv_heads, head_dim;
+} ctcpb_lm_store_args;
+int ctcpb_lm_cache_store(const ctcpb_lm_store_args* args, void* stream);
 
 /* Attention of one token per request over its pages (the token's own key and
  * value stored before).  With t over the last `window` of the request's
@@ -122,16 +134,20 @@ int ctcpb_lm_cache_store(int32_t dtype, const void* k, int64_t k_stride_t, int64
  *   workspace  device, >= ctcpb_lm_attention_workspace bytes, 16-byte aligned;
  *            its contents on entry do not matter; calls that share it must not
  *            overlap.  */
-int ctcpb_lm_attention_workspace(int32_t dtype, int32_t rows, int32_t q_heads, int32_t kv_heads,
-                                 int32_t head_dim, int32_t max_len, int32_t window,
-                                 size_t* out_bytes);
-int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t q_stride_h,
-                       const ctcpb_lm_cache* k_cache, const ctcpb_lm_cache* v_cache,
-                       int32_t num_pages, int32_t page_size, const int32_t* tables,
-                       int64_t table_stride, int32_t table_width, const int32_t* lengths,
-                       int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                       int32_t max_len, int32_t window, float scale, void* out,
-                       int64_t out_stride_r, int64_t out_stride_h, float* lse, void* workspace,
+typedef struct {
+  const void* q;
+  const int32_t *tables, *lengths;
+  void* out;
+  float* lse;
+  int64_t q_stride_r, q_stride_h, out_stride_r, out_stride_h, table_stride;
+  ctcpb_lm_cache k_cache, v_cache;
+  int32_t dtype, rows, q_heads, kv_heads, head_dim, num_pages, page_size, table_width, max_len,
+      window;
+  float scale;
+} ctcpb_lm_attention_args;
+/* Reads no pointer of `args`, only sizes. */
+int ctcpb_lm_attention_workspace(const ctcpb_lm_attention_args* args, size_t* out_bytes);
+int ctcpb_lm_attention(const ctcpb_lm_attention_args* args, void* workspace,
                        size_t workspace_bytes, void* stream);
 
 /* Token losses of an output layer, the vocabulary taken in pieces:
@@ -147,13 +163,17 @@ int ctcpb_lm_attention(int32_t dtype, const void* q, int64_t q_stride_r, int64_t
  * entry do not matter; calls that share it must not overlap.  Its size depends
  * on the addresses and strides of x and w (rows that are not 16-byte aligned
  * are copied to aligned ones there); the size query does not read them. */
-int ctcpb_lm_loss_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
-                            int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
-                            size_t* out_bytes);
-int ctcpb_lm_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w, int64_t stride_w,
-                  const float* bias, const int32_t* targets, int32_t rows, int32_t vocab,
-                  int32_t hidden, float* loss, float* lse, void* workspace,
-                  size_t workspace_bytes, void* stream);
+typedef struct {
+  const void *x, *w;
+  const float* bias;
+  const int32_t* targets;
+  float *loss, *lse;
+  int64_t stride_x, stride_w;
+  int32_t dtype, rows, vocab, hidden;
+} ctcpb_lm_loss_args;
+int ctcpb_lm_loss_workspace(const ctcpb_lm_loss_args* args, size_t* out_bytes);
+int ctcpb_lm_loss(const ctcpb_lm_loss_args* args, void* workspace, size_t workspace_bytes,
+                  void* stream);
 
 /* Gradients of sum_n grad[n] * loss[n], recomputing the probabilities piece by
  * piece from lse:
@@ -166,14 +186,19 @@ int ctcpb_lm_loss(int32_t dtype, const void* x, int64_t stride_x, const void* w,
  *            of them may be NULL and is then not computed.
  * With 16-bit types d is rounded to that type before the products (for f16
  * after a power-of-two scaling that keeps it in range); sums are float32. */
-int ctcpb_lm_loss_grad_workspace(int32_t dtype, const void* x, int64_t stride_x, const void* w,
-                                 int64_t stride_w, int32_t rows, int32_t vocab, int32_t hidden,
-                                 size_t* out_bytes);
-int ctcpb_lm_loss_grad(int32_t dtype, const float* grad, const void* x, int64_t stride_x,
-                       const void* w, int64_t stride_w, const float* bias,
-                       const int32_t* targets, const float* lse, int32_t rows, int32_t vocab,
-                       int32_t hidden, void* dx, void* dw, float* dbias, void* workspace,
-                       size_t workspace_bytes, void* stream);
+typedef struct {
+  const void *x, *w;
+  const float* bias;
+  const int32_t* targets;
+  const float *grad, *lse;
+  void *dx, *dw;
+  float* dbias;
+  int64_t stride_x, stride_w;
+  int32_t dtype, rows, vocab, hidden;
+} ctcpb_lm_grad_args;
+int ctcpb_lm_loss_grad_workspace(const ctcpb_lm_grad_args* args, size_t* out_bytes);
+int ctcpb_lm_loss_grad(const ctcpb_lm_grad_args* args, void* workspace, size_t workspace_bytes,
+                       void* stream);
 
 /* Human-readable description of the last error on this thread ("" if none). */
 const char* ctcpb_lm_last_error(void);
