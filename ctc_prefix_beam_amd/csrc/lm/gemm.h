@@ -65,6 +65,24 @@ struct Operand {
   int32_t rows;
 };
 
+// 64 pieces of 16 bytes, lane l's from base + offset, to lds + l*16 (zeros for
+// offsets outside).  Written as assembly, with no register result, because the
+// compiler makes every transposing LDS read wait for all fetches it knows of; the
+// waits that are needed are those of wait_and_meet().
+__device__ inline void fetch_to_lds(const char* base, char* lds, uint32_t offset) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const u32x4 rsrc = {(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
+  const uint32_t to = (uint32_t)(uintptr_t)(lds_char*)lds;
+  // nothing else in these kernels uses m0 (the warning is about reserved registers)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(to), "v"(offset), "s"(rsrc)
+               : "m0");
+#pragma clang diagnostic pop
+}
+
 // Fetches an R-row tile of an operand into LDS and reads fragments from it.
 // W: waves of the workgroup.
 template <typename T, int R, bool KC, int W>
@@ -74,57 +92,64 @@ struct TileLoader {
   static constexpr int kLoads = R / 8 / W;        // 1 KB loads per wave
   static constexpr int kRow = KC ? 128 : R * (int)sizeof(T);   // bytes of a row in LDS
   static constexpr int kPieces = kRow / 16;
-  static_assert(kLoads * 8 * W == R, "tile and waves do not match");
+  static constexpr int kReads = KC ? 1 : sizeof(T) == 2 ? 2 : 4;   // LDS reads of a fragment
+  static_assert(R >= 64 && kLoads * 8 * W == R, "tile and waves do not match");
   typedef typename Frag<T>::V V;
 
-  const char* base;
-  int64_t step;            // bytes from one k-tile to the next
-  uint32_t off[kLoads];
-  int32_t kpos[kLoads];    // first k of the lane's piece in the tile
+  // A load covers kRows rows of the tile in LDS; its first row is wave-uniform, so a
+  // lane keeps only its row and byte in the first load and derives the others.
+  static constexpr int kRows = 64 / kPieces;
 
-  static __device__ int swizzle(int k) {
-    if constexpr (sizeof(T) == 2)
-      return ((k & 3) | ((k >> 3) & 1) << 2) << 1;
+  const char* base;        // the next tile
+  int64_t ld, step;        // bytes from row to row, from tile to tile
+  int32_t lane_row;
+  uint32_t lane_byte, lane_off;
+  int32_t rows;            // rows (k contiguous) or bytes (m contiguous) left of m
+
+  // Row r of the tile has its piece p at p ^ swizzle(r): bits of r, so that
+  // swizzle(a + b) = swizzle(a) ^ swizzle(b) where a and b share none.
+  static __device__ int swizzle(int r) {
+    if constexpr (KC)
+      return (r >> 1) & 7;
+    else if constexpr (sizeof(T) == 2 && R >= 128)
+      return ((r & 3) | ((r >> 3) & 1) << 2) << 1;
+    else if constexpr (sizeof(T) == 2)   // rows of 128 bytes, two to all the banks
+      return (((r >> 1) & 1) | ((r >> 3) & 1) << 1) << 1;
     else
-      return ((k >> 2) & 3) << 2;
+      return ((r >> 2) & 3) << 2;
   }
 
-  __device__ void init(const Operand& o, int row0, int wave, int lane) {
+  __device__ void init(const Operand& o, int row0, int k0, int lane) {
+    ld = o.ld;
     if constexpr (KC) {
-      base = o.data + row0 * o.ld;
+      base = o.data + row0 * o.ld + (int64_t)k0 * (int)sizeof(T);
       step = 128;
+      rows = o.rows - row0;
     } else {
-      base = o.data + (int64_t)row0 * (int)sizeof(T);
+      base = o.data + k0 * o.ld + (int64_t)row0 * (int)sizeof(T);
       step = kBK * o.ld;
+      rows = min(o.rows - row0, R) * (int)sizeof(T);
     }
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      const int i = (wave * kLoads + q) * 64 + lane;   // piece of the tile
-      const int r = i / kPieces, p = i % kPieces;
-      if constexpr (KC) {
-        const int lp = p ^ ((r >> 1) & 7);
-        kpos[q] = lp * kPer;
-        off[q] = row0 + r < o.rows ? (uint32_t)(r * o.ld + lp * 16) : kOutside;
-      } else {
-        const int lp = p ^ swizzle(r);
-        kpos[q] = r;
-        off[q] = row0 + lp * kPer < o.rows ? (uint32_t)(r * o.ld + lp * 16) : kOutside;
-      }
-    }
+    lane_row = lane / kPieces;
+    lane_byte = (lane % kPieces ^ swizzle(lane_row)) * 16;
+    lane_off = (uint32_t)(lane_row * o.ld);
   }
 
-  // The tile of k0 .. (of K in all) to `lds`; `base` moves on to the next one.
-  __device__ void load(char* lds, int k0, int K, int wave) {
-    const bool whole = k0 + kBK <= K;
-    __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0x7fffffff, 0x00027000);
+  // Starts fetch q of the tile that begins `left` values of k before the operand's
+  // end (0 or less: all zeros).
+  __device__ void fetch(char* lds, int q, int left, int wave) const {
+    const int first = (wave * kLoads + q) * kRows;
+    const uint32_t byte = lane_byte ^ (uint32_t)(swizzle(first) * 16);
+    const int row_end = (KC ? rows : left) - first;
+    const int byte_end = KC ? min(left, kBK) * (int)sizeof(T) : rows;
+    const uint32_t o = lane_row < row_end && (int)byte < byte_end ? lane_off + byte : kOutside;
+    fetch_to_lds(base + first * ld, lds + (wave * kLoads + q) * 1024, o);
+  }
+
+  // The whole tile; `base` moves on to the next one.
+  __device__ void load(char* lds, int left, int wave) {
 #pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      uint32_t o = off[q];
-      if (!whole && k0 + kpos[q] >= K) o = kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (lds_char*)(lds + (wave * kLoads + q) * 1024), 16, o, 0, 0, 0);
-    }
+    for (int q = 0; q < kLoads; ++q) fetch(lds, q, left, wave);
     base += step;
   }
 
@@ -132,7 +157,7 @@ struct TileLoader {
   static __device__ V read(const char* lds, int r0, int kk, int lane) {
     const int g = lane >> 4, c = lane & 15;
     if constexpr (KC) {
-      const int p = (kk * 4 + g) ^ (c >> 1);
+      const int p = (kk * 4 + g) ^ swizzle(c);
       return *reinterpret_cast<const V*>(lds + (r0 + c) * 128 + p * 16);
     } else if constexpr (sizeof(T) == 2) {
       // two transposing reads of four k each: lane i of a group gives the address of
@@ -147,7 +172,7 @@ struct TileLoader {
       return __builtin_bit_cast(V, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       V v;
-      const int p = (r0 / 4 + (c >> 2)) ^ (g << 2);
+      const int p = (r0 / 4 + (c >> 2)) ^ swizzle(g * 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         v[j] = *reinterpret_cast<const float*>(lds + (kk * 16 + g * 4 + j) * kRow + p * 16 +
@@ -161,69 +186,155 @@ struct GemmArgs {
   Operand a, b;
   int32_t K;
   int32_t tiles_m, tiles_n;
+  int32_t splits, part;   // parts of k, and the length of one (a multiple of the k-tile)
 };
 
-// Tile of workgroup `id`: consecutive ids go to the eight XCDs in turn, so each
-// XCD is given a contiguous part of the tiles, walked eight n-tiles wide, to
-// find its operands in its own L2.
-__device__ inline void tile_of(const GemmArgs& a, int id, int* tm, int* tn) {
-  const int total = a.tiles_m * a.tiles_n, per = total / 8;
+// Where work item `id` lies.  Consecutive ids go to the eight XCDs in turn, so
+// each XCD is given a contiguous range of the items, walked eight n-tiles wide,
+// to find its operands in its own L2.
+struct Place {
+  int32_t m, n, split;
+};
+__device__ inline Place place_of(const GemmArgs& a, int id) {
+  const int tiles = a.tiles_m * a.tiles_n, per = tiles * a.splits / 8;
   if (id < per * 8) id = (id % 8) * per + id / 8;
+  Place p;
+  p.split = id / tiles;
+  id -= p.split * tiles;
   const int band = 8 * a.tiles_m;
   const int first = id / band * 8;
   const int wide = min(8, a.tiles_n - first);
-  *tn = first + id % band % wide;
-  *tm = id % band / wide;
+  p.n = first + id % band % wide;
+  p.m = id % band / wide;
+  return p;
 }
 
-// BM x BN per workgroup, WM x WN waves.
+// Waits for this wave's fetches into LDS and its LDS reads, then for the other waves.
+__device__ inline void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The order of the instructions behind it: `reads` LDS reads spread evenly over
+// the first matrix instructions of `macs`; those after them hide the reads' latency.
+template <int reads, int macs>
+__device__ inline void interleave() {
+  constexpr int span = macs > 8 ? macs - 8 : macs;
+#pragma unroll
+  for (int i = 0; i < macs; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+    if (i < span) {
+      const int n = reads * (i + 1) / span - reads * i / span;
+      for (int r = 0; r < n; ++r) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  }
+}
+
+// BM x BN per work item, WM x WN waves.  Workgroups stay for as many items as
+// come to them: an item's first fetches are under way while the one before is
+// finished by the epilogue.
 template <typename T, int BM, int BN, int WM, int WN, bool AKC, bool BKC, typename Epilogue>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs a, Epilogue ep) {
   constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   typedef TileLoader<T, BM, AKC, W> LA;
   typedef TileLoader<T, BN, BKC, W> LB;
+  constexpr int kReads = TM * LA::kReads + TN * LB::kReads;
+  constexpr int kMacs = TM * TN * (sizeof(T) == 2 ? 1 : 4);
+  constexpr int kFetches = LA::kLoads + LB::kLoads;
+  constexpr int kEarly = TM > 2 ? TM / 4 : 1;   // rows of products with the fetches among them
   __shared__ __align__(1024) char lds[2][(BM + BN) * 128];
+  __shared__ float2 scratch[WM * BN];           // the epilogue's
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  int tm, tn;
-  tile_of(a, blockIdx.x, &tm, &tn);
+  const int items = a.tiles_m * a.tiles_n * a.splits;
   LA la;
   LB lb;
-  la.init(a.a, tm * BM, wave, lane);
-  lb.init(a.b, tn * BN, wave, lane);
-  f32x4 acc[TM][TN];
+  Place at = place_of(a, blockIdx.x);
+  int K;                                        // length of the item's part of k
+  const auto begin = [&] {
+    const int k0 = at.split * a.part;
+    K = min(a.part, a.K - k0);
+    la.init(a.a, at.m * BM, k0, lane);
+    lb.init(a.b, at.n * BN, k0, lane);
+    la.load(lds[0], K, wave);
+    lb.load(lds[0] + BM * 128, K, wave);
+    la.load(lds[1], K - LA::kBK, wave);
+    lb.load(lds[1] + BM * 128, K - LA::kBK, wave);
+  };
+  begin();
+  for (int id = blockIdx.x; id < items;) {
+    f32x4 acc[TM][TN];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  la.load(lds[0], 0, a.K, wave);
-  lb.load(lds[0] + BM * 128, 0, a.K, wave);
-  __syncthreads();
-  int cur = 0;
-  for (int k0 = 0; k0 < a.K; k0 += LA::kBK) {
-    if (k0 + LA::kBK < a.K) {
-      la.load(lds[cur ^ 1], k0 + LA::kBK, a.K, wave);
-      lb.load(lds[cur ^ 1] + BM * 128, k0 + LA::kBK, a.K, wave);
-    }
-    const char *ta = lds[cur], *tb = lds[cur] + BM * 128;
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    // Fragments are read half a k-tile ahead of their products, and tiles fetched one and a
+    // half ahead, so that the matrix unit has work across the barrier: at it, a wave has
+    // read all of the current tile (its buffer may be overwritten) and the next has arrived.
+    const int steps = (K + LA::kBK - 1) / LA::kBK;
+    typename Frag<T>::V fa[2][TM], fb[2][TN];
+    wait_and_meet();
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      typename Frag<T>::V fa[TM], fb[TN];
+    for (int i = 0; i < TM; ++i) fa[0][i] = LA::read(lds[0], (wm * TM + i) * 16, 0, lane);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = LA::read(ta, (wm * TM + i) * 16, kk, lane);
+    for (int j = 0; j < TN; ++j)
+      fb[0][j] = LB::read(lds[0] + BM * 128, (wn * TN + j) * 16, 0, lane);
+    for (int s = 0; s < steps; ++s) {
+      char* now = lds[s & 1];
+      char* next = lds[(s & 1) ^ 1];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = LB::read(tb, (wn * TN + j) * 16, kk, lane);
+      for (int i = 0; i < TM; ++i) fa[1][i] = LA::read(now, (wm * TM + i) * 16, 1, lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fb[1][j] = LB::read(now + BM * 128, (wn * TN + j) * 16, 1, lane);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = Frag<T>::mac(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < TN; ++j) acc[i][j] = Frag<T>::mac(fa[0][i], fb[0][j], acc[i][j]);
+      interleave<kReads, kMacs>();
+      __builtin_amdgcn_sched_barrier(0);
+      wait_and_meet();
+      const int left = K - (s + 2) * LA::kBK;
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          acc[i][j] = Frag<T>::mac(fa[1][i], fb[1][j], acc[i][j]);
+#pragma unroll
+          for (int q = (i * TN + j) * kFetches / (kEarly * TN);
+               q < (i * TN + j + 1) * kFetches / (kEarly * TN); ++q) {
+            if (q < LA::kLoads)
+              la.fetch(now, q, left, wave);
+            else
+              lb.fetch(now + BM * 128, q - LA::kLoads, left, wave);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      la.base += la.step;
+      lb.base += lb.step;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) fa[0][i] = LA::read(next, (wm * TM + i) * 16, 0, lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        fb[0][j] = LB::read(next + BM * 128, (wn * TN + j) * 16, 0, lane);
+#pragma unroll
+      for (int i = kEarly; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = Frag<T>::mac(fa[1][i], fb[1][j], acc[i][j]);
+      interleave<kReads, kMacs - kEarly * TN * (sizeof(T) == 2 ? 1 : 4)>();
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
-    cur ^= 1;
+    wait_and_meet();   // nothing is on its way, and nobody reads the buffers
+    const Place done = at;
+    id += gridDim.x;
+    if (id < items) {
+      at = place_of(a, id);
+      begin();
+    }
+    // sums acc[i][j][r]: m = done.m*BM + (wm*TM + i)*16 + (lane>>4)*4 + r,
+    //                    n = done.n*BN + (wn*TN + j)*16 + (lane&15)
+    ep.template run<TM, TN, WM, WN>(acc, done, wm, wn, lane, scratch);
   }
-  // sums acc[i][j][r]: m = tm*BM + (wm*TM + i)*16 + (lane>>4)*4 + r, n = tn*BN + (wn*TN + j)*16 + (lane&15)
-  ep.template run<TM, TN, WM, WN>(acc, tm, tn, wm, wn, lane, lds[0]);
 }
 
 }  // namespace ctcpb_lm

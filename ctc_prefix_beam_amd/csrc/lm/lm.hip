@@ -163,17 +163,77 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 // ------------------------------------------------------------------ loss --
 
 constexpr size_t kPieceBytes = (size_t)256 << 20;   // workspace for d at a time
-constexpr int kTile = 128;                          // tokens and vocabulary rows of a tile
+
+// How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
+struct TileShape {
+  int bm, bn, wn;   // wn: waves along n (dbias sums per token tile)
+};
+enum { kSmall = 0, kMiddle = 1, kLarge = 2 };
+constexpr TileShape kShapes[3] = {{64, 64, 2}, {128, 128, 2}, {256, 256, 4}};
+constexpr int kResident[3] = {4, 2, 1};   // workgroups that share a CU
+constexpr int kCUs = 256;
+
+struct Cut {
+  int shape;
+  int32_t tiles_m, tiles_n, splits, part;
+};
+
+int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b); }
 
 size_t up(size_t v, size_t n) { return (v + n - 1) / n * n; }
+
+// Estimated time (us) of a cut.  What decides is how well the tiles feed the
+// matrix units against how evenly the items fill the CUs.  Measured with bf16 and
+// f32 on products of 10^8 to 10^12 multiplications, for each shape: the time that
+// a k-tile of an item takes of its CU when CUs are full (`unit`; 256x256: 1430
+// TFLOP/s with bf16, 145 with f32), and when the item is alone on it (`alone`: its
+// fetches' latency), and a launch's beginning and end (`ends`).
+double cut_time(int es, const Cut& c, int64_t m, int64_t n) {
+  constexpr double unit[2][3] = {{0.225, 0.56, 1.5}, {0.56, 2.05, 7.4}};
+  constexpr double alone[2][3] = {{0.45, 0.73, 1.5}, {0.73, 2.28, 7.4}};
+  constexpr double ends[3] = {2.5, 5.0, 8.0};
+  const int type = es == 4;
+  const int64_t items = (int64_t)c.tiles_m * c.tiles_n * c.splits;
+  const int64_t slots = kCUs * kResident[c.shape], rest = items % slots;
+  const auto round = [&](int64_t shared) {   // one item each for `shared` workgroups of a CU
+    const double full = (double)shared * unit[type][c.shape], one = alone[type][c.shape];
+    return (full > one ? full : one) * (c.part * es / 128.0) + 2.5;
+  };
+  double time = ends[c.shape] + (double)(items / slots) * round(kResident[c.shape]);
+  if (rest) time += round((rest + kCUs - 1) / kCUs);
+  // planes are written, and read and added by a launch of its own
+  if (c.splits > 1) time += 4.5 + (double)c.splits * m * n * 8 / 3.3e6;
+  return time;
+}
+
+// The cut of an m x n x K product; only those with `split` may divide k (what
+// they leave are sums that can be added).
+Cut choose_cut(int es, int64_t m, int64_t n, int64_t K, bool split) {
+  const int64_t bk = 128 / es;
+  Cut best{};
+  double least = 0;
+  for (int shape = kSmall; shape <= kLarge; ++shape)
+    for (int splits = 1; splits <= (split ? 16 : 1); ++splits) {
+      Cut c{shape, ceil_div(m, kShapes[shape].bm), ceil_div(n, kShapes[shape].bn), splits, 0};
+      c.part = (int32_t)(ceil_div(ceil_div(K, splits), bk) * bk);
+      if (c.part < bk) c.part = (int32_t)bk;   // K = 0: one empty part
+      c.splits = K > 0 ? ceil_div(K, c.part) : 1;
+      const double t = cut_time(es, c, m, n);
+      if (best.part == 0 || t < least) {
+        best = c;
+        least = t;
+      }
+    }
+  return best;
+}
 
 // Sizes and workspace offsets of a loss or gradient call.
 struct LossPlan {
   int es, padded;          // padded: hidden up to 16 bytes
   bool pad_x, pad_w;       // rows to be copied to aligned ones
-  int32_t tiles_v, tiles_n;
   int32_t piece, pieces;   // gradient: vocabulary rows at a time
-  size_t o_x, o_w, o_part, o_hit, o_d, o_sums, o_bias, o_scale, bytes;
+  Cut logits, dx, dw;      // of a whole piece
+  size_t o_x, o_w, o_part, o_hit, o_d, o_sums, o_planes, o_bias, o_scale, bytes;
 };
 
 bool row_aligned(const void* p, int64_t stride, int es) {
@@ -190,8 +250,6 @@ LossPlan plan_loss(const Args& g, bool grad) {
   // a row is read up to its last 16 bytes
   p.pad_x = p.padded != hidden || !row_aligned(g.x, g.stride_x, p.es);
   p.pad_w = p.padded != hidden || !row_aligned(g.w, g.stride_w, p.es);
-  p.tiles_v = (vocab + kTile - 1) / kTile;
-  p.tiles_n = (rows + kTile - 1) / kTile;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -201,18 +259,25 @@ LossPlan plan_loss(const Args& g, bool grad) {
   if (p.pad_x) p.o_x = take((size_t)rows * p.padded * p.es);
   if (p.pad_w) p.o_w = take((size_t)vocab * p.padded * p.es);
   if (!grad) {
-    p.o_part = take((size_t)p.tiles_v * rows * sizeof(float2));
+    p.logits = choose_cut(p.es, vocab, rows, p.padded, false);
+    p.o_part = take((size_t)p.logits.tiles_m * rows * sizeof(float2));
     p.o_hit = take((size_t)rows * sizeof(float));
   } else {
-    const size_t most = kPieceBytes / ((size_t)(rows ? rows : 1) * p.es) / kTile * kTile;
-    const size_t all = up(vocab, kTile);
-    size_t piece = most < kTile ? kTile : most < all ? most : all;
-    p.pieces = (int32_t)((all + piece - 1) / piece);
-    p.piece = (int32_t)up((all + p.pieces - 1) / p.pieces, kTile);   // of about the same size
-    p.pieces = (int32_t)((all + p.piece - 1) / p.piece);             // none empty
+    const size_t unit = 256;   // vocabulary rows of a piece: whole tiles of any shape
+    const size_t most = kPieceBytes / ((size_t)(rows ? rows : 1) * p.es) / unit * unit;
+    const size_t all = up(vocab, unit);
+    p.pieces = (int32_t)ceil_div(all, most < unit ? unit : most < all ? most : all);
+    p.piece = (int32_t)up(ceil_div(all, p.pieces), unit);   // of about the same size
+    p.pieces = ceil_div(all, p.piece);                      // none empty
+    p.logits = choose_cut(p.es, p.piece, rows, p.padded, false);
+    p.dx = choose_cut(p.es, hidden, rows, p.piece, true);
+    p.dw = choose_cut(p.es, hidden, p.piece, rows, true);
     p.o_d = take((size_t)rows * p.piece * p.es);
     if (p.pieces > 1) p.o_sums = take((size_t)rows * hidden * sizeof(float));
-    p.o_bias = take((size_t)p.tiles_n * 2 * vocab * sizeof(float));
+    const size_t px = p.dx.splits > 1 ? (size_t)p.dx.splits * rows * hidden : 0;
+    const size_t pw = p.dw.splits > 1 ? (size_t)p.dw.splits * p.piece * hidden : 0;
+    p.o_planes = take((px > pw ? px : pw) * sizeof(float));
+    p.o_bias = take((size_t)p.logits.tiles_n * kShapes[p.logits.shape].wn * vocab * sizeof(float));
     p.o_scale = take(2 * sizeof(float));
   }
   p.bytes = at;
@@ -228,8 +293,8 @@ int check_loss(const Args& g) {
     return fail(CTCPB_ERR_INVALID, "stride_x and stride_w must be >= hidden");
   if (g.hidden > 1 << 20 || g.vocab > 1 << 30 || g.rows > 1 << 30)
     return fail(CTCPB_ERR_UNSUPPORTED, "hidden above 2^20, or vocab or rows above 2^30");
-  const int64_t tiles = ((int64_t)g.vocab + kTile - 1) / kTile * ((g.rows + kTile - 1) / kTile);
-  if (tiles > INT_MAX) return fail(CTCPB_ERR_UNSUPPORTED, "too many tiles for one launch");
+  if ((int64_t)ceil_div(g.vocab, 64) * ceil_div(g.rows, 64) > INT_MAX)
+    return fail(CTCPB_ERR_UNSUPPORTED, "too many tiles for one launch");
   return CTCPB_OK;
 }
 
@@ -249,12 +314,39 @@ Operand aligned_rows(const void* data, int64_t stride, int32_t rows, int32_t hid
   return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows};
 }
 
+template <typename T, int BM, int BN, int WM, int WN, bool AKC, bool BKC, typename Epilogue>
+void launch_tiles(const GemmArgs& g, const Epilogue& ep, int resident, hipStream_t st) {
+  const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits, slots = kCUs * resident;
+  gemm_kernel<T, BM, BN, WM, WN, AKC, BKC, Epilogue>
+      <<<(unsigned)(items < slots ? items : slots), 64 * WM * WN, 0, st>>>(g, ep);
+}
+
+// The product of a and b, a of `m` rows and b of `n`, cut as `c` (whose tile
+// counts may be those of a larger product of the same kind).
 template <typename T, bool AKC, bool BKC, typename Epilogue>
-void launch_gemm(const Operand& a, const Operand& b, int32_t m, int32_t n, int32_t K,
+void launch_gemm(const Operand& a, const Operand& b, int64_t m, int64_t n, int32_t K, const Cut& c,
                  const Epilogue& ep, hipStream_t st) {
-  const GemmArgs g{a, b, K, (m + kTile - 1) / kTile, (n + kTile - 1) / kTile};
-  gemm_kernel<T, kTile, kTile, 2, 2, AKC, BKC, Epilogue>
-      <<<(unsigned)(g.tiles_m * g.tiles_n), 256, 0, st>>>(g, ep);
+  const GemmArgs g{a,
+                   b,
+                   K,
+                   ceil_div(m, kShapes[c.shape].bm),
+                   ceil_div(n, kShapes[c.shape].bn),
+                   K > 0 ? ceil_div(K, c.part) : 1,
+                   c.part};
+  if (c.shape == kLarge)
+    launch_tiles<T, 256, 256, 2, 4, AKC, BKC>(g, ep, kResident[kLarge], st);
+  else if (c.shape == kMiddle)
+    launch_tiles<T, 128, 128, 2, 2, AKC, BKC>(g, ep, kResident[kMiddle], st);
+  else
+    launch_tiles<T, 64, 64, 2, 2, AKC, BKC>(g, ep, kResident[kSmall], st);
+}
+
+template <typename T>
+void launch_planes(const float* planes, int32_t count, int64_t n, const float* before, float* sums,
+                   T* out, const float* scale, hipStream_t st) {
+  const int64_t blocks = (n + 255) / 256;
+  planes_kernel<T><<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
+      planes, count, n, before, sums, out, scale);
 }
 
 template <typename T>
@@ -266,9 +358,9 @@ void run_loss(const LossPlan& p, const ctcpb_lm_loss_args& g, char* ws, hipStrea
   float2* part = reinterpret_cast<float2*>(ws + p.o_part);
   float* hit = reinterpret_cast<float*>(ws + p.o_hit);
   const ForwardEpilogue ep{Logits{g.bias, g.targets, g.rows, g.vocab, 0}, part, hit};
-  launch_gemm<T, true, true>(w, x, g.vocab, g.rows, p.padded, ep, st);
+  launch_gemm<T, true, true>(w, x, g.vocab, g.rows, p.padded, p.logits, ep, st);
   loss_join_kernel<<<(unsigned)((g.rows + 31) / 32), 256, 0, st>>>(
-      part, hit, g.targets, g.rows, g.vocab, p.tiles_v, g.loss, g.lse);
+      part, hit, g.targets, g.rows, g.vocab, p.logits.tiles_m, g.loss, g.lse);
 }
 
 template <typename T>
@@ -278,7 +370,8 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
   const Operand w =
       aligned_rows<T>(g.w, g.stride_w, g.vocab, g.hidden, p, p.pad_w, ws + p.o_w, st);
   T* d = reinterpret_cast<T*>(ws + p.o_d);
-  float* sums = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.o_sums) : nullptr;
+  float* sums = reinterpret_cast<float*>(ws + p.o_sums);
+  float* planes = reinterpret_cast<float*>(ws + p.o_planes);
   float* part = g.dbias ? reinterpret_cast<float*>(ws + p.o_bias) : nullptr;
   float* scale = nullptr;
   if (std::is_same<T, _Float16>::value) {
@@ -292,25 +385,34 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
     const Operand wp{w.data + v0 * w.ld, w.ld, nv};
     const GradEpilogue<T> ge{Logits{g.bias, g.targets, g.rows, g.vocab, v0}, g.grad, g.lse, scale,
                              d, p.piece, part};
-    if (g.rows) launch_gemm<T, true, true>(wp, x, nv, g.rows, p.padded, ge, st);
+    if (g.rows) launch_gemm<T, true, true>(wp, x, nv, g.rows, p.padded, p.logits, ge, st);
     if (g.dx && g.rows) {
       // out[token, h]: m = h, n = token, k = vocabulary
       const Operand a{wp.data, wp.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, g.rows};
-      const OutEpilogue<T> oe{static_cast<T*>(g.dx), sums, scale, g.hidden, g.rows, k == 0,
-                              k == p.pieces - 1};
-      launch_gemm<T, false, true>(a, b, g.hidden, g.rows, nv, oe, st);
+      T* dx = static_cast<T*>(g.dx);
+      const bool by_planes = p.dx.splits > 1, last = k == p.pieces - 1;
+      const OutEpilogue<T> oe{dx,       sums,   by_planes ? planes : nullptr, scale,
+                              g.hidden, g.rows, k && !by_planes,              last};
+      launch_gemm<T, false, true>(a, b, g.hidden, g.rows, nv, p.dx, oe, st);
+      if (by_planes)
+        launch_planes<T>(planes, ceil_div(nv, p.dx.part), (int64_t)g.rows * g.hidden,
+                         k ? sums : nullptr, last ? nullptr : sums, dx, scale, st);
     }
     if (g.dw) {
       // out[v, h]: m = h, n = v, k = token
       const Operand a{x.data, x.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, nv};
-      const OutEpilogue<T> oe{static_cast<T*>(g.dw) + (int64_t)v0 * g.hidden, nullptr, scale,
-                              g.hidden, nv, true, true};
-      launch_gemm<T, false, false>(a, b, g.hidden, nv, g.rows, oe, st);
+      T* dw = static_cast<T*>(g.dw) + (int64_t)v0 * g.hidden;
+      const OutEpilogue<T> oe{dw,       nullptr, p.dw.splits > 1 ? planes : nullptr, scale,
+                              g.hidden, nv,      false,                              true};
+      launch_gemm<T, false, false>(a, b, g.hidden, nv, g.rows, p.dw, oe, st);
+      if (p.dw.splits > 1)
+        launch_planes<T>(planes, p.dw.splits, (int64_t)nv * g.hidden, nullptr, nullptr, dw, scale,
+                         st);
     }
   }
   if (g.dbias)
-    dbias_kernel<<<(unsigned)((g.vocab + 255) / 256), 256, 0, st>>>(part, p.tiles_n * 2, g.vocab,
-                                                                    g.dbias);
+    dbias_kernel<<<(unsigned)((g.vocab + 255) / 256), 256, 0, st>>>(
+        part, g.rows ? p.logits.tiles_n * kShapes[p.logits.shape].wn : 0, g.vocab, g.dbias);
 }
 
 }  // namespace

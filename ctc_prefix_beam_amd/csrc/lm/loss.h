@@ -22,39 +22,58 @@ struct Logits {
   int32_t v0;               // first vocabulary row of the launch
 };
 
+// Adds the bias of a wave's rows vb + i*16 + r (past the vocabulary: nothing).
+template <int TM, int TN>
+__device__ inline void add_bias(f32x4 (&acc)[TM][TN], const Logits& lg, int vb) {
+  if (!lg.bias) return;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int v = vb + i * 16 + r;
+      const float b = v < lg.vocab ? lg.bias[v] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j][r] += b;
+    }
+}
+
 struct ForwardEpilogue {
   Logits lg;
   float2* part;             // [vocabulary tile][token]: maximum, sum of exp(logit - maximum)
   float* hit;               // [token]: logit of the target
 
   template <int TM, int TN, int WM, int WN>
-  __device__ void run(f32x4 (&acc)[TM][TN], int tm, int tn, int wm, int wn, int lane, char* lds) {
+  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane,
+                      float2* red) {
     constexpr int BN = WN * TN * 16;
     const int g = lane >> 4, c = lane & 15;
-    const int vb = (tm * WM + wm) * TM * 16 + g * 4;
-    float2* red = reinterpret_cast<float2*>(lds);   // [WM][BN]; the tiles are done with
+    const int vb = (at.m * WM + wm) * TM * 16 + g * 4;
+    add_bias<TM, TN>(acc, lg, vb);
+    if ((at.m * WM + wm + 1) * TM * 16 > lg.vocab) {   // rows past the vocabulary
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int v = vb + i * 16 + r;
-        const bool in = v < lg.vocab;
-        const float b = in && lg.bias ? lg.bias[v] : 0.0f;
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j][r] = in ? acc[i][j][r] + b : neg_inf();
-      }
+          for (int j = 0; j < TN; ++j)
+            if (vb + i * 16 + r >= lg.vocab) acc[i][j][r] = neg_inf();
+    }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = tn * BN + (wn * TN + j) * 16 + c;
+      const int n = at.n * BN + (wn * TN + j) * 16 + c;
       const int t = n < lg.tokens ? lg.targets[n] : -1;
+      if (__any(t >= vb && t < vb + TM * 16 && t < lg.vocab)) {   // few tiles have a target
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (vb + i * 16 + r == t && t < lg.vocab) hit[n] = acc[i][j][r];
+      }
       float m = neg_inf();
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          m = fmaxf(m, acc[i][j][r]);
-          if (vb + i * 16 + r == t && t < lg.vocab) hit[n] = acc[i][j][r];
-        }
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
       m = max_over_groups(m);
       const float m0 = m == neg_inf() ? 0.0f : m;
       float s = 0.0f;
@@ -67,13 +86,13 @@ struct ForwardEpilogue {
     }
     __syncthreads();
     for (int k = threadIdx.x; k < BN; k += 64 * WM * WN) {
-      const int n = tn * BN + k;
+      const int n = at.n * BN + k;
       if (n >= lg.tokens) continue;
       float m = neg_inf(), s = 0.0f;
       for (int w = 0; w < WM; ++w) m = fmaxf(m, red[w * BN + k].x);
       const float m0 = m == neg_inf() ? 0.0f : m;
       for (int w = 0; w < WM; ++w) s += red[w * BN + k].y * exp_fast(red[w * BN + k].x - m0);
-      part[(int64_t)tm * lg.tokens + n] = float2{m, s};
+      part[(int64_t)at.m * lg.tokens + n] = float2{m, s};
     }
   }
 };
@@ -118,36 +137,46 @@ struct GradEpilogue {
   float* dbias_part;        // [token tile and wave][vocab], or null
 
   template <int TM, int TN, int WM, int WN>
-  __device__ void run(f32x4 (&acc)[TM][TN], int tm, int tn, int wm, int wn, int lane, char*) {
+  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*) {
     constexpr int BN = WN * TN * 16;
+    typedef T T4 __attribute__((ext_vector_type(4)));
     const int g = lane >> 4, c = lane & 15;
-    const int vl = (tm * WM + wm) * TM * 16 + g * 4;   // in the piece
+    const int vl = (at.m * WM + wm) * TM * 16 + g * 4;   // in the piece
+    const int vb = lg.v0 + vl;
     const float sc = scale ? scale[0] : 1.0f;
-    f32x4 sum[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) sum[i] = f32x4{0, 0, 0, 0};
+    add_bias<TM, TN>(acc, lg, vb);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = tn * BN + (wn * TN + j) * 16 + c;
+      const int n = at.n * BN + (wn * TN + j) * 16 + c;
       const bool live = n < lg.tokens;
       const int t = live ? lg.targets[n] : -1;
       const bool in = t >= 0 && t < lg.vocab;
-      const float gn = in ? grad[n] : 0.0f, ln = in ? lse[n] : 0.0f;
+      // a row without a target: exp(logit - inf) = 0
+      const float gn = in ? grad[n] : 0.0f, ln = in ? lse[n] : __builtin_huge_valf();
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        T out[4];
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int v = lg.v0 + vl + i * 16 + r;
-          const float b = v < lg.vocab && lg.bias ? lg.bias[v] : 0.0f;
-          float p = exp_of<T>(acc[i][j][r] + b - ln);
-          p = in && v < lg.vocab ? gn * (v == t ? p - 1.0f : p) : 0.0f;
-          sum[i][r] += p;
-          out[r] = (T)(p * sc);
-        }
-        if (live) {
-          typedef T T4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<T4*>(d + n * ldd + vl + i * 16) = T4{out[0], out[1], out[2], out[3]};
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = gn * exp_of<T>(acc[i][j][r] - ln);
+      if (__any(in && t >= vb && t < vb + TM * 16)) {   // few tiles have a target
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (in && vb + i * 16 + r == t) acc[i][j][r] -= gn;
+      }
+      if (vb + TM * 16 > lg.vocab) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (vb + i * 16 + r >= lg.vocab) acc[i][j][r] = 0.0f;
+      }
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const f32x4 v = acc[i][j] * sc;
+          *reinterpret_cast<T4*>(d + n * ldd + vl + i * 16) =
+              T4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
         }
       }
     }
@@ -156,10 +185,12 @@ struct GradEpilogue {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float s = sum[i][r];
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) s += acc[i][j][r];   // rows past the tokens are 0
         for (int x = 1; x < 16; x <<= 1) s += __shfl_xor(s, x);
-        const int v = lg.v0 + vl + i * 16 + r;
-        if (c == 0 && v < lg.vocab) dbias_part[(int64_t)(tn * WN + wn) * lg.vocab + v] = s;
+        const int v = vb + i * 16 + r;
+        if (c == 0 && v < lg.vocab) dbias_part[(int64_t)(at.n * WN + wn) * lg.vocab + v] = s;
       }
   }
 };
@@ -173,56 +204,77 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* part, int32_t p
   dbias[v] = s;
 }
 
-// out[n, m] (m contiguous) from the sums, which over several launches are added
-// up in `sums` (float32) and rounded by the last one.
+// Where the sums of a launch go: out[n, m] (m contiguous), rounded, or float32
+// `sums`, added to what earlier pieces of the vocabulary left there (`add`);
+// with k in parts, each part's sums to its own [N][M] plane.
 template <typename T>
 struct OutEpilogue {
   T* out;
-  float* sums;              // [N][M], null when one launch does it all
+  float *sums, *planes;     // or null
   const float* scale;       // f16: what d was multiplied by
   int32_t M, N;
-  bool first, last;
+  bool add, last;           // sums hold something; the result goes to `out`
 
   template <int TM, int TN, int WM, int WN>
-  __device__ void run(f32x4 (&acc)[TM][TN], int tm, int tn, int wm, int wn, int lane, char*) {
+  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*) {
     constexpr int BN = WN * TN * 16;
-    const int g = lane >> 4, c = lane & 15;
-    const int mb = (tm * WM + wm) * TM * 16 + g * 4;
-    const float inv = scale ? scale[1] : 1.0f;
     typedef T T4 __attribute__((ext_vector_type(4)));
+    const int g = lane >> 4, c = lane & 15;
+    const int mb = (at.m * WM + wm) * TM * 16 + g * 4;
+    const float inv = scale ? scale[1] : 1.0f;
+    float* f = planes ? planes + (int64_t)at.split * N * M : last ? nullptr : sums;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = tn * BN + (wn * TN + j) * 16 + c;
+      const int n = at.n * BN + (wn * TN + j) * 16 + c;
       if (n >= N) continue;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const int m = mb + i * 16;
-        const int64_t at = (int64_t)n * M + m;
-        if (M % 4 == 0) {   // rows start 4-element aligned: whole or not at all
+        const int64_t to = (int64_t)n * M + m;
+        if (M % 4 == 0) {   // rows start 4-element aligned: four values or none
           if (m >= M) continue;
           f32x4 v = acc[i][j];
-          if (!first) v += *reinterpret_cast<const f32x4*>(sums + at);
-          if (!last) {
-            *reinterpret_cast<f32x4*>(sums + at) = v;
+          if (add) v += *reinterpret_cast<const f32x4*>(sums + to);
+          if (f) {
+            *reinterpret_cast<f32x4*>(f + to) = v;
           } else {
             v *= inv;
-            *reinterpret_cast<T4*>(out + at) = T4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+            *reinterpret_cast<T4*>(out + to) = T4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
           }
         } else {
+#pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if (m + r >= M) break;
-            float v = acc[i][j][r];
-            if (!first) v += sums[at + r];
-            if (!last)
-              sums[at + r] = v;
+            if (m + r >= M) continue;
+            const float v = acc[i][j][r] + (add ? sums[to + r] : 0.0f);
+            if (f)
+              f[to + r] = v;
             else
-              out[at + r] = (T)(v * inv);
+              out[to + r] = (T)(v * inv);
           }
         }
       }
     }
   }
 };
+
+// Adds `count` planes of n values, in their order, to `sums` (if not null: what
+// earlier pieces of the vocabulary left there) and leaves the result in `sums` or,
+// rounded, in `out`.
+template <typename T>
+__global__ __launch_bounds__(256) void planes_kernel(const float* planes, int32_t count, int64_t n,
+                                                     const float* before, float* sums, T* out,
+                                                     const float* scale) {
+  const float inv = scale ? scale[1] : 1.0f;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    float v = before ? before[i] : 0.0f;
+    for (int p = 0; p < count; ++p) v += planes[p * n + i];
+    if (sums)
+      sums[i] = v;
+    else
+      out[i] = (T)(v * inv);
+  }
+}
 
 // f16 only: a power of two that brings the largest |grad| of a row with a
 // target to 2^11..2^12, so that d (at most |grad|) neither overflows nor loses
