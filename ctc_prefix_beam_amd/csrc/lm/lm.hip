@@ -2,6 +2,7 @@
 // include/ctcpb_lm.h).
 #include "ctcpb_lm.h"
 
+#include <algorithm>
 #include <climits>
 #include <exception>
 #include <string>
@@ -162,7 +163,7 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 
 // ------------------------------------------------------------------ loss --
 
-constexpr size_t kPieceBytes = (size_t)256 << 20;   // workspace for d at a time
+constexpr size_t kPieceBytes = (size_t)512 << 20;   // workspace for d at a time
 
 // How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
 struct TileShape {
@@ -208,13 +209,16 @@ double cut_time(int es, const Cut& c, int64_t m, int64_t n) {
 
 // The cut of an m x n x K product; only those with `split` may divide k (what
 // they leave are sums that can be added).
-Cut choose_cut(int es, int64_t m, int64_t n, int64_t K, bool split) {
+Cut choose_cut(int es, int64_t m, int64_t n, int64_t K, bool split, double* time = nullptr) {
   const int64_t bk = 128 / es;
   Cut best{};
   double least = 0;
-  for (int shape = kSmall; shape <= kLarge; ++shape)
-    for (int splits = 1; splits <= (split ? 16 : 1); ++splits) {
-      Cut c{shape, ceil_div(m, kShapes[shape].bm), ceil_div(n, kShapes[shape].bn), splits, 0};
+  for (int shape = kSmall; shape <= kLarge; ++shape) {
+    const int32_t tm = ceil_div(m, kShapes[shape].bm), tn = ceil_div(n, kShapes[shape].bn);
+    // parts of k fill a last round at most when there are many tiles
+    const int most = !split ? 1 : (int64_t)tm * tn >= 1024 ? 2 : 16;
+    for (int splits = 1; splits <= most; ++splits) {
+      Cut c{shape, tm, tn, splits, 0};
       c.part = (int32_t)(ceil_div(ceil_div(K, splits), bk) * bk);
       if (c.part < bk) c.part = (int32_t)bk;   // K = 0: one empty part
       c.splits = K > 0 ? ceil_div(K, c.part) : 1;
@@ -224,7 +228,48 @@ Cut choose_cut(int es, int64_t m, int64_t n, int64_t K, bool split) {
         least = t;
       }
     }
+  }
+  if (time) *time = least;
   return best;
+}
+
+// The products of a gradient for one piece of the vocabulary.
+struct PieceCuts {
+  Cut logits, dx, dw;
+  double time;
+};
+PieceCuts choose_piece(int es, int64_t rows, int64_t vocab, int64_t hidden) {
+  PieceCuts c;
+  double t[3];
+  c.logits = choose_cut(es, vocab, rows, hidden, false, &t[0]);
+  c.dx = choose_cut(es, hidden, rows, vocab, true, &t[1]);
+  c.dw = choose_cut(es, hidden, vocab, rows, true, &t[2]);
+  c.time = t[0] + t[1] + t[2] + 8.0 * rows * hidden / 4e6;   // sums of dx between pieces
+  return c;
+}
+
+// Vocabulary rows of a piece, in whole tiles of any shape: all where d fits the
+// workspace, else the size whose pieces fill the CUs best (of 24 from half of the
+// largest up; at 8192 x 50000 x 2048 pieces of 24576 take 0.87 of the time of four
+// of 12544, estimated).
+int32_t choose_piece_rows(int es, int64_t rows, int64_t vocab, int64_t hidden) {
+  const int64_t unit = 256, all = ceil_div(vocab, unit);
+  int64_t most = kPieceBytes / ((rows ? rows : 1) * es) / unit;
+  if (most >= all) return (int32_t)(all * unit);
+  if (most < 1) most = 1;
+  int64_t best = most;
+  double least = 0;
+  for (int64_t k = 0; k < 24; ++k) {
+    const int64_t u = most - k * most / 48, n = all / u;
+    const int64_t tail = vocab - n * u * unit;
+    double t = n * choose_piece(es, rows, u * unit, hidden).time;
+    if (tail > 0) t += choose_piece(es, rows, tail, hidden).time;
+    if (k == 0 || t < least) {
+      best = u;
+      least = t;
+    }
+  }
+  return (int32_t)(best * unit);
 }
 
 // Sizes and workspace offsets of a loss or gradient call.
@@ -232,7 +277,8 @@ struct LossPlan {
   int es, padded;          // padded: hidden up to 16 bytes
   bool pad_x, pad_w;       // rows to be copied to aligned ones
   int32_t piece, pieces;   // gradient: vocabulary rows at a time
-  Cut logits, dx, dw;      // of a whole piece
+  Cut logits;              // forward
+  PieceCuts whole, tail;   // gradient: a whole piece, and the last one
   size_t o_x, o_w, o_part, o_hit, o_d, o_sums, o_planes, o_bias, o_scale, bytes;
 };
 
@@ -263,21 +309,20 @@ LossPlan plan_loss(const Args& g, bool grad) {
     p.o_part = take((size_t)p.logits.tiles_m * rows * sizeof(float2));
     p.o_hit = take((size_t)rows * sizeof(float));
   } else {
-    const size_t unit = 256;   // vocabulary rows of a piece: whole tiles of any shape
-    const size_t most = kPieceBytes / ((size_t)(rows ? rows : 1) * p.es) / unit * unit;
-    const size_t all = up(vocab, unit);
-    p.pieces = (int32_t)ceil_div(all, most < unit ? unit : most < all ? most : all);
-    p.piece = (int32_t)up(ceil_div(all, p.pieces), unit);   // of about the same size
-    p.pieces = ceil_div(all, p.piece);                      // none empty
-    p.logits = choose_cut(p.es, p.piece, rows, p.padded, false);
-    p.dx = choose_cut(p.es, hidden, rows, p.piece, true);
-    p.dw = choose_cut(p.es, hidden, p.piece, rows, true);
+    p.piece = choose_piece_rows(p.es, rows, vocab, p.padded);
+    p.pieces = ceil_div(vocab, p.piece);
+    p.whole = choose_piece(p.es, rows, p.pieces > 1 ? p.piece : vocab, p.padded);
+    p.tail = choose_piece(p.es, rows, vocab - (int64_t)(p.pieces - 1) * p.piece, p.padded);
     p.o_d = take((size_t)rows * p.piece * p.es);
     if (p.pieces > 1) p.o_sums = take((size_t)rows * hidden * sizeof(float));
-    const size_t px = p.dx.splits > 1 ? (size_t)p.dx.splits * rows * hidden : 0;
-    const size_t pw = p.dw.splits > 1 ? (size_t)p.dw.splits * p.piece * hidden : 0;
-    p.o_planes = take((px > pw ? px : pw) * sizeof(float));
-    p.o_bias = take((size_t)p.logits.tiles_n * kShapes[p.logits.shape].wn * vocab * sizeof(float));
+    size_t planes = 0, parts = 0;
+    for (const PieceCuts* c : {&p.whole, &p.tail}) {
+      if (c->dx.splits > 1) planes = std::max(planes, (size_t)c->dx.splits * rows * hidden);
+      if (c->dw.splits > 1) planes = std::max(planes, (size_t)c->dw.splits * p.piece * hidden);
+      parts = std::max(parts, (size_t)c->logits.tiles_n * kShapes[c->logits.shape].wn);
+    }
+    p.o_planes = take(planes * sizeof(float));
+    p.o_bias = take(parts * p.piece * sizeof(float));
     p.o_scale = take(2 * sizeof(float));
   }
   p.bytes = at;
@@ -321,18 +366,11 @@ void launch_tiles(const GemmArgs& g, const Epilogue& ep, int resident, hipStream
       <<<(unsigned)(items < slots ? items : slots), 64 * WM * WN, 0, st>>>(g, ep);
 }
 
-// The product of a and b, a of `m` rows and b of `n`, cut as `c` (whose tile
-// counts may be those of a larger product of the same kind).
+// The product of a and b over K, cut as `c`.
 template <typename T, bool AKC, bool BKC, typename Epilogue>
-void launch_gemm(const Operand& a, const Operand& b, int64_t m, int64_t n, int32_t K, const Cut& c,
-                 const Epilogue& ep, hipStream_t st) {
-  const GemmArgs g{a,
-                   b,
-                   K,
-                   ceil_div(m, kShapes[c.shape].bm),
-                   ceil_div(n, kShapes[c.shape].bn),
-                   K > 0 ? ceil_div(K, c.part) : 1,
-                   c.part};
+void launch_gemm(const Operand& a, const Operand& b, int32_t K, const Cut& c, const Epilogue& ep,
+                 hipStream_t st) {
+  const GemmArgs g{a, b, K, c.tiles_m, c.tiles_n, c.splits, c.part};
   if (c.shape == kLarge)
     launch_tiles<T, 256, 256, 2, 4, AKC, BKC>(g, ep, kResident[kLarge], st);
   else if (c.shape == kMiddle)
@@ -358,7 +396,7 @@ void run_loss(const LossPlan& p, const ctcpb_lm_loss_args& g, char* ws, hipStrea
   float2* part = reinterpret_cast<float2*>(ws + p.o_part);
   float* hit = reinterpret_cast<float*>(ws + p.o_hit);
   const ForwardEpilogue ep{Logits{g.bias, g.targets, g.rows, g.vocab, 0}, part, hit};
-  launch_gemm<T, true, true>(w, x, g.vocab, g.rows, p.padded, p.logits, ep, st);
+  launch_gemm<T, true, true>(w, x, p.padded, p.logits, ep, st);
   loss_join_kernel<<<(unsigned)((g.rows + 31) / 32), 256, 0, st>>>(
       part, hit, g.targets, g.rows, g.vocab, p.logits.tiles_m, g.loss, g.lse);
 }
@@ -382,37 +420,38 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
   for (int32_t k = 0; k < p.pieces; ++k) {
     const int32_t v0 = k * p.piece;
     const int32_t nv = g.vocab - v0 < p.piece ? g.vocab - v0 : p.piece;
+    const PieceCuts& cut = k == p.pieces - 1 ? p.tail : p.whole;
     const Operand wp{w.data + v0 * w.ld, w.ld, nv};
     const GradEpilogue<T> ge{Logits{g.bias, g.targets, g.rows, g.vocab, v0}, g.grad, g.lse, scale,
-                             d, p.piece, part};
-    if (g.rows) launch_gemm<T, true, true>(wp, x, nv, g.rows, p.padded, p.logits, ge, st);
+                             d, p.piece, part, nv};
+    if (g.rows) launch_gemm<T, true, true>(wp, x, p.padded, cut.logits, ge, st);
     if (g.dx && g.rows) {
       // out[token, h]: m = h, n = token, k = vocabulary
       const Operand a{wp.data, wp.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, g.rows};
       T* dx = static_cast<T*>(g.dx);
-      const bool by_planes = p.dx.splits > 1, last = k == p.pieces - 1;
+      const bool by_planes = cut.dx.splits > 1, last = k == p.pieces - 1;
       const OutEpilogue<T> oe{dx,       sums,   by_planes ? planes : nullptr, scale,
                               g.hidden, g.rows, k && !by_planes,              last};
-      launch_gemm<T, false, true>(a, b, g.hidden, g.rows, nv, p.dx, oe, st);
+      launch_gemm<T, false, true>(a, b, nv, cut.dx, oe, st);
       if (by_planes)
-        launch_planes<T>(planes, ceil_div(nv, p.dx.part), (int64_t)g.rows * g.hidden,
-                         k ? sums : nullptr, last ? nullptr : sums, dx, scale, st);
+        launch_planes<T>(planes, cut.dx.splits, (int64_t)g.rows * g.hidden, k ? sums : nullptr,
+                         last ? nullptr : sums, dx, scale, st);
     }
     if (g.dw) {
       // out[v, h]: m = h, n = v, k = token
       const Operand a{x.data, x.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, nv};
       T* dw = static_cast<T*>(g.dw) + (int64_t)v0 * g.hidden;
-      const OutEpilogue<T> oe{dw,       nullptr, p.dw.splits > 1 ? planes : nullptr, scale,
-                              g.hidden, nv,      false,                              true};
-      launch_gemm<T, false, false>(a, b, g.hidden, nv, g.rows, p.dw, oe, st);
-      if (p.dw.splits > 1)
-        launch_planes<T>(planes, p.dw.splits, (int64_t)nv * g.hidden, nullptr, nullptr, dw, scale,
+      const OutEpilogue<T> oe{dw,       nullptr, cut.dw.splits > 1 ? planes : nullptr, scale,
+                              g.hidden, nv,      false,                                true};
+      launch_gemm<T, false, false>(a, b, g.rows, cut.dw, oe, st);
+      if (cut.dw.splits > 1)
+        launch_planes<T>(planes, cut.dw.splits, (int64_t)nv * g.hidden, nullptr, nullptr, dw, scale,
                          st);
     }
+    if (g.dbias)
+      dbias_kernel<<<(unsigned)((nv + 255) / 256), 256, 0, st>>>(
+          part, g.rows ? cut.logits.tiles_n * kShapes[cut.logits.shape].wn : 0, nv, g.dbias + v0);
   }
-  if (g.dbias)
-    dbias_kernel<<<(unsigned)((g.vocab + 255) / 256), 256, 0, st>>>(
-        part, g.rows ? p.logits.tiles_n * kShapes[p.logits.shape].wn : 0, g.vocab, g.dbias);
 }
 
 }  // namespace

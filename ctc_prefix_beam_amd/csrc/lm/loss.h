@@ -134,7 +134,8 @@ struct GradEpilogue {
   const float* scale;       // f16: power of two that d is multiplied by; else null
   T* d;                     // [token][ldd]
   int64_t ldd;
-  float* dbias_part;        // [token tile and wave][vocab], or null
+  float* dbias_part;        // [token tile and wave][rows], or null
+  int32_t rows;             // vocabulary rows of the piece
 
   template <int TM, int TN, int WM, int WN>
   __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*) {
@@ -189,12 +190,13 @@ struct GradEpilogue {
 #pragma unroll
         for (int j = 0; j < TN; ++j) s += acc[i][j][r];   // rows past the tokens are 0
         for (int x = 1; x < 16; x <<= 1) s += __shfl_xor(s, x);
-        const int v = vb + i * 16 + r;
-        if (c == 0 && v < lg.vocab) dbias_part[(int64_t)(at.n * WN + wn) * lg.vocab + v] = s;
+        const int v = vl + i * 16 + r;
+        if (c == 0 && v < rows) dbias_part[(int64_t)(at.n * WN + wn) * rows + v] = s;
       }
   }
 };
 
+// Adds the token tiles' partial sums of a piece, in their order.
 __global__ __launch_bounds__(256) void dbias_kernel(const float* part, int32_t parts, int32_t vocab,
                                                     float* dbias) {
   const int v = blockIdx.x * 256 + threadIdx.x;
