@@ -49,6 +49,8 @@ int guarded(F f) {
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b); }
+
 int log2_of(int32_t v) {
   int n = 0;
   while ((1 << n) < v) ++n;
@@ -103,8 +105,9 @@ bool wide_cache(const CacheView& v) {
 // The launch plan of an attention call, a function of sizes only (the lengths
 // stay on the device).
 struct AttnPlan {
-  int32_t head_tiles, chunk, splits, max_len, tile;
-  size_t bytes;
+  int32_t head_tiles, max_len, waves, ranges;
+  int64_t items;
+  size_t o_part, bytes;   // workspace: the rows' prefix sums, then the parts
 };
 
 int32_t length_bound(const ctcpb_lm_attention_args& g) {
@@ -113,25 +116,32 @@ int32_t length_bound(const ctcpb_lm_attention_args& g) {
 }
 
 AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
-  const int32_t rows = g.rows, heads = g.q_heads, kv_heads = g.kv_heads, window = g.window;
-  const int32_t max_len = length_bound(g);
-  AttnPlan p;
-  p.tile = g.dtype == CTCPB_LM_F32 ? 16 : 32;
-  p.head_tiles = (heads / kv_heads + 15) / 16;
-  p.max_len = max_len;
+  AttnPlan p{};
+  const int32_t tile = g.dtype == CTCPB_LM_F32 ? 16 : 32, group = g.q_heads / g.kv_heads;
+  p.head_tiles = (group + 15) / 16;
+  p.max_len = length_bound(g);
   // tokens a row can have in its range (a window starts at a tile's edge)
-  int64_t span = max_len;
-  if (window > 0 && (int64_t)window + p.tile < span) span = (int64_t)window + p.tile;
-  const int64_t blocks = (int64_t)rows * kv_heads * p.head_tiles;
-  const int64_t step = kAttnWaves * p.tile;
-  int64_t want = blocks ? (1024 + blocks - 1) / blocks : 1;
-  int64_t chunk = (span + want - 1) / want;
-  chunk = (chunk + step - 1) / step * step;
-  if (chunk < 2 * step) chunk = 2 * step;
-  p.chunk = (int32_t)(chunk < INT_MAX / 2 ? chunk : INT_MAX / 2);
-  p.splits = (int32_t)((span + p.chunk - 1) / p.chunk);
-  if (p.splits < 1) p.splits = 1;
-  p.bytes = p.splits > 1 ? (size_t)rows * heads * p.splits * (g.head_dim + 2) * sizeof(float) : 0;
+  int64_t span = p.max_len;
+  if (g.window > 0) span = std::min<int64_t>(span, (int64_t)g.window + tile);
+  const int64_t all = (int64_t)g.kv_heads * p.head_tiles;
+  p.items = g.rows * all;
+  // workgroups of a range kernel that fit on the card at once: by registers, a
+  // head of up to 64 / 128 / 256 values leaves room for 4 / 3 (f32: 2) / 1 on a CU
+  const int64_t slots =
+      256 * (g.head_dim <= 64 ? 4 : g.head_dim > 128 ? 1 : g.dtype == CTCPB_LM_F32 ? 2 : 3);
+  const int64_t steps = ceil_div(std::max<int64_t>(span, 1), kRangeWaves * tile);
+  if (span <= 512 && p.items >= 8 * slots) {
+    p.waves = 1;
+  } else if (span <= 32 * tile && p.items <= slots / 4) {
+    p.waves = 8;
+  } else {
+    p.waves = 0;
+    p.ranges = (int32_t)std::max<int64_t>(
+        1, std::min(slots / all, (g.rows * steps + kLeastSteps - 1) / kLeastSteps));
+    p.o_part = ((size_t)(g.rows + 1) * sizeof(int32_t) + 255) / 256 * 256;
+    p.bytes = p.o_part + (size_t)p.ranges * all * 2 * std::min(16, group) * (g.head_dim + 2) *
+                             sizeof(float);
+  }
   return p;
 }
 
@@ -147,18 +157,45 @@ int check_attention(const ctcpb_lm_attention_args& g) {
   return check_table(g.rows, g.table_stride, g.table_width, g.page_size);
 }
 
+template <typename K>
+void launch_with_lds(K kernel, unsigned blocks, int threads, size_t lds, const AttnArgs& a,
+                     hipStream_t st) {
+  if (lds > 65536)   // more dynamic LDS than a kernel has unasked
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  kernel<<<blocks, threads, lds, st>>>(a);
+}
+
+template <typename T, int DP>
+void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  const size_t state = (size_t)std::min(16, a.group) * (DP + 6) * sizeof(float);
+  if (p.waves == 1) {
+    attn_kernel<T, DP, 1><<<(unsigned)((p.items + 3) / 4), 256, 0, st>>>(a);
+  } else if (p.waves == 8) {
+    // wider heads leave a wave too few registers in workgroups of eight
+    constexpr int NW = DP <= 128 ? 8 : 4;
+    launch_with_lds(attn_kernel<T, DP, NW>, (unsigned)p.items, 64 * NW, NW * state, a, st);
+  } else {
+    launch_with_lds(attn_range_kernel<T, DP>,
+                    (unsigned)((int64_t)p.ranges * a.kv_heads * a.head_tiles), 64 * kRangeWaves,
+                    kRangeWaves * state, a, st);
+    if (p.ranges == 1) return;   // no row is split
+    constexpr int LANES = DP / 4, kGroups = 256 / LANES;
+    const int64_t heads = (int64_t)a.rows * a.heads;
+    // a workgroup to each head while that does not make more than a few to a CU
+    const int ways = heads <= 1024 ? kGroups : 1, per = kGroups / ways;
+    join_kernel<T, LANES><<<(unsigned)((heads + per - 1) / per), 256, 0, st>>>(a, ways);
+  }
+}
+
 template <typename T>
 void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const unsigned blocks = (unsigned)((int64_t)a.rows * a.kv_heads * p.head_tiles * p.splits);
-  const dim3 block(64 * kAttnWaves);
   if (a.D <= 64)
-    attn_kernel<T, 64><<<blocks, block, 0, st>>>(a);
+    launch_attention<T, 64>(a, p, st);
   else if (a.D <= 128)
-    attn_kernel<T, 128><<<blocks, block, 0, st>>>(a);
+    launch_attention<T, 128>(a, p, st);
   else
-    attn_kernel<T, 256><<<blocks, block, 0, st>>>(a);
-  if (p.splits > 1)
-    join_kernel<T><<<(unsigned)(a.rows * a.heads), 256, 0, st>>>(a, p.tile);
+    launch_attention<T, 256>(a, p, st);
 }
 
 // ------------------------------------------------------------------ loss --
@@ -178,8 +215,6 @@ struct Cut {
   int shape;
   int32_t tiles_m, tiles_n, splits, part;
 };
-
-int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b); }
 
 size_t up(size_t v, size_t n) { return (v + n - 1) / n * n; }
 
@@ -586,13 +621,15 @@ int ctcpb_lm_attention(const ctcpb_lm_attention_args* args, void* workspace,
       return fail(CTCPB_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
     if (workspace_bytes < p.bytes)
       return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_attention_workspace");
-    if ((int64_t)g.rows * g.kv_heads * p.head_tiles * p.splits > INT_MAX ||
-        (int64_t)g.rows * g.q_heads > INT_MAX)
+    // steps of all rows are counted with 31 bits
+    if (p.items > INT_MAX || (int64_t)g.rows * g.q_heads > INT_MAX ||
+        (int64_t)g.rows * (p.max_len / 64 + 1) > INT_MAX)
       return fail(CTCPB_ERR_UNSUPPORTED, "too many rows for one launch");
     a.q = static_cast<const char*>(g.q);
     a.out = static_cast<char*>(g.out);
     a.lse = g.lse;
-    a.part = static_cast<float*>(workspace);
+    a.prefix = static_cast<int32_t*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.o_part);
     a.tables = g.tables;
     a.lengths = g.lengths;
     a.q_r = g.q_stride_r;
@@ -611,8 +648,11 @@ int ctcpb_lm_attention(const ctcpb_lm_attention_args* args, void* workspace,
     a.num_pages = g.num_pages;
     a.max_len = p.max_len;
     a.window = g.window;
-    a.chunk = p.chunk;
-    a.splits = p.splits;
+    a.items = (int32_t)p.items;
+    a.ranges = p.ranges;
+    a.wide_q = aligned(g.q, 16) && g.q_stride_r * es % 16 == 0 && g.q_stride_h * es % 16 == 0;
+    a.wide_out =
+        aligned(g.out, 16) && g.out_stride_r * es % 16 == 0 && g.out_stride_h * es % 16 == 0;
     a.scale = g.scale;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (g.dtype == CTCPB_LM_BF16)
