@@ -59,10 +59,12 @@ struct Frag<float> {
 // data[m*ld + k] (k contiguous) or data[k*ld + m] (m contiguous); ld in bytes,
 // a multiple of 16, data 16-byte aligned.  Where m is contiguous, every row of
 // the operand can be read up to the next multiple of 16 bytes.
+// With `twice` (m contiguous only), rows k = 2i and 2i + 1 are both row i of the data.
 struct Operand {
   const char* data;
   int64_t ld;
   int32_t rows;
+  int32_t twice;
 };
 
 // 64 pieces of 16 bytes, lane l's from base + offset, to lds + l*16 (zeros for
@@ -105,6 +107,7 @@ struct TileLoader {
   int32_t lane_row;
   uint32_t lane_byte, lane_off;
   int32_t rows;            // rows (k contiguous) or bytes (m contiguous) left of m
+  int32_t twice;
 
   // Row r of the tile has its piece p at p ^ swizzle(r): bits of r, so that
   // swizzle(a + b) = swizzle(a) ^ swizzle(b) where a and b share none.
@@ -126,13 +129,14 @@ struct TileLoader {
       step = 128;
       rows = o.rows - row0;
     } else {
-      base = o.data + k0 * o.ld + (int64_t)row0 * (int)sizeof(T);
-      step = kBK * o.ld;
+      twice = o.twice;
+      base = o.data + (k0 >> twice) * o.ld + (int64_t)row0 * (int)sizeof(T);
+      step = (kBK >> twice) * o.ld;
       rows = min(o.rows - row0, R) * (int)sizeof(T);
     }
     lane_row = lane / kPieces;
     lane_byte = (lane % kPieces ^ swizzle(lane_row)) * 16;
-    lane_off = (uint32_t)(lane_row * o.ld);
+    lane_off = (uint32_t)((KC ? lane_row : lane_row >> twice) * o.ld);
   }
 
   // Starts fetch q of the tile that begins `left` values of k before the operand's
@@ -143,7 +147,7 @@ struct TileLoader {
     const int row_end = (KC ? rows : left) - first;
     const int byte_end = KC ? min(left, kBK) * (int)sizeof(T) : rows;
     const uint32_t o = lane_row < row_end && (int)byte < byte_end ? lane_off + byte : kOutside;
-    fetch_to_lds(base + first * ld, lds + (wave * kLoads + q) * 1024, o);
+    fetch_to_lds(base + (KC ? first : first >> twice) * ld, lds + (wave * kLoads + q) * 1024, o);
   }
 
   // The whole tile; `base` moves on to the next one.

@@ -201,6 +201,7 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 // ------------------------------------------------------------------ loss --
 
 constexpr size_t kPieceBytes = (size_t)512 << 20;   // workspace for d at a time
+constexpr int32_t kPairRows = 64;                   // tokens up to which d has two rows each
 
 // How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
 struct TileShape {
@@ -273,12 +274,12 @@ struct PieceCuts {
   Cut logits, dx, dw;
   double time;
 };
-PieceCuts choose_piece(int es, int64_t rows, int64_t vocab, int64_t hidden) {
+PieceCuts choose_piece(int es, int64_t rows, int64_t vocab, int64_t hidden, bool pairs = false) {
   PieceCuts c;
   double t[3];
   c.logits = choose_cut(es, vocab, rows, hidden, false, &t[0]);
-  c.dx = choose_cut(es, hidden, rows, vocab, true, &t[1]);
-  c.dw = choose_cut(es, hidden, vocab, rows, true, &t[2]);
+  c.dx = choose_cut(es, hidden, pairs ? 2 * rows : rows, vocab, true, &t[1]);
+  c.dw = choose_cut(es, hidden, vocab, pairs ? 2 * rows : rows, true, &t[2]);
   c.time = t[0] + t[1] + t[2] + 8.0 * rows * hidden / 4e6;   // sums of dx between pieces
   return c;
 }
@@ -312,6 +313,7 @@ struct LossPlan {
   int es, padded;          // padded: hidden up to 16 bytes
   bool pad_x, pad_w;       // rows to be copied to aligned ones
   int32_t piece, pieces;   // gradient: vocabulary rows at a time
+  bool pairs;              // d has two rows for each token
   Cut logits;              // forward
   PieceCuts whole, tail;   // gradient: a whole piece, and the last one
   size_t o_x, o_w, o_part, o_hit, o_d, o_sums, o_planes, o_bias, o_scale, bytes;
@@ -344,11 +346,13 @@ LossPlan plan_loss(const Args& g, bool grad) {
     p.o_part = take((size_t)p.logits.tiles_m * rows * sizeof(float2));
     p.o_hit = take((size_t)rows * sizeof(float));
   } else {
-    p.piece = choose_piece_rows(p.es, rows, vocab, p.padded);
+    p.pairs = p.es == 2 && rows <= kPairRows;
+    p.piece = choose_piece_rows(p.es, p.pairs ? 2 * rows : rows, vocab, p.padded);
     p.pieces = ceil_div(vocab, p.piece);
-    p.whole = choose_piece(p.es, rows, p.pieces > 1 ? p.piece : vocab, p.padded);
-    p.tail = choose_piece(p.es, rows, vocab - (int64_t)(p.pieces - 1) * p.piece, p.padded);
-    p.o_d = take((size_t)rows * p.piece * p.es);
+    p.whole = choose_piece(p.es, rows, p.pieces > 1 ? p.piece : vocab, p.padded, p.pairs);
+    p.tail =
+        choose_piece(p.es, rows, vocab - (int64_t)(p.pieces - 1) * p.piece, p.padded, p.pairs);
+    p.o_d = take((size_t)rows * (p.pairs ? 2 : 1) * p.piece * p.es);
     if (p.pieces > 1) p.o_sums = take((size_t)rows * hidden * sizeof(float));
     size_t planes = 0, parts = 0;
     for (const PieceCuts* c : {&p.whole, &p.tail}) {
@@ -383,15 +387,15 @@ template <typename T>
 Operand aligned_rows(const void* data, int64_t stride, int32_t rows, int32_t hidden,
                      const LossPlan& p, bool pad, char* copy, hipStream_t st) {
   if (!pad)
-    return Operand{static_cast<const char*>(data), stride * (int)sizeof(T), rows};
+    return Operand{static_cast<const char*>(data), stride * (int)sizeof(T), rows, 0};
   typedef typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type U;
   const int64_t all = (int64_t)rows * p.padded;
-  if (all == 0) return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows};
+  if (all == 0) return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows, 0};
   const int64_t blocks = (all + 255) / 256 < 8192 ? (all + 255) / 256 : 8192;
   pad_kernel<U><<<(unsigned)blocks, 256, 0, st>>>(static_cast<const U*>(data), stride,
                                                   reinterpret_cast<U*>(copy), rows, hidden,
                                                   p.padded);
-  return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows};
+  return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows, 0};
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool AKC, bool BKC, typename Epilogue>
@@ -447,26 +451,30 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
   float* planes = reinterpret_cast<float*>(ws + p.o_planes);
   float* part = g.dbias ? reinterpret_cast<float*>(ws + p.o_bias) : nullptr;
   float* scale = nullptr;
-  if (std::is_same<T, _Float16>::value) {
+  const bool f16 = std::is_same<T, _Float16>::value;
+  if (sizeof(T) == 2 && (f16 || !p.pairs)) {
     scale = reinterpret_cast<float*>(ws + p.o_scale);
-    scale_kernel<<<1, 1024, 0, st>>>(g.grad, g.targets, g.rows, g.vocab, scale);
+    // f16 holds 4096 times numbers down to 10^-11 of the largest
+    scale_kernel<<<1, 1024, 0, st>>>(g.grad, g.targets, g.rows, g.vocab, f16 ? 4096.0f : 1.0f,
+                                     scale);
   }
+  const int32_t drows = p.pairs ? 2 * g.rows : g.rows;
   const int64_t ldd = (int64_t)p.piece * (int)sizeof(T);
   for (int32_t k = 0; k < p.pieces; ++k) {
     const int32_t v0 = k * p.piece;
     const int32_t nv = g.vocab - v0 < p.piece ? g.vocab - v0 : p.piece;
     const PieceCuts& cut = k == p.pieces - 1 ? p.tail : p.whole;
-    const Operand wp{w.data + v0 * w.ld, w.ld, nv};
+    const Operand wp{w.data + v0 * w.ld, w.ld, nv, 0};
     const GradEpilogue<T> ge{Logits{g.bias, g.targets, g.rows, g.vocab, v0}, g.grad, g.lse, scale,
-                             d, p.piece, part, nv};
+                             d, p.pairs, p.piece, part, nv};
     if (g.rows) launch_gemm<T, true, true>(wp, x, p.padded, cut.logits, ge, st);
     if (g.dx && g.rows) {
       // out[token, h]: m = h, n = token, k = vocabulary
-      const Operand a{wp.data, wp.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, g.rows};
+      const Operand a{wp.data, wp.ld, p.padded, 0}, b{reinterpret_cast<char*>(d), ldd, drows, 0};
       T* dx = static_cast<T*>(g.dx);
       const bool by_planes = cut.dx.splits > 1, last = k == p.pieces - 1;
       const OutEpilogue<T> oe{dx,       sums,   by_planes ? planes : nullptr, scale,
-                              g.hidden, g.rows, k && !by_planes,              last};
+                              g.hidden, g.rows, p.pairs, k && !by_planes,     last};
       launch_gemm<T, false, true>(a, b, nv, cut.dx, oe, st);
       if (by_planes)
         launch_planes<T>(planes, cut.dx.splits, (int64_t)g.rows * g.hidden, k ? sums : nullptr,
@@ -474,11 +482,11 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
     }
     if (g.dw) {
       // out[v, h]: m = h, n = v, k = token
-      const Operand a{x.data, x.ld, p.padded}, b{reinterpret_cast<char*>(d), ldd, nv};
+      const Operand a{x.data, x.ld, p.padded, p.pairs}, b{reinterpret_cast<char*>(d), ldd, nv, 0};
       T* dw = static_cast<T*>(g.dw) + (int64_t)v0 * g.hidden;
       const OutEpilogue<T> oe{dw,       nullptr, cut.dw.splits > 1 ? planes : nullptr, scale,
-                              g.hidden, nv,      false,                                true};
-      launch_gemm<T, false, false>(a, b, g.rows, cut.dw, oe, st);
+                              g.hidden, nv,      false, false,                         true};
+      launch_gemm<T, false, false>(a, b, drows, cut.dw, oe, st);
       if (cut.dw.splits > 1)
         launch_planes<T>(planes, cut.dw.splits, (int64_t)nv * g.hidden, nullptr, nullptr, dw, scale,
                          st);

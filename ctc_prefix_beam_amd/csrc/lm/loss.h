@@ -6,9 +6,17 @@
 // loss_join_kernel joins them.  Backward: a piece of the vocabulary at a time,
 //   d[n, v] = g[n] (exp(logit[n, v] - lse[n]) - [v = t[n]])
 // is recomputed, rounded to the inputs' type and kept for the piece only (at most
-// kPieceBytes of workspace); dx += d w and dw = d^T x follow from it.  The
-// rounding of d is unbiased and enters sums of many terms: it adds to dx and dw
-// about what their own rounding to that type does.
+// kPieceBytes of workspace); dx += d w and dw = d^T x follow from it.
+//
+// The rounding of d is unbiased, and what it adds to dx and dw is about what their
+// own rounding to that type does.  Two things keep it there.  d is scaled so that
+// the largest |g| is a power of two: the targets' entries, -g (1 - p), the largest
+// of their rows, then lie mostly just below one, where a rounding is smallest for
+// its number (random entries: error of dx 1.33 times that of the result's rounding
+// alone, not 1.41 to 1.6); with f16 it also keeps d in range.  And with up to
+// kPairRows tokens, too few to average over, d is kept as the sum of two values of
+// the type in neighbouring rows (2n and 2n + 1): twice the products, in calls that
+// wait for memory.
 #pragma once
 #include "gemm.h"
 
@@ -131,8 +139,9 @@ template <typename T>
 struct GradEpilogue {
   Logits lg;
   const float *grad, *lse;
-  const float* scale;       // f16: power of two that d is multiplied by; else null
-  T* d;                     // [token][ldd]
+  const float* scale;       // what d is multiplied by, or null
+  T* d;                     // [token][ldd], with pairs [2 token]
+  bool pairs;
   int64_t ldd;
   float* dbias_part;        // [token tile and wave][rows], or null
   int32_t rows;             // vocabulary rows of the piece
@@ -176,8 +185,13 @@ struct GradEpilogue {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
           const f32x4 v = acc[i][j] * sc;
-          *reinterpret_cast<T4*>(d + n * ldd + vl + i * 16) =
-              T4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+          const T4 t4 = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+          T* to = d + (pairs ? 2 * n : n) * ldd + vl + i * 16;
+          *reinterpret_cast<T4*>(to) = t4;
+          if (pairs)
+            *reinterpret_cast<T4*>(to + ldd) =
+                T4{(T)(v[0] - (float)t4[0]), (T)(v[1] - (float)t4[1]), (T)(v[2] - (float)t4[2]),
+                   (T)(v[3] - (float)t4[3])};
         }
       }
     }
@@ -213,8 +227,9 @@ template <typename T>
 struct OutEpilogue {
   T* out;
   float *sums, *planes;     // or null
-  const float* scale;       // f16: what d was multiplied by
+  const float* scale;       // what d was multiplied by, or null
   int32_t M, N;
+  bool pairs;               // the product's rows n = 2i and 2i + 1 add up to row i
   bool add, last;           // sums hold something; the result goes to `out`
 
   template <int TM, int TN, int WM, int WN>
@@ -227,7 +242,15 @@ struct OutEpilogue {
     float* f = planes ? planes + (int64_t)at.split * N * M : last ? nullptr : sums;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = at.n * BN + (wn * TN + j) * 16 + c;
+      int n = at.n * BN + (wn * TN + j) * 16 + c;
+      if (pairs) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] += __shfl_xor(acc[i][j][r], 1);
+        if (c & 1) continue;
+        n >>= 1;
+      }
       if (n >= N) continue;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
@@ -278,28 +301,27 @@ __global__ __launch_bounds__(256) void planes_kernel(const float* planes, int32_
   }
 }
 
-// f16 only: a power of two that brings the largest |grad| of a row with a
-// target to 2^11..2^12, so that d (at most |grad|) neither overflows nor loses
-// its small values, and its inverse.
+// scale[0]: what takes the largest |grad| of a row with a target to `top`, a power
+// of two, and scale[1] its inverse.
 __global__ __launch_bounds__(1024) void scale_kernel(const float* grad, const int32_t* targets,
-                                                     int32_t tokens, int32_t vocab, float* scale) {
-  __shared__ float top[16];
+                                                     int32_t tokens, int32_t vocab, float top,
+                                                     float* scale) {
+  __shared__ float most[16];
   float m = 0.0f;
+#pragma unroll 4
   for (int n = threadIdx.x; n < tokens; n += 1024) {
     const float v = fabsf(grad[n]);
     const int t = targets[n];
     if (t >= 0 && t < vocab && v <= 3.4028235e38f) m = fmaxf(m, v);
   }
   for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-  if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x) return;
-  for (int w = 0; w < 16; ++w) m = fmaxf(m, top[w]);
-  int e = 0;
-  if (m > 0.0f) frexpf(m, &e);          // m < 2^e
-  e = min(max(12 - e, -100), 100);
-  scale[0] = ldexpf(1.0f, e);
-  scale[1] = ldexpf(1.0f, -e);
+  for (int w = 0; w < 16; ++w) m = fmaxf(m, most[w]);
+  const float s = m > 0.0f ? fminf(fmaxf(top / m, 1e-30f), 1e30f) : 1.0f;
+  scale[0] = s;
+  scale[1] = 1.0f / s;
 }
 
 // Rows of `width` elements to rows of `padded` (zeros behind them): operands
