@@ -382,22 +382,25 @@ def token_loss(x, w, targets, bias=None):
 
 
 class PagedCache:
-    """A paged key/value cache of one attention layer and its page allocator,
-    for `rows` requests of at most `max_len` tokens each.
+    """The paged key/value cache of a model's attention layers and its page
+    allocator, for `rows` requests of at most `max_len` tokens each.  The layers
+    share their pages' numbers, so one plan serves them all.
 
-    ``append(counts, total)`` hands out pages, ``store(k, v, slots)`` writes the
-    new tokens, ``attend(q)`` attends over each request's tokens, and
-    ``release(finished)`` gives pages back.  `num_pages` (default: every request
-    at max_len) may be smaller: a request the pool cannot serve is flagged in
-    the plan's status and holds only the tokens that have a slot.  Use one
-    PagedCache per stream, or order its calls."""
+    ``append(counts, total)`` hands out pages, ``store(k, v, slots, layer)``
+    writes a layer's new tokens, ``attend(q, layer)`` attends over each request's
+    tokens, and ``release(finished)`` gives pages back.  `num_pages` (default:
+    every request at max_len) may be smaller: a request the pool cannot serve is
+    flagged in the plan's status and holds only the tokens that have a slot.  Use
+    one PagedCache per stream, or order its calls."""
 
     def __init__(self, rows: int, max_len: int, kv_heads: int, head_dim: int,
-                 dtype=torch.bfloat16, page_size: int = 16, num_pages: int = 0, device="cuda"):
+                 dtype=torch.bfloat16, page_size: int = 16, num_pages: int = 0, device="cuda",
+                 layers: int = 1):
         width = -(-max_len // page_size)
         num_pages = num_pages or max(1, rows * width)
         self.page_size, self.max_len = page_size, max_len
-        self.k = torch.empty((num_pages, page_size, kv_heads, head_dim), dtype=dtype, device=device)
+        self.k = torch.empty((layers, num_pages, page_size, kv_heads, head_dim), dtype=dtype,
+                             device=device)
         self.v = torch.empty_like(self.k)
         self.tables = torch.full((rows, width), -1, dtype=torch.int32, device=device)
         self.pool = torch.arange(num_pages, dtype=torch.int32, device=device)
@@ -410,11 +413,11 @@ class PagedCache:
         self.lengths, self.taken = plan.lengths, plan.taken
         return plan
 
-    def store(self, k, v, slots, stream=None):
-        cache_store(k, v, slots, self.k, self.v, stream)
+    def store(self, k, v, slots, layer: int = 0, stream=None):
+        cache_store(k, v, slots, self.k[layer], self.v[layer], stream)
 
-    def attend(self, q, scale=None, window=0, max_len=0, stream=None):
-        return attention(q, self.k, self.v, self.tables, self.lengths, scale, window,
+    def attend(self, q, layer: int = 0, scale=None, window: int = 0, max_len: int = 0, stream=None):
+        return attention(q, self.k[layer], self.v[layer], self.tables, self.lengths, scale, window,
                          max_len or self.max_len, stream=stream)
 
     def release(self, finished, stream=None):
