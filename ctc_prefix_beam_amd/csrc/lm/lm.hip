@@ -436,8 +436,13 @@ void run_loss(const LossPlan& p, const ctcpb_lm_loss_args& g, char* ws, hipStrea
   float* hit = reinterpret_cast<float*>(ws + p.o_hit);
   const ForwardEpilogue ep{Logits{g.bias, g.targets, g.rows, g.vocab, 0}, part, hit};
   launch_gemm<T, true, true>(w, x, p.padded, p.logits, ep, st);
-  loss_join_kernel<<<(unsigned)((g.rows + 31) / 32), 256, 0, st>>>(
-      part, hit, g.targets, g.rows, g.vocab, p.logits.tiles_m, g.loss, g.lse);
+  // few tokens: more threads to each, for latency
+  if (g.rows <= 2048)
+    loss_join_kernel<4><<<(unsigned)ceil_div(g.rows, 4), 256, 0, st>>>(
+        part, hit, g.targets, g.rows, g.vocab, p.logits.tiles_m, g.loss, g.lse);
+  else
+    loss_join_kernel<32><<<(unsigned)ceil_div(g.rows, 32), 256, 0, st>>>(
+        part, hit, g.targets, g.rows, g.vocab, p.logits.tiles_m, g.loss, g.lse);
 }
 
 template <typename T>
@@ -517,12 +522,19 @@ int ctcpb_lm_cache_plan(const ctcpb_lm_plan_args* args, void* stream) {
       return fail(CTCPB_ERR_INVALID, kNull);
     PlanArgs a{g.lengths,   g.counts, g.pool,        g.taken,     g.tables, g.slots,
                g.positions, g.starts, g.out_lengths, g.out_taken, g.status, g.table_stride,
-               g.rows,      g.table_width, g.pool_size, log2_of(g.page_size), g.capacity, 0};
+               g.rows,      g.table_width, g.pool_size, log2_of(g.page_size), g.capacity, 0, false};
     const int threads = g.rows <= 256 ? 256 : kPlanThreads;
-    // a workgroup's part of the slot map: a few tokens per thread
-    a.per_block = 4 * threads;
-    const int blocks = g.capacity ? (g.capacity + a.per_block - 1) / a.per_block : 1;
-    plan_kernel<<<blocks, threads, 0, static_cast<hipStream_t>(stream)>>>(a);
+    // a workgroup's part of the slot map: no more workgroups than CUs (each scans all
+    // rows) while that leaves every thread four tokens at least
+    a.per_block = (int32_t)(ceil_div(ceil_div(g.capacity, 256), 4 * threads) * 4 * threads);
+    if (a.per_block == 0) a.per_block = 4 * threads;
+    a.wide = aligned(g.slots, 16) && aligned(g.positions, 16);
+    const unsigned blocks = g.capacity ? ceil_div(g.capacity, a.per_block) : 1;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (g.rows <= kPlanThreads)
+      plan_kernel<1><<<blocks, threads, 0, st>>>(a);
+    else
+      plan_kernel<4><<<blocks, threads, 0, st>>>(a);
     return launched("plan_kernel");
   });
 }

@@ -105,17 +105,20 @@ struct ForwardEpilogue {
   }
 };
 
-// Joins the tiles of 32 tokens, 8 threads to each.
+// Joins the tiles of TOKENS tokens, 256 / TOKENS threads to each.
+template <int TOKENS>
 __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, const float* hit,
                                                         const int32_t* targets, int32_t tokens,
                                                         int32_t vocab, int32_t tiles, float* loss,
                                                         float* lse) {
-  __shared__ float2 red[8][32];
-  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int64_t n = (int64_t)blockIdx.x * 32 + c;
+  constexpr int kShare = 256 / TOKENS;
+  __shared__ float2 red[kShare][TOKENS + 1];
+  const int c = threadIdx.x % TOKENS, k = threadIdx.x / TOKENS;
+  const int64_t n = (int64_t)blockIdx.x * TOKENS + c;
   float m = neg_inf(), s = 0.0f;
   if (n < tokens)
-    for (int t = k; t < tiles; t += 8) {
+#pragma unroll 4
+    for (int t = k; t < tiles; t += kShare) {
       const float2 p = part[t * (int64_t)tokens + n];
       const float m1 = fmaxf(m, p.x), m0 = m1 == neg_inf() ? 0.0f : m1;
       s = s * expf(m - m0) + p.y * expf(p.x - m0);
@@ -123,12 +126,16 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, cons
     }
   red[k][c] = float2{m, s};
   __syncthreads();
+  for (int half = kShare / 2; half; half >>= 1) {
+    if (k < half) {
+      const float2 p = red[k][c], q = red[k + half][c];
+      const float m1 = fmaxf(p.x, q.x), m0 = m1 == neg_inf() ? 0.0f : m1;
+      red[k][c] = float2{m1, p.y * expf(p.x - m0) + q.y * expf(q.x - m0)};
+    }
+    __syncthreads();
+  }
   if (k || n >= tokens) return;
-  for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w][c].x);
-  const float m0 = m == neg_inf() ? 0.0f : m;
-  s = 0.0f;
-  for (int w = 0; w < 8; ++w) s += red[w][c].y * expf(red[w][c].x - m0);
-  const float l = m + logf(s);
+  const float l = red[0][c].x + logf(red[0][c].y);
   const int t = targets[n];
   lse[n] = l;
   loss[n] = t >= 0 && t < vocab ? l - hit[n] : 0.0f;
