@@ -64,25 +64,45 @@ struct Operand {
   const char* data;
   int64_t ld;
   int32_t rows;
-  int32_t twice;
+  bool twice;
 };
 
-// 64 pieces of 16 bytes, lane l's from base + offset, to lds + l*16 (zeros for
-// offsets outside).  Written as assembly, with no register result, because the
-// compiler makes every transposing LDS read wait for all fetches it knows of; the
-// waits that are needed are those of wait_and_meet().
-__device__ inline void fetch_to_lds(const char* base, char* lds, uint32_t offset) {
+// A fetch straight into LDS: lane l's BYTES (4 or 16) from base + offset to lds +
+// l*BYTES (zeros for offsets outside).  Written as assembly, with no register
+// result, because the compiler makes every transposing LDS read wait for all fetches
+// it knows of; the waits that are needed are those of wait_and_meet().
+template <int BYTES>
+__device__ inline void fetch_to_lds(const void* base, void* lds, uint32_t offset) {
   const uint64_t b = reinterpret_cast<uint64_t>(base);
   const u32x4 rsrc = {(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, 0x7fffffffu, 0x00027000u};
   const uint32_t to = (uint32_t)(uintptr_t)(lds_char*)lds;
   // nothing else in these kernels uses m0 (the warning is about reserved registers)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(to), "v"(offset), "s"(rsrc)
-               : "m0");
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(offset), "s"(rsrc)
+                 : "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(offset), "s"(rsrc)
+                 : "m0");
 #pragma clang diagnostic pop
+}
+
+// N (a multiple of 64) floats from `from` on to `lds`, zeros past `count` of them,
+// the fetches dealt to the W waves from wave `first` on.
+template <int N, int W>
+__device__ inline void fetch_floats(const void* from, int count, float* lds, int first, int wave,
+                                    int lane) {
+#pragma unroll
+  for (int i = 0; i < N / 64; ++i)
+    if ((i + first) % W == wave) {
+      const int k = i * 64 + lane;
+      fetch_to_lds<4>(from, lds + i * 64, k < count ? (uint32_t)k * 4 : kOutside);
+    }
 }
 
 // Fetches an R-row tile of an operand into LDS and reads fragments from it.
@@ -129,7 +149,7 @@ struct TileLoader {
       step = 128;
       rows = o.rows - row0;
     } else {
-      twice = o.twice;
+      twice = o.twice ? 1 : 0;
       base = o.data + (k0 >> twice) * o.ld + (int64_t)row0 * (int)sizeof(T);
       step = (kBK >> twice) * o.ld;
       rows = min(o.rows - row0, R) * (int)sizeof(T);
@@ -147,7 +167,7 @@ struct TileLoader {
     const int row_end = (KC ? rows : left) - first;
     const int byte_end = KC ? min(left, kBK) * (int)sizeof(T) : rows;
     const uint32_t o = lane_row < row_end && (int)byte < byte_end ? lane_off + byte : kOutside;
-    fetch_to_lds(base + (KC ? first : first >> twice) * ld, lds + (wave * kLoads + q) * 1024, o);
+    fetch_to_lds<16>(base + (KC ? first : first >> twice) * ld, lds + (wave * kLoads + q) * 1024, o);
   }
 
   // The whole tile; `base` moves on to the next one.
@@ -191,13 +211,15 @@ struct GemmArgs {
   int32_t K;
   int32_t tiles_m, tiles_n;
   int32_t splits, part;   // parts of k, and the length of one (a multiple of the k-tile)
+  int32_t n0;             // the epilogue's n of b's first row
 };
 
 // Where work item `id` lies.  Consecutive ids go to the eight XCDs in turn, so
 // each XCD is given a contiguous range of the items, walked eight n-tiles wide,
 // to find its operands in its own L2.
 struct Place {
-  int32_t m, n, split;
+  int32_t m, n, split;   // tiles
+  int32_t n0;            // the epilogue's n of the tile's first row
 };
 __device__ inline Place place_of(const GemmArgs& a, int id) {
   const int tiles = a.tiles_m * a.tiles_n, per = tiles * a.splits / 8;
@@ -235,9 +257,10 @@ __device__ inline void interleave() {
 
 // BM x BN per work item, WM x WN waves.  Workgroups stay for as many items as
 // come to them: an item's first fetches are under way while the one before is
-// finished by the epilogue.
+// finished by the epilogue.  LDS lets one, two or four workgroups of the three
+// shapes share a CU; the registers have to leave room for them.
 template <typename T, int BM, int BN, int WM, int WN, bool AKC, bool BKC, typename Epilogue>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs a, Epilogue ep) {
+__global__ __launch_bounds__(64 * WM * WN, BM == 64 ? 4 : 2) void gemm_kernel(GemmArgs a, Epilogue ep) {
   constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   typedef TileLoader<T, BM, AKC, W> LA;
   typedef TileLoader<T, BN, BKC, W> LB;
@@ -246,7 +269,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs a, Epilogue
   constexpr int kFetches = LA::kLoads + LB::kLoads;
   constexpr int kEarly = TM > 2 ? TM / 4 : 1;   // rows of products with the fetches among them
   __shared__ __align__(1024) char lds[2][(BM + BN) * 128];
-  __shared__ float2 scratch[WM * BN];           // the epilogue's
+  // the epilogue's: room to join the waves, and what it asked for of this item and the next
+  __shared__ float2 scratch[Epilogue::kJoins ? WM * BN : 1];
+  constexpr int kWanted = Epilogue::template wanted<BM, BN>();
+  __shared__ __align__(16) float aside[2][kWanted ? kWanted : 4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -254,6 +280,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs a, Epilogue
   LA la;
   LB lb;
   Place at = place_of(a, blockIdx.x);
+  int parity = 0;
   int K;                                        // length of the item's part of k
   const auto begin = [&] {
     const int k0 = at.split * a.part;
@@ -264,6 +291,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs a, Epilogue
     lb.load(lds[0] + BM * 128, K, wave);
     la.load(lds[1], K - LA::kBK, wave);
     lb.load(lds[1] + BM * 128, K - LA::kBK, wave);
+    at.n0 = a.n0 + at.n * BN;
+    ep.template fetch<BM, BN, W>(at, aside[parity], wave, lane);
   };
   begin();
   for (int id = blockIdx.x; id < items;) {
@@ -330,14 +359,16 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs a, Epilogue
     }
     wait_and_meet();   // nothing is on its way, and nobody reads the buffers
     const Place done = at;
+    const float* got = aside[parity];
     id += gridDim.x;
     if (id < items) {
       at = place_of(a, id);
+      parity ^= 1;
       begin();
     }
     // sums acc[i][j][r]: m = done.m*BM + (wm*TM + i)*16 + (lane>>4)*4 + r,
-    //                    n = done.n*BN + (wn*TN + j)*16 + (lane&15)
-    ep.template run<TM, TN, WM, WN>(acc, done, wm, wn, lane, scratch);
+    //                    n = done.n0 + (wn*TN + j)*16 + (lane&15)
+    ep.template run<TM, TN, WM, WN>(acc, done, wm, wn, lane, scratch, got);
   }
 }
 

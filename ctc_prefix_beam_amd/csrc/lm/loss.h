@@ -30,33 +30,66 @@ struct Logits {
   int32_t v0;               // first vocabulary row of the launch
 };
 
-// Adds the bias of a wave's rows vb + i*16 + r (past the vocabulary: nothing).
+// Adds the bias of a wave's rows i*16 + r (`bias`: of the first of them, in LDS).
 template <int TM, int TN>
-__device__ inline void add_bias(f32x4 (&acc)[TM][TN], const Logits& lg, int vb) {
-  if (!lg.bias) return;
+__device__ inline void add_bias(f32x4 (&acc)[TM][TN], const float* bias) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i) {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(bias + i * 16);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int v = vb + i * 16 + r;
-      const float b = v < lg.vocab ? lg.bias[v] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j][r] += b;
-    }
+    for (int j = 0; j < TN; ++j) acc[i][j] += b;
+  }
 }
 
+// Two neighbouring 16 x 16 tiles of a wave's sums as 16-bit values in rows of
+// memory: lane (g, c) has rows' places 4g .. 4g+3 of both in column c.  Swapping the
+// odd lane groups of the first with the even ones of the second gives every lane
+// eight neighbouring values, and a row's 32 values (64 bytes) to the same store:
+// half as many requests to the L2 as with eight bytes a lane.
+template <typename T>
+struct TilePair {
+  u32x4 bits;
+  static __device__ uint32_t two(float a, float b) {
+    typedef T T2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, T2{(T)a, (T)b});
+  }
+  __device__ TilePair(const f32x4& x, const f32x4& y) {
+    const auto a = __builtin_amdgcn_permlane16_swap(two(x[0], x[1]), two(y[0], y[1]), false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(two(x[2], x[3]), two(y[2], y[3]), false, false);
+    bits = u32x4{a[0], b[0], a[1], b[1]};
+  }
+  // where the lane's eight values begin, from the first tile's first row
+  static __device__ int at(int g) { return (g & 1) * 16 + (g >> 1) * 8; }
+  __device__ void store(T* to) const { *reinterpret_cast<u32x4*>(to) = bits; }
+};
+
+// The epilogues of the logits run with the next item's fetches under way, which
+// would delay loads of their own: what they need of the item's rows and columns is
+// fetched into LDS with its first tiles ([BM] bias, then arrays of [BN]).
 struct ForwardEpilogue {
   Logits lg;
   float2* part;             // [vocabulary tile][token]: maximum, sum of exp(logit - maximum)
   float* hit;               // [token]: logit of the target
 
+  static constexpr bool kJoins = true;
+  template <int BM, int BN>
+  static constexpr int wanted() {
+    return BM + BN;
+  }
+  template <int BM, int BN, int W>
+  __device__ void fetch(const Place& at, float* to, int wave, int lane) const {
+    if (lg.bias)
+      fetch_floats<BM, W>(lg.bias + at.m * BM, lg.vocab - at.m * BM, to, 0, wave, lane);
+    fetch_floats<BN, W>(lg.targets + at.n0, lg.tokens - at.n0, to + BM, BM / 64, wave, lane);
+  }
+
   template <int TM, int TN, int WM, int WN>
   __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane,
-                      float2* red) {
-    constexpr int BN = WN * TN * 16;
+                      float2* red, const float* got) {
+    constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     const int g = lane >> 4, c = lane & 15;
     const int vb = (at.m * WM + wm) * TM * 16 + g * 4;
-    add_bias<TM, TN>(acc, lg, vb);
+    if (lg.bias) add_bias<TM, TN>(acc, got + wm * TM * 16 + g * 4);
     if ((at.m * WM + wm + 1) * TM * 16 > lg.vocab) {   // rows past the vocabulary
 #pragma unroll
       for (int i = 0; i < TM; ++i)
@@ -68,8 +101,8 @@ struct ForwardEpilogue {
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = at.n * BN + (wn * TN + j) * 16 + c;
-      const int t = n < lg.tokens ? lg.targets[n] : -1;
+      const int k = (wn * TN + j) * 16 + c, n = at.n0 + k;
+      const int t = n < lg.tokens ? __float_as_int(got[BM + k]) : -1;
       if (__any(t >= vb && t < vb + TM * 16 && t < lg.vocab)) {   // few tiles have a target
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -94,7 +127,7 @@ struct ForwardEpilogue {
     }
     __syncthreads();
     for (int k = threadIdx.x; k < BN; k += 64 * WM * WN) {
-      const int n = at.n * BN + k;
+      const int n = at.n0 + k;
       if (n >= lg.tokens) continue;
       float m = neg_inf(), s = 0.0f;
       for (int w = 0; w < WM; ++w) m = fmaxf(m, red[w * BN + k].x);
@@ -105,17 +138,20 @@ struct ForwardEpilogue {
   }
 };
 
-// Joins the tiles of TOKENS tokens, 256 / TOKENS threads to each.
+// Joins the tiles of TOKENS tokens, 256 / TOKENS threads to each.  Tokens from
+// `main` on were cut into other tiles.
 template <int TOKENS>
 __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, const float* hit,
                                                         const int32_t* targets, int32_t tokens,
-                                                        int32_t vocab, int32_t tiles, float* loss,
+                                                        int32_t vocab, int32_t main, int32_t tiles,
+                                                        int32_t rest_tiles, float* loss,
                                                         float* lse) {
   constexpr int kShare = 256 / TOKENS;
   __shared__ float2 red[kShare][TOKENS + 1];
   const int c = threadIdx.x % TOKENS, k = threadIdx.x / TOKENS;
   const int64_t n = (int64_t)blockIdx.x * TOKENS + c;
   float m = neg_inf(), s = 0.0f;
+  if (n >= main) tiles = rest_tiles;
   if (n < tokens)
 #pragma unroll 4
     for (int t = k; t < tiles; t += kShare) {
@@ -152,24 +188,40 @@ struct GradEpilogue {
   int64_t ldd;
   float* dbias_part;        // [token tile and wave][rows], or null
   int32_t rows;             // vocabulary rows of the piece
+  int32_t first_part;       // of this launch
+
+  static constexpr bool kJoins = false;
+  template <int BM, int BN>
+  static constexpr int wanted() {
+    return BM + 3 * BN;
+  }
+  template <int BM, int BN, int W>
+  __device__ void fetch(const Place& at, float* to, int wave, int lane) const {
+    const int v = lg.v0 + at.m * BM, n = lg.tokens - at.n0;
+    if (lg.bias) fetch_floats<BM, W>(lg.bias + v, lg.vocab - v, to, 0, wave, lane);
+    fetch_floats<BN, W>(lg.targets + at.n0, n, to + BM, BM / 64, wave, lane);
+    fetch_floats<BN, W>(lse + at.n0, n, to + BM + BN, (BM + BN) / 64, wave, lane);
+    fetch_floats<BN, W>(grad + at.n0, n, to + BM + 2 * BN, (BM + 2 * BN) / 64, wave, lane);
+  }
 
   template <int TM, int TN, int WM, int WN>
-  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*) {
-    constexpr int BN = WN * TN * 16;
-    typedef T T4 __attribute__((ext_vector_type(4)));
+  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*,
+                      const float* got) {
+    constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     const int g = lane >> 4, c = lane & 15;
     const int vl = (at.m * WM + wm) * TM * 16 + g * 4;   // in the piece
     const int vb = lg.v0 + vl;
-    const float sc = scale ? scale[0] : 1.0f;
-    add_bias<TM, TN>(acc, lg, vb);
+    const float sc = scale ? scale[0] : 1.0f, inv = scale ? scale[1] : 1.0f;
+    if (lg.bias) add_bias<TM, TN>(acc, got + wm * TM * 16 + g * 4);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = at.n * BN + (wn * TN + j) * 16 + c;
+      const int k = (wn * TN + j) * 16 + c, n = at.n0 + k;
       const bool live = n < lg.tokens;
-      const int t = live ? lg.targets[n] : -1;
+      const int t = live ? __float_as_int(got[BM + k]) : -1;
       const bool in = t >= 0 && t < lg.vocab;
       // a row without a target: exp(logit - inf) = 0
-      const float gn = in ? grad[n] : 0.0f, ln = in ? lse[n] : __builtin_huge_valf();
+      const float gn = in ? sc * got[BM + 2 * BN + k] : 0.0f;
+      const float ln = in ? got[BM + BN + k] : __builtin_huge_valf();
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -188,18 +240,28 @@ struct GradEpilogue {
           for (int r = 0; r < 4; ++r)
             if (vb + i * 16 + r >= lg.vocab) acc[i][j][r] = 0.0f;
       }
-      if (live) {
+      T* row = d + (pairs ? 2 * n : n) * ldd + (at.m * WM + wm) * TM * 16;
+      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const f32x4 v = acc[i][j] * sc;
-          const T4 t4 = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-          T* to = d + (pairs ? 2 * n : n) * ldd + vl + i * 16;
-          *reinterpret_cast<T4*>(to) = t4;
-          if (pairs)
-            *reinterpret_cast<T4*>(to + ldd) =
-                T4{(T)(v[0] - (float)t4[0]), (T)(v[1] - (float)t4[1]), (T)(v[2] - (float)t4[2]),
-                   (T)(v[3] - (float)t4[3])};
+        for (int i = 0; i < TM; i += 2) {
+          const f32x4 x = acc[i][j], y = acc[i + 1][j];
+          const TilePair<T> hi(x, y);
+          if (live) hi.store(row + i * 16 + TilePair<T>::at(g));
+          if (pairs) {
+            f32x4 xl, yl;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              xl[r] = x[r] - (float)(T)x[r];
+              yl[r] = y[r] - (float)(T)y[r];
+            }
+            const TilePair<T> lo(xl, yl);
+            if (live) lo.store(row + ldd + i * 16 + TilePair<T>::at(g));
+          }
         }
+      } else if (live) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+          *reinterpret_cast<f32x4*>(row + i * 16 + g * 4) = acc[i][j];
       }
     }
     if (!dbias_part) return;
@@ -212,7 +274,8 @@ struct GradEpilogue {
         for (int j = 0; j < TN; ++j) s += acc[i][j][r];   // rows past the tokens are 0
         for (int x = 1; x < 16; x <<= 1) s += __shfl_xor(s, x);
         const int v = vl + i * 16 + r;
-        if (c == 0 && v < rows) dbias_part[(int64_t)(at.n * WN + wn) * rows + v] = s;
+        if (c == 0 && v < rows)
+          dbias_part[(int64_t)(first_part + at.n * WN + wn) * rows + v] = s * inv;
       }
   }
 };
@@ -239,49 +302,69 @@ struct OutEpilogue {
   bool pairs;               // the product's rows n = 2i and 2i + 1 add up to row i
   bool add, last;           // sums hold something; the result goes to `out`
 
+  static constexpr bool kJoins = false;
+  template <int BM, int BN>
+  static constexpr int wanted() {
+    return 0;
+  }
+  template <int BM, int BN, int W>
+  __device__ void fetch(const Place&, float*, int, int) const {}
+
   template <int TM, int TN, int WM, int WN>
-  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*) {
-    constexpr int BN = WN * TN * 16;
-    typedef T T4 __attribute__((ext_vector_type(4)));
+  __device__ void run(f32x4 (&acc)[TM][TN], const Place& at, int wm, int wn, int lane, float2*,
+                      const float*) {
     const int g = lane >> 4, c = lane & 15;
     const int mb = (at.m * WM + wm) * TM * 16 + g * 4;
     const float inv = scale ? scale[1] : 1.0f;
     float* f = planes ? planes + (int64_t)at.split * N * M : last ? nullptr : sums;
+    // results of 16-bit types whose rows are 16-byte aligned
+    const bool wide = sizeof(T) == 2 && !f && M % 8 == 0;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      int n = at.n * BN + (wn * TN + j) * 16 + c;
+      int n = at.n0 + (wn * TN + j) * 16 + c;
+      bool live = true;
       if (pairs) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] += __shfl_xor(acc[i][j][r], 1);
-        if (c & 1) continue;
+        live = !(c & 1);
         n >>= 1;
       }
-      if (n >= N) continue;
+      live = live && n < N;
+      if (add && live) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (mb + i * 16 + r < M) acc[i][j][r] += sums[(int64_t)n * M + mb + i * 16 + r];
+      }
+      if constexpr (sizeof(T) == 2) {
+        if (wide) {
+#pragma unroll
+          for (int i = 0; i < TM; i += 2) {
+            const TilePair<T> t(acc[i][j] * inv, acc[i + 1][j] * inv);
+            const int m = mb - g * 4 + i * 16 + TilePair<T>::at(g);
+            if (live && m < M) t.store(out + (int64_t)n * M + m);
+          }
+          continue;
+        }
+      }
+      if (!live) continue;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const int m = mb + i * 16;
         const int64_t to = (int64_t)n * M + m;
-        if (M % 4 == 0) {   // rows start 4-element aligned: four values or none
-          if (m >= M) continue;
-          f32x4 v = acc[i][j];
-          if (add) v += *reinterpret_cast<const f32x4*>(sums + to);
-          if (f) {
-            *reinterpret_cast<f32x4*>(f + to) = v;
-          } else {
-            v *= inv;
-            *reinterpret_cast<T4*>(out + to) = T4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-          }
+        if (f && M % 4 == 0) {   // rows start 4-element aligned: four values or none
+          if (m < M) *reinterpret_cast<f32x4*>(f + to) = acc[i][j];
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if (m + r >= M) continue;
-            const float v = acc[i][j][r] + (add ? sums[to + r] : 0.0f);
             if (f)
-              f[to + r] = v;
+              f[to + r] = acc[i][j][r];
             else
-              out[to + r] = (T)(v * inv);
+              out[to + r] = (T)(acc[i][j][r] * inv);
           }
         }
       }
@@ -289,18 +372,19 @@ struct OutEpilogue {
   }
 };
 
-// Adds `count` planes of n values, in their order, to `sums` (if not null: what
-// earlier pieces of the vocabulary left there) and leaves the result in `sums` or,
-// rounded, in `out`.
+// Adds `count` planes of n values (`pitch` apart), in their order, to `before` (if
+// not null: what earlier pieces of the vocabulary left) and leaves the result in
+// `sums` or, rounded, in `out`.
 template <typename T>
-__global__ __launch_bounds__(256) void planes_kernel(const float* planes, int32_t count, int64_t n,
-                                                     const float* before, float* sums, T* out,
-                                                     const float* scale) {
+__global__ __launch_bounds__(256) void planes_kernel(const float* planes, int32_t count,
+                                                     int64_t pitch, int64_t n, const float* before,
+                                                     float* sums, T* out, const float* scale) {
   const float inv = scale ? scale[1] : 1.0f;
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
     float v = before ? before[i] : 0.0f;
-    for (int p = 0; p < count; ++p) v += planes[p * n + i];
+#pragma unroll 4
+    for (int p = 0; p < count; ++p) v += planes[p * pitch + i];
     if (sums)
       sums[i] = v;
     else
@@ -315,11 +399,18 @@ __global__ __launch_bounds__(1024) void scale_kernel(const float* grad, const in
                                                      float* scale) {
   __shared__ float most[16];
   float m = 0.0f;
-#pragma unroll 4
-  for (int n = threadIdx.x; n < tokens; n += 1024) {
-    const float v = fabsf(grad[n]);
-    const int t = targets[n];
-    if (t >= 0 && t < vocab && v <= 3.4028235e38f) m = fmaxf(m, v);
+  for (int64_t n0 = threadIdx.x; n0 < tokens; n0 += 8 * 1024) {
+    float v[8];
+    int32_t t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // all of them on their way at once
+      const int64_t n = n0 + i * 1024;
+      v[i] = n < tokens ? grad[n] : 0.0f;
+      t[i] = n < tokens ? targets[n] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t[i] >= 0 && t[i] < vocab && fabsf(v[i]) <= 3.4028235e38f) m = fmaxf(m, fabsf(v[i]));
   }
   for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
   if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
