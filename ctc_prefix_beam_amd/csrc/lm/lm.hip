@@ -211,6 +211,8 @@ enum { kSmall = 0, kMiddle = 1, kLarge = 2 };
 constexpr TileShape kShapes[3] = {{64, 64, 2}, {128, 128, 2}, {256, 256, 4}};
 constexpr int kResident[3] = {4, 2, 1};   // workgroups that share a CU
 constexpr int kCUs = 256;
+// f32 sums in two levels, which leaves no registers for the large tiles.
+constexpr int largest(int es) { return es == 4 ? kMiddle : kLarge; }
 
 struct Cut {
   int shape;
@@ -226,8 +228,8 @@ size_t up(size_t v, size_t n) { return (v + n - 1) / n * n; }
 // TFLOP/s with bf16, 145 with f32), and when the item is alone on it (`alone`: its
 // fetches' latency), and a launch's beginning and end (`ends`).
 double cut_time(int es, const Cut& c, int64_t m, int64_t n) {
-  constexpr double unit[2][3] = {{0.225, 0.56, 1.5}, {0.56, 2.05, 7.4}};
-  constexpr double alone[2][3] = {{0.45, 0.73, 1.5}, {0.73, 2.28, 7.4}};
+  constexpr double unit[2][3] = {{0.26, 0.56, 1.5}, {0.56, 2.05, 0}};
+  constexpr double alone[2][3] = {{0.5, 0.73, 1.5}, {0.73, 2.28, 0}};
   constexpr double ends[3] = {2.5, 5.0, 8.0};
   const int type = es == 4;
   const int64_t items = (int64_t)c.tiles_m * c.tiles_n * c.splits;
@@ -249,7 +251,7 @@ Cut choose_cut(int es, int64_t m, int64_t n, int64_t K, bool split, double* time
   const int64_t bk = 128 / es;
   Cut best{};
   double least = 0;
-  for (int shape = kSmall; shape <= kLarge; ++shape) {
+  for (int shape = kSmall; shape <= largest(es); ++shape) {
     const int32_t tm = ceil_div(m, kShapes[shape].bm), tn = ceil_div(n, kShapes[shape].bn);
     // parts of k fill a last round at most when there are many tiles
     const int most = !split ? 1 : (int64_t)tm * tn >= 1024 ? 2 : 16;
@@ -282,7 +284,7 @@ Product choose_product(int es, int64_t m, int64_t n, int64_t K, bool split, bool
   Product p{};
   p.main = choose_cut(es, m, n, K, split, &p.time);
   p.n = (int32_t)n;
-  for (int shape = kMiddle; shape <= kLarge && !one; ++shape) {
+  for (int shape = kMiddle; shape <= largest(es) && !one; ++shape) {
     const TileShape& t = kShapes[shape];
     const int64_t tm = ceil_div(m, t.bm), tn = ceil_div(n, t.bn);
     const int64_t slots = kCUs * kResident[shape], rounds = tm * tn / slots;
@@ -447,9 +449,10 @@ template <typename T, bool AKC, bool BKC, typename Epilogue>
 void launch_cut(const Operand& a, const Operand& b, int32_t K, const Cut& c, int32_t n0,
                 const Epilogue& ep, hipStream_t st) {
   const GemmArgs g{a, b, K, c.tiles_m, c.tiles_n, c.splits, c.part, n0};
-  if (c.shape == kLarge)
-    launch_tiles<T, 256, 256, 2, 4, AKC, BKC>(g, ep, kResident[kLarge], st);
-  else if (c.shape == kMiddle)
+  if constexpr (sizeof(T) == 2)
+    if (c.shape == kLarge)
+      return launch_tiles<T, 256, 256, 2, 4, AKC, BKC>(g, ep, kResident[kLarge], st);
+  if (c.shape == kMiddle)
     launch_tiles<T, 128, 128, 2, 2, AKC, BKC>(g, ep, kResident[kMiddle], st);
   else
     launch_tiles<T, 64, 64, 2, 2, AKC, BKC>(g, ep, kResident[kSmall], st);

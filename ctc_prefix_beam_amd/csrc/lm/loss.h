@@ -286,6 +286,7 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* part, int32_t p
   const int v = blockIdx.x * 256 + threadIdx.x;
   if (v >= vocab) return;
   float s = 0.0f;
+#pragma unroll 8
   for (int p = 0; p < parts; ++p) s += part[(int64_t)p * vocab + v];
   dbias[v] = s;
 }

@@ -117,6 +117,23 @@ def test_f16_gradients_keep_small_and_large_rows():
             assert (off[fits] <= 0).all()
 
 
+@pytest.mark.parametrize("N,V,H", [(3, 319, 1377), (1, 700, 2048), (40, 200, 2000),
+                                   (300, 128, 4096)])
+def test_f32_products_over_long_rows(N, V, H):
+    """Their 2-norms, to what sums in parts allow.  The logits reach 16, whose float32
+    are 2^-20 apart, and a rounding is 0.29 of that at the root mean square: H / 128
+    additions of parts and the rounding of lse lose 0.29 2^-20 (sqrt(H / 128) + 1),
+    additions within the parts, of sqrt(128 / H) the size, the same times sqrt(H / 128)
+    sqrt(128) sqrt(128 / H) / 3.  Twice their sum is allowed."""
+    x, w, t, b, grad = make(N, V, H, torch.float32, seed=H, pad=0)
+    _, lse = lm.token_loss_forward(x, w, t, b)
+    got = lm.token_loss_backward(grad, x, w, t, lse, b)
+    want, _ = lm_ref.loss(x, w, t, b, grad)
+    tol = 2 * 0.29 * 2.0 ** -20 * ((H / 128) ** 0.5 + 1 + 128 ** 0.5 / 3)
+    for name, a, e in zip(("dx", "dw", "dbias"), got, want[2:]):
+        assert (a.cpu().double() - e).norm() <= tol * e.norm(), name
+
+
 @pytest.mark.parametrize("bias", [True, False])
 def test_gradient_against_differences(bias):
     x, w, t, b, grad = make(24, 60, 32, torch.float32, bias=bias, seed=5)
