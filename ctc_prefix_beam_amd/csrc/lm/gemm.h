@@ -262,7 +262,7 @@ __device__ inline void interleave() {
 //
 // Products of f32 are summed in parts of kPartTiles k-tiles.  One chain of K additions
 // loses about sqrt(K) roundings of the whole sum, and the error of a logit is the
-// relative error of its exponential: 3 x 319 x 1377 gradients 3.7e-6 off with one chain.
+// relative error of its exponential: 3 x 319 x 1377 gradients 3.7e-6 off with one chain,
 // under 1e-6 with parts.  The second set of sums does not fit beside that of a 256x256 tile,
 // which f32 does not use for that reason (4096 x 16000 x 1024: loss 973 us with it
 // and one chain, 1022 without).

@@ -616,10 +616,13 @@ int ctcpb_lm_cache_release(const ctcpb_lm_release_args* args, void* stream) {
          (!g.finished || !g.lengths || !g.out_lengths || (!g.tables && g.table_width))) ||
         (!g.pool && g.pool_size) || !g.taken || !g.out_taken)
       return fail(CTCPB_ERR_INVALID, kNull);
+    // at least a row to each of a workgroup's waves, and at most a workgroup to a CU
+    const int32_t per = std::max(ceil_div(g.rows, 256), kPlanThreads / 64);
     const ReleaseArgs a{g.finished,  g.lengths,      g.tables, g.taken,       g.pool,
                         g.out_lengths, g.out_taken, g.table_stride, g.rows, g.table_width,
-                        g.pool_size, log2_of(g.page_size)};
-    release_kernel<<<1, kPlanThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
+                        g.pool_size, log2_of(g.page_size), per};
+    release_kernel<<<(unsigned)std::max(ceil_div(g.rows, per), 1), kPlanThreads, 0,
+                     static_cast<hipStream_t>(stream)>>>(a);
     return launched("release_kernel");
   });
 }

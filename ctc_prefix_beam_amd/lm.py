@@ -203,11 +203,13 @@ def cache_plan(lengths, counts, tables, pool, taken, page_size: int, total: int,
 
 
 def cache_release(finished, lengths, tables, pool, taken, page_size: int, stream=None):
-    """Give the pages of the requests with finished[r] != 0 (uint8 on the GPU)
+    """Give the pages of the requests with finished[r] != 0 (uint8 or bool on the GPU)
     back to the pool.  Returns (lengths, taken) afterwards; `pool` changes below
     `taken` only, so the call can be repeated on the same inputs."""
     dev = _gpu(lengths, "lengths")
     rows = lengths.numel()
+    if isinstance(finished, torch.Tensor) and finished.dtype == torch.bool:
+        finished = finished.view(torch.uint8)
     _check_dev(finished, lengths.device, "finished", torch.uint8, (rows,), contiguous=True)
     _i32(lengths, dev, "lengths", (rows,))
     stride, width = _tables(tables, dev, rows)

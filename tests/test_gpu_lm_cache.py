@@ -122,6 +122,25 @@ def test_release_many_rows_and_twice():
     assert int(t) == 0 and args[3][:7].tolist() == back[:7]
 
 
+@pytest.mark.parametrize("rows", [1, 15, 17, 4097])
+def test_release_by_a_bool_mask(rows):
+    page, width = 4, 70
+    rng = np.random.default_rng(rows)
+    lengths = rng.integers(0, page * width + 1, rows).astype(np.int32)
+    pool = rng.permutation(rows * width).astype(np.int32)
+    tables, taken = held_tables(lengths, width, page, pool)
+    fin = rng.random(rows) < 0.7
+    back = [p for r in range(rows) if fin[r] for p in tables[r, :-(-int(lengths[r]) // page)]]
+    p = dev(pool)
+    n, t = lm.cache_release(torch.from_numpy(fin).cuda(), dev(lengths), dev(tables), p,
+                            dev(np.array([taken], np.int32)), page)
+    assert int(t) == taken - len(back)
+    assert np.array_equal(n.cpu().numpy(), np.where(fin, 0, lengths))
+    want = pool.copy()
+    want[taken - len(back):taken] = back
+    assert np.array_equal(p.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("T,H,D,page,order,odd", [
     (1, 1, 8, 4, "thd", False), (37, 8, 128, 16, "thd", False), (500, 3, 80, 64, "htd", False),
