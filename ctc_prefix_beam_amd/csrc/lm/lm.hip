@@ -130,10 +130,22 @@ AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
   const int64_t slots =
       256 * (g.head_dim <= 64 ? 4 : g.head_dim > 128 ? 1 : g.dtype == CTCPB_LM_F32 ? 2 : 3);
   const int64_t steps = ceil_div(std::max<int64_t>(span, 1), kRangeWaves * tile);
-  if (span <= 512 && p.items >= 8 * slots) {
+  // Ranges cost some 15 us more than a workgroup to each item (the prefix sums, the
+  // join), so they are for rows that would keep a workgroup's waves for more than a few
+  // tiles each, where uneven lengths leave CUs idle (f32: fewer, its products take
+  // longer).  Bytes alone decide once there are many items, and a wave to each then
+  // saves joining waves.  16 query and 4 key/value heads of 64, bf16, rows of up to
+  // 256 tokens (us, ranges / a workgroup each / a wave each): 64 rows 20.8 / 5.8 / 12.1,
+  // 256 22.7 / 12.7 / 14.5, 512 27.7 / 21.4 / 18.1; of up to 2048: 64 rows 23.7 / 18.0 /
+  // 81, 1024 233 / 225 / 245, 4096 907 / 861 / 801; of up to 4096: 16 rows 18.8 / 25.6 /
+  // 144, 256 125 / 138 / 204.
+  // wider heads leave a wave too few registers in workgroups of eight
+  const int32_t group_waves = g.head_dim <= 128 ? 8 : 4;
+  const int64_t few = (int64_t)group_waves * tile * (g.dtype == CTCPB_LM_F32 ? 4 : 8);
+  if (span <= few && p.items * 4 * tile >= slots * span) {
     p.waves = 1;
-  } else if (span <= 32 * tile && p.items <= slots / 4) {
-    p.waves = 8;
+  } else if (span <= few) {
+    p.waves = group_waves;
   } else {
     p.waves = 0;
     p.ranges = (int32_t)std::max<int64_t>(
@@ -171,8 +183,7 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   const size_t state = (size_t)std::min(16, a.group) * (DP + 6) * sizeof(float);
   if (p.waves == 1) {
     attn_kernel<T, DP, 1><<<(unsigned)((p.items + 3) / 4), 256, 0, st>>>(a);
-  } else if (p.waves == 8) {
-    // wider heads leave a wave too few registers in workgroups of eight
+  } else if (p.waves) {
     constexpr int NW = DP <= 128 ? 8 : 4;
     launch_with_lds(attn_kernel<T, DP, NW>, (unsigned)p.items, 64 * NW, NW * state, a, st);
   } else {

@@ -90,6 +90,23 @@ def test_many_rows():
     check(*make(lens, 4, 2, 64, torch.bfloat16, 16), 16)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [40, 64, 128, 256])
+@pytest.mark.parametrize("width", [70, 140, 2000])
+@pytest.mark.parametrize("window", [0, 37, 600])
+def test_short_rows_in_tables_of_any_width(dtype, D, width, window):
+    """What the lengths may be decides how the work is split, not what they are."""
+    a = make([0, 1, 3, 16, 17, 0, 500, 64, 1100, 255], 6, 3, D, dtype, 16, seed=D, width=width)
+    check(*a, 16, window=window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 64), (20, 1, 64), (4, 2, 136)])
+def test_many_rows_with_a_window(dtype, Hq, Hkv, D):
+    lens = [(11 * r) % 70 for r in range(1100)]
+    check(*make(lens, Hq, Hkv, D, dtype, 8, seed=D), 8, window=21)
+
+
 def test_max_len_bounds_the_launch_not_the_result():
     a = make([5, 300, 77], 4, 2, 64, torch.bfloat16, 16, width=400)
     x = check(*a, 16)
