@@ -211,8 +211,13 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 
 // ------------------------------------------------------------------ loss --
 
-constexpr size_t kPieceBytes = (size_t)512 << 20;   // workspace for d at a time
-constexpr int32_t kPairRows = 64;                   // tokens up to which d has two rows each
+// Workspace for d at a time.  Larger pieces fill the CUs better and add to dx less often:
+// 20000 x 30000 x 1024 bf16 4340 us with 128 MB, 3381 with 512, 3182 with 2 GB;
+// 8192 x 50000 x 2048 4199 us with 512 MB (two pieces), 4035 in one.
+constexpr size_t kPieceBytes = (size_t)1 << 30;
+// Tokens up to which d has two rows each.  64 x 5000 x 512 bf16 20.3 us with them, 21.5
+// without (another cut); 64 x 20000 x 2048 86 and 75; 128 x 20000 x 2048 108 and 89.
+constexpr int32_t kPairRows = 64;
 
 // How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
 struct TileShape {
@@ -332,8 +337,7 @@ PieceCuts choose_piece(int es, int64_t rows, int64_t vocab, int64_t hidden, bool
 
 // Vocabulary rows of a piece, in whole tiles of any shape: all where d fits the
 // workspace, else the size whose pieces fill the CUs best (of 24 from half of the
-// largest up; at 8192 x 50000 x 2048 pieces of 24576 take 0.87 of the time of four
-// of 12544, estimated).
+// largest up).
 int32_t choose_piece_rows(int es, int64_t rows, int64_t vocab, int64_t hidden) {
   const int64_t unit = 256, all = ceil_div(vocab, unit);
   int64_t most = kPieceBytes / ((rows ? rows : 1) * es) / unit;

@@ -186,8 +186,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const float2* part, cons
 }
 
 // d of one piece of the vocabulary, and the piece's partial sums for dbias.  Bound as
-// the loss is, and by writing d: 8192 x 50000 x 2048 bf16 in two pieces 1.57 ms, 1070
-// TFLOP/s, matrix units busy in 51 % of the cycles.
+// the loss is, and by writing d: 8192 x 50000 x 2048 bf16 1.45 ms, 1155
+// TFLOP/s, matrix units busy in 55 % of the cycles.
 template <typename T>
 struct GradEpilogue {
   Logits lg;
@@ -305,8 +305,8 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* part, int32_t p
 // Where the sums of a launch go: out[n, m] (m contiguous), rounded, or float32
 // `sums`, added to what earlier pieces of the vocabulary left there (`add`);
 // with k in parts, each part's sums to its own [N][M] plane.  The products are bound by
-// the matrix units, busy in 60 % (dx) and 64 % (dw) of the cycles at 8192 x 50000 x 2048
-// bf16: 1.33 and 1.34 ms, 1260 and 1250 TFLOP/s.
+// the matrix units, busy in 65 % (dx) and 68 % (dw) of the cycles at 8192 x 50000 x 2048
+// bf16: 1.25 and 1.30 ms, 1345 and 1290 TFLOP/s.
 template <typename T>
 struct OutEpilogue {
   T* out;

@@ -184,8 +184,10 @@ int ctcpb_lm_loss(const ctcpb_lm_loss_args* args, void* workspace, size_t worksp
  *   dx       device, typed [rows][hidden], contiguous;  dw: device, typed
  *            [vocab][hidden], contiguous;  dbias: device float32 [vocab].  Any
  *            of them may be NULL and is then not computed.
- * With 16-bit types d is rounded to that type before the products (for f16
- * after a power-of-two scaling that keeps it in range); sums are float32. */
+ * With 16-bit types d is rounded to that type before the products, scaled so
+ * that the largest |grad| is a power of two (which keeps f16 in range and the
+ * rounding small), and to the sum of two such values for up to 64 rows; sums
+ * are float32.  The workspace holds up to 1 GiB of d at a time. */
 typedef struct {
   const void *x, *w;
   const float* bias;
