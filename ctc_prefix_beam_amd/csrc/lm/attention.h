@@ -51,7 +51,9 @@ namespace ctcpb_lm {
 // Ranges are counted in steps of the four waves' tiles, at least kLeastSteps each: with
 // shorter ones, joining costs what splitting gains.  One request of 30000 tokens takes
 // 36 us with 4, 30 with 8; 32 requests of 100 to 2000 tokens 38 us with 4, 40 with 8.
-constexpr int kRangeWaves = 4;
+// Where the rows' average is less, it is that: shorter rows are then not done one after
+// another by a few workgroups (64 requests of up to 64 tokens, with tables of 8192: 19.9 us
+// with six always, 9.5 so).
 constexpr int kLeastSteps = 6;
 
 struct AttnArgs {
@@ -585,7 +587,7 @@ __device__ inline int row_steps(const Range& rg) {
 
 // Steps of a range, for `total` steps in all.
 __device__ inline int range_steps(const AttnArgs& a, int total) {
-  return max((total + a.ranges - 1) / a.ranges, kLeastSteps);
+  return max((total + a.ranges - 1) / a.ranges, min(kLeastSteps, total / a.rows));
 }
 
 // Where a part goes: a workgroup has two places, for the row that began in an

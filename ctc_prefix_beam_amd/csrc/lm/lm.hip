@@ -130,14 +130,14 @@ AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
   const int64_t slots =
       256 * (g.head_dim <= 64 ? 4 : g.head_dim > 128 ? 1 : g.dtype == CTCPB_LM_F32 ? 2 : 3);
   const int64_t steps = ceil_div(std::max<int64_t>(span, 1), kRangeWaves * tile);
-  // Ranges cost some 15 us more than a workgroup to each item (the prefix sums, the
+  // Ranges cost some 6 us more than a workgroup to each item (the prefix sums, the
   // join), so they are for rows that would keep a workgroup's waves for more than a few
   // tiles each, where uneven lengths leave CUs idle (f32: fewer, its products take
   // longer).  Bytes alone decide once there are many items, and a wave to each then
   // saves joining waves.  16 query and 4 key/value heads of 64, bf16, rows of up to
-  // 256 tokens (us, ranges / a workgroup each / a wave each): 64 rows 20.8 / 5.8 / 12.1,
-  // 256 22.7 / 12.7 / 14.5, 512 27.7 / 21.4 / 18.1; of up to 2048: 64 rows 23.7 / 18.0 /
-  // 81, 1024 233 / 225 / 245, 4096 907 / 861 / 801; of up to 4096: 16 rows 18.8 / 25.6 /
+  // 256 tokens (us, ranges / a workgroup each / a wave each): 64 rows 12.0 / 5.8 / 12.1,
+  // 256 17.6 / 12.7 / 14.5, 512 23.7 / 21.4 / 18.1; of up to 2048: 64 rows 23.7 / 18.0 /
+  // 81, 1024 233 / 225 / 245, 4096 886 / 861 / 801; of up to 4096: 16 rows 18.8 / 25.6 /
   // 144, 256 125 / 138 / 204.
   // wider heads leave a wave too few registers in workgroups of eight
   const int32_t group_waves = g.head_dim <= 128 ? 8 : 4;
@@ -148,8 +148,7 @@ AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
     p.waves = group_waves;
   } else {
     p.waves = 0;
-    p.ranges = (int32_t)std::max<int64_t>(
-        1, std::min(slots / all, (g.rows * steps + kLeastSteps - 1) / kLeastSteps));
+    p.ranges = (int32_t)std::max<int64_t>(1, std::min(slots / all, g.rows * steps));
     p.o_part = ((size_t)(g.rows + 1) * sizeof(int32_t) + 255) / 256 * 256;
     p.bytes = p.o_part + (size_t)p.ranges * all * 2 * std::min(16, group) * (g.head_dim + 2) *
                              sizeof(float);
