@@ -54,6 +54,7 @@ namespace ctcpb_lm {
 // Where the rows' average is less, it is that: shorter rows are then not done one after
 // another by a few workgroups (64 requests of up to 64 tokens, with tables of 8192: 19.9 us
 // with six always, 9.5 so).
+constexpr int kRangeWaves = 4;
 constexpr int kLeastSteps = 6;
 
 struct AttnArgs {
