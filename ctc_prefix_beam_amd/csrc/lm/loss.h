@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* part, int32_t p
 // Where the sums of a launch go: out[n, m] (m contiguous), rounded, or float32
 // `sums`, added to what earlier pieces of the vocabulary left there (`add`);
 // with k in parts, each part's sums to its own [N][M] plane.  The products are bound by
-// the matrix units, busy in 65 % (dx) and 68 % (dw) of the cycles at 8192 x 50000 x 2048
+// the matrix units, busy in 65 % (dx) and 67 % (dw) of the cycles at 8192 x 50000 x 2048
 // bf16: 1.25 and 1.30 ms, 1345 and 1290 TFLOP/s.
 template <typename T>
 struct OutEpilogue {
