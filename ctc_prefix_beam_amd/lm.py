@@ -409,19 +409,34 @@ class PagedCache:
         self.lengths = torch.zeros(rows, dtype=torch.int32, device=device)
         self.taken = torch.zeros(1, dtype=torch.int32, device=device)
 
+    def _keep(self, stream, *tensors):
+        """Marks `tensors` as used by the call just made on `stream` (None: the current
+        one), so that their memory, should the cache give it up, is not handed out again
+        before that call has run: it may belong to another stream."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.k.device)
+        for t in tensors:
+            t.record_stream(stream)
+
     def append(self, counts, total: int, stream=None) -> CachePlan:
         plan = cache_plan(self.lengths, counts, self.tables, self.pool, self.taken,
                           self.page_size, total, stream)
+        self._keep(stream, self.lengths, self.taken, self.tables, self.pool)
         self.lengths, self.taken = plan.lengths, plan.taken
         return plan
 
     def store(self, k, v, slots, layer: int = 0, stream=None):
         cache_store(k, v, slots, self.k[layer], self.v[layer], stream)
+        self._keep(stream, self.k, self.v)
 
     def attend(self, q, layer: int = 0, scale=None, window: int = 0, max_len: int = 0, stream=None):
-        return attention(q, self.k[layer], self.v[layer], self.tables, self.lengths, scale, window,
-                         max_len or self.max_len, stream=stream)
+        got = attention(q, self.k[layer], self.v[layer], self.tables, self.lengths, scale, window,
+                        max_len or self.max_len, stream=stream)
+        self._keep(stream, self.k, self.v, self.tables, self.lengths)
+        return got
 
     def release(self, finished, stream=None):
-        self.lengths, self.taken = cache_release(finished, self.lengths, self.tables, self.pool,
-                                                 self.taken, self.page_size, stream)
+        lengths, taken = cache_release(finished, self.lengths, self.tables, self.pool, self.taken,
+                                       self.page_size, stream)
+        self._keep(stream, self.lengths, self.taken, self.tables, self.pool)
+        self.lengths, self.taken = lengths, taken

@@ -1,0 +1,51 @@
+"""What the binding of the language-model operators does on the host, without a
+GPU: the library's calls are replaced by stand-ins."""
+import pytest
+import torch
+
+from ctc_prefix_beam_amd import lm
+
+
+class Marked:
+    """A tensor's stand-in that keeps the streams it was marked as used on."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def marked_cache():
+    c = lm.PagedCache(2, 32, 1, 8, dtype=torch.float32, device="cpu")
+    for name in ("k", "v", "tables", "pool", "lengths", "taken"):
+        setattr(c, name, Marked())
+    return c
+
+
+@pytest.mark.parametrize("call", ["append", "release"])
+def test_memory_that_a_cache_gives_up_is_kept_for_the_stream_that_reads_it(call, monkeypatch):
+    """append and release leave the old lengths and `taken` to the allocator while the
+    call on `stream` may not have read them yet."""
+    new = lm.CachePlan(*[torch.zeros(1)] * 6)
+    monkeypatch.setattr(lm, "cache_plan", lambda *a: new)
+    monkeypatch.setattr(lm, "cache_release", lambda *a: (new.lengths, new.taken))
+    c, stream = marked_cache(), object()
+    held = [c.lengths, c.taken, c.tables, c.pool]
+    if call == "append":
+        c.append(None, 1, stream=stream)
+    else:
+        c.release(None, stream=stream)
+    assert c.lengths is new.lengths and c.taken is new.taken
+    assert all(t.streams == [stream] for t in held)
+
+
+def test_a_cache_dropped_after_a_call_is_kept_for_the_stream_of_the_call(monkeypatch):
+    monkeypatch.setattr(lm, "cache_store", lambda *a: None)
+    monkeypatch.setattr(lm, "attention", lambda *a, **kw: None)
+    c, stream = marked_cache(), object()
+    monkeypatch.setattr(Marked, "__getitem__", lambda self, layer: None, raising=False)
+    c.store(None, None, None, stream=stream)
+    assert c.k.streams == [stream] and c.v.streams == [stream]
+    c.attend(None, stream=stream)
+    assert c.tables.streams == [stream] and c.lengths.streams == [stream]
