@@ -603,11 +603,18 @@ __device__ inline int range_steps(const AttnArgs& a, int total) {
   return max((total + a.ranges - 1) / a.ranges, min(kLeastSteps, total / a.rows));
 }
 
+// Floats of a part's place: D values, m and l for each head of a tile, up to a whole number
+// of 16 bytes (which an odd number of heads does not make), since parts are accessed 16
+// bytes at a time.
+__host__ __device__ inline int part_floats(int group, int D) {
+  return ((group < 16 ? group : 16) * (D + 2) + 3) & ~3;
+}
+
 // Where a part goes: a workgroup has two places, for the row that began in an
 // earlier range (or with the range) and for one that begins inside it.
 __device__ inline float* part_at(const AttnArgs& a, int range, int hh, bool inside) {
   const int64_t slot = ((int64_t)range * a.kv_heads * a.head_tiles + hh) * 2 + inside;
-  return a.part + slot * min(16, a.group) * (a.D + 2);
+  return a.part + slot * part_floats(a.group, a.D);
 }
 
 template <typename T, int DP>

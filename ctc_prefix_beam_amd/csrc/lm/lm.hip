@@ -150,8 +150,8 @@ AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
     p.waves = 0;
     p.ranges = (int32_t)std::max<int64_t>(1, std::min(slots / all, g.rows * steps));
     p.o_part = ((size_t)(g.rows + 1) * sizeof(int32_t) + 255) / 256 * 256;
-    p.bytes = p.o_part + (size_t)p.ranges * all * 2 * std::min(16, group) * (g.head_dim + 2) *
-                             sizeof(float);
+    p.bytes = p.o_part +
+              (size_t)p.ranges * all * 2 * part_floats(group, g.head_dim) * sizeof(float);
   }
   return p;
 }

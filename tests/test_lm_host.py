@@ -1,9 +1,20 @@
 """What the binding of the language-model operators does on the host, without a
 GPU: the library's calls are replaced by stand-ins."""
+import ctypes
+import os
+
 import pytest
 import torch
 
 from ctc_prefix_beam_amd import lm
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(lm.LIB_PATH):
+        from ctc_prefix_beam_amd import build
+        build.build_lm()
+    return lm.lib()
 
 
 class Marked:
@@ -49,3 +60,21 @@ def test_a_cache_dropped_after_a_call_is_kept_for_the_stream_of_the_call(monkeyp
     assert c.k.streams == [stream] and c.v.streams == [stream]
     c.attend(None, stream=stream)
     assert c.tables.streams == [stream] and c.lengths.streams == [stream]
+
+
+@pytest.mark.parametrize("dtype,D", [(0, 64), (1, 72), (2, 128)])
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 16, 17, 40])
+def test_every_part_of_a_split_row_begins_on_16_bytes(L, group, dtype, D):
+    """The parts lie one after another behind the rows' prefix sums, two to a range, and
+    are accessed 16 bytes at a time: an odd number of ranges shows a place that is not a
+    multiple of 16 bytes."""
+    n, page = 128 * 65, 16   # 65 steps of four tiles of 32 tokens (f32: 130 of 16)
+    out = ctypes.c_size_t()
+    assert L.ctcpb_lm_attention_workspace(lm._ATTENTION.pack(
+        0, 0, 0, 0, 0, 0, 0, 0, 0, n // page, *(256, 64, 64, 64) * 2, dtype, 1, group, 1, D, 1, page,
+        n // page, n, 0, 1.0), out) == 0
+    tiles, ranges = -(-group // 16), 65 if dtype < 2 else 130
+    places = ranges * tiles * 2
+    each, rest = divmod(out.value - 256, places)   # prefix sums of one row: 256 bytes
+    assert rest == 0 and each % 16 == 0
+    assert each >= min(16, group) * (D + 2) * 4
