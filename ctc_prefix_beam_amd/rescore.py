@@ -83,6 +83,23 @@ def _norm(x):
     return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
 
 
+def _longest(model: LanguageModel, toks, lens) -> int:
+    """Tokens of the longest hypothesis (-1: there is none).  What the model's tables cannot
+    be indexed with is refused here: on the GPU it would be read past their ends."""
+    rows, L = toks.shape
+    if rows == 0:
+        return -1
+    used = torch.arange(L, device=toks.device) < lens[:, None]
+    label = torch.where(used, toks, -1).amax(1) if L else torch.full_like(lens, -1)
+    longest, label = torch.stack((lens.clamp(max=L).amax(), label.amax())).tolist()
+    if longest > model.cfg.max_len:
+        raise ValueError(f"a hypothesis has {longest} tokens, the model's max_len is "
+                         f"{model.cfg.max_len}")
+    if label >= model.cfg.vocab:
+        raise ValueError(f"label {label} is outside the model's vocabulary of {model.cfg.vocab}")
+    return longest
+
+
 def score(model: LanguageModel, tokens, lengths, keep_states: bool = False):
     """Log-probabilities (B, N) of hypotheses as the decoder gives them: tokens
     (B, N, L) int32, -1 padded, lengths (B, N) int32.  Each is scored with the end
@@ -92,12 +109,13 @@ def score(model: LanguageModel, tokens, lengths, keep_states: bool = False):
     B, N, L = tokens.shape
     rows = B * N
     toks, lens = tokens.reshape(rows, L), lengths.reshape(rows)
+    longest = _longest(model, toks, lens)
     cache = model.cache(rows, L + 1)
     total = torch.zeros(rows, device=tokens.device)
     end = torch.zeros(rows, dtype=torch.int32, device=tokens.device)
     states, targets = [], []
     now = end.long()
-    for t in range(min(L, int(lens.max())) + 1):
+    for t in range(longest + 1):
         alive = lens >= t
         target = toks[:, t] if t < L else torch.full_like(end, -1)
         target = torch.where(lens > t, target, torch.where(lens == t, end, -1)).contiguous()
@@ -109,7 +127,11 @@ def score(model: LanguageModel, tokens, lengths, keep_states: bool = False):
             targets.append(target)
         now = target.clamp(min=0).long()
     total = total.view(B, N)
-    return (total, torch.stack(states), torch.stack(targets)) if keep_states else total
+    if not keep_states:
+        return total
+    if not states:
+        return total, model.out[:0][None], end[None]
+    return total, torch.stack(states), torch.stack(targets)
 
 
 def rescore(model: LanguageModel, tokens, lengths, scores, weight: float = 0.3):
