@@ -374,12 +374,27 @@ class _TokenLoss(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx, dw, db = token_loss_backward(grad.contiguous(), x, w, targets, lse, bias,
                                          (need[0], need[1], need[3]))
+        if torch.is_grad_enabled():   # create_graph: the gradients are asked to have a graph
+            dx, dw, db = _Last.apply((dx, dw, db), grad, x, w, bias)
         return dx, dw, None, db
+
+
+class _Last(torch.autograd.Function):
+    """Gradients that cannot be differentiated again: the library's carry no graph, and what
+    would follow from them would be left out without a word."""
+
+    @staticmethod
+    def forward(ctx, gradients, *of):
+        return tuple(None if g is None else g.view_as(g) for g in gradients)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("token_loss cannot be differentiated twice")
 
 
 def token_loss(x, w, targets, bias=None):
     """The losses of ``token_loss_forward`` as a torch function: gradients flow
-    to x, w and bias."""
+    to x, w and bias.  First derivatives only; differentiating them again raises."""
     return _TokenLoss.apply(x, w, targets, bias)
 
 

@@ -78,3 +78,18 @@ def test_every_part_of_a_split_row_begins_on_16_bytes(L, group, dtype, D):
     each, rest = divmod(out.value - 256, places)   # prefix sums of one row: 256 bytes
     assert rest == 0 and each % 16 == 0
     assert each >= min(16, group) * (D + 2) * 4
+
+
+def test_second_derivatives_of_the_token_loss_are_refused(monkeypatch):
+    """The gradients come from the library and carry no graph of their own: a loss of them
+    would lose their part without a word."""
+    monkeypatch.setattr(lm, "token_loss_forward",
+                        lambda x, w, t, b: ((x.detach() ** 3).sum(1), x.detach().sum(1)))
+    monkeypatch.setattr(lm, "token_loss_backward",
+                        lambda g, x, w, t, lse, b, need: (g[:, None] * 3 * x ** 2, None, None))
+    x = torch.ones((2, 3), requires_grad=True)
+    loss = lm.token_loss(x, torch.zeros(4, 3), torch.zeros(2, dtype=torch.int32)).sum()
+    (d,) = torch.autograd.grad(loss, x, create_graph=True)
+    assert torch.equal(d, torch.full_like(d, 3.0))
+    with pytest.raises(RuntimeError, match="twice"):
+        (loss + d.pow(2).sum()).backward()
