@@ -400,12 +400,14 @@ def token_loss(x, w, targets, bias=None):
 
 class PagedCache:
     """The paged key/value cache of a model's attention layers and its page
-    allocator, for `rows` requests of at most `max_len` tokens each.  The layers
-    share their pages' numbers, so one plan serves them all.
+    allocator, for `rows` requests of at most `max_len` tokens each, rounded up to
+    whole pages (`self.max_len`): tokens past that have no slot, and are flagged.
+    The layers share their pages' numbers, so one plan serves them all.
 
     ``append(counts, total)`` hands out pages, ``store(k, v, slots, layer)``
     writes a layer's new tokens, ``attend(q, layer)`` attends over each request's
-    tokens, and ``release(finished)`` gives pages back.  `num_pages` (default:
+    tokens (`max_len`: a closer bound of the lengths, where the caller knows one), and
+    ``release(finished)`` gives pages back.  `num_pages` (default:
     every request at max_len) may be smaller: a request the pool cannot serve is
     flagged in the plan's status and holds only the tokens that have a slot.  Use
     one PagedCache per stream, or order its calls."""
@@ -415,7 +417,7 @@ class PagedCache:
                  layers: int = 1):
         width = -(-max_len // page_size)
         num_pages = num_pages or max(1, rows * width)
-        self.page_size, self.max_len = page_size, max_len
+        self.page_size, self.max_len = page_size, width * page_size
         self.k = torch.empty((layers, num_pages, page_size, kv_heads, head_dim), dtype=dtype,
                              device=device)
         self.v = torch.empty_like(self.k)
@@ -446,7 +448,7 @@ class PagedCache:
 
     def attend(self, q, layer: int = 0, scale=None, window: int = 0, max_len: int = 0, stream=None):
         got = attention(q, self.k[layer], self.v[layer], self.tables, self.lengths, scale, window,
-                        max_len or self.max_len, stream=stream)
+                        max_len, stream=stream)
         self._keep(stream, self.k, self.v, self.tables, self.lengths)
         return got
 

@@ -38,3 +38,29 @@ def test_calls_on_a_late_stream_read_what_they_were_given(call):
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert len(taken) == 80
+
+
+@pytest.mark.parametrize("max_len,page", [(100, 16), (65, 64), (128, 16), (1, 4)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_rows_up_to_the_last_place_of_their_last_page(max_len, page, window):
+    """The tables hold max_len tokens rounded up to whole pages: as many are taken, all of
+    them are attended to, and what goes past them is flagged."""
+    n = -(-max_len // page) * page
+    g = torch.Generator().manual_seed(max_len)
+    c = lm.PagedCache(2, max_len, 1, 64, torch.float32, page)
+    k, v = torch.randn((2, n, 1, 64), generator=g), torch.randn((2, n, 1, 64), generator=g)
+    for first, more in ((0, n - 1), (n - 1, 1)):   # row 1 stays one behind at first
+        plan = c.append(i32(more, more), 2 * more)
+        assert not plan.status.any()
+        c.store(k[:, first:first + more].flatten(0, 1).cuda(),
+                v[:, first:first + more].flatten(0, 1).cuda(), plan.slots)
+    assert c.lengths.tolist() == [n, n]
+    q = 2 * torch.randn((2, 1, 64), generator=g)
+    out, lse = c.attend(q.cuda(), window=window)
+    lo = max(0, n - window) if window else 0
+    for r in range(2):
+        s = k[r, lo:, 0].double() @ q[r, 0].double() / 8
+        want = torch.softmax(s, 0) @ v[r, lo:, 0].double()
+        assert torch.allclose(out[r, 0].cpu().double(), want, atol=1e-5, rtol=0)
+        assert abs(float(lse[r, 0]) - float(torch.logsumexp(s, 0))) < 1e-5
+    assert c.append(i32(1, 0), 1).status.tolist() == [lm.NO_ENTRY, 0]
