@@ -31,9 +31,12 @@
 //   16-byte load per token, 256 contiguous bytes per 16 lanes); the transposed
 //   operand for d = 8c + j is a byte permutation within the lane.
 // - The probabilities of 16-bit types enter the second product as the sum of
-//   two values of that type (high part and remainder): the products are not
-//   what bounds the kernel, and the output then differs from the exact one by
-//   its own rounding only.
+//   two values of that type (high part and remainder), which have 16 bits together
+//   (bf16) or 22: the products are not what bounds the kernel, and the output then
+//   differs from the exact one by its own rounding and some 2^-17 of the values.  f16
+//   ends at 2^-24, so its probabilities are multiplied by 2^15 first: without that, what
+//   a wave added for tokens 17 below the largest score it had met was 1.4 times too
+//   much, and nothing for those 18 below, while the sum l counted them in full.
 //
 // What bounds it, measured: memory.  256 requests of 1..4095 tokens, 32 query and 8
 // key/value heads of 128, bf16: 2.15 GB in 419 us, 5.1 TB/s, where a kernel that only
@@ -81,6 +84,7 @@ struct Elem;
 template <>
 struct Elem<__bf16> {
   typedef bf16x8 V8;
+  static constexpr float kRaise = 1.0f;   // of the probabilities in the second product
   static __device__ f32x4 mfma(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -88,12 +92,15 @@ struct Elem<__bf16> {
 template <>
 struct Elem<_Float16> {
   typedef f16x8 V8;
+  static constexpr float kRaise = 32768.0f;   // the largest power of two that f16 holds
   static __device__ f32x4 mfma(V8 a, V8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
 template <>
-struct Elem<float> {};
+struct Elem<float> {
+  static constexpr float kRaise = 1.0f;
+};
 
 // A request's range of tokens [lo, hi), lo rounded down to `tile` in `base`.
 struct Range {
@@ -121,7 +128,7 @@ __device__ inline Range attn_range_uniform(const AttnArgs& a, int row, int tile)
 template <int NA>
 struct WaveState {
   float m, l;      // scores stay in natural units: times log2(e), the lowest float is -inf
-  f32x4 acc[NA];   // acc[j][r]: see the tile functions for the d each one is
+  f32x4 acc[NA];   // kRaise times the sums; acc[j][r]: see the tile functions for the d
 };
 
 // The page of token t's group of four.  It does not wait for the request's length:
@@ -271,8 +278,9 @@ struct Tile {
     for (int i = 0; i < 8; ++i) {
       p[i] = exp_fast(p[i] - m0);
       s.l += p[i];
-      hi[i] = (T)p[i];
-      lo[i] = (T)(p[i] - (float)hi[i]);
+      const float x = p[i] * Elem<T>::kRaise;
+      hi[i] = (T)x;
+      lo[i] = (T)(x - (float)hi[i]);
     }
 #pragma unroll
     for (int b = 0; b < kH; ++b)
@@ -479,7 +487,8 @@ struct Attend {
   }
 
   // Joins the states of NW waves through LDS ([NW][nh][kPitch] sums, then (m, l)
-  // pairs): to the result, or to `part` ([nh][D], then [nh] pairs) if not null.
+  // pairs): to the result, or to `part` ([nh][D], then [nh] pairs) if not null.  The
+  // sums lose their factor kRaise here.
   template <int NW>
   __device__ void join(const AttnArgs& a, int row, int wave, float* lds, float* part) {
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
@@ -499,7 +508,8 @@ struct Attend {
           for (int j = 0; j < kRun; j += 4)
             *reinterpret_cast<f32x4*>(mine + TL::run_of(b, r) + j) =
                 f32x4{s.acc[b * kRun + j][r], s.acc[b * kRun + j + 1][r],
-                      s.acc[b * kRun + j + 2][r], s.acc[b * kRun + j + 3][r]};
+                      s.acc[b * kRun + j + 2][r], s.acc[b * kRun + j + 3][r]} *
+                (1.0f / Elem<T>::kRaise);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < nh * (DP / 4); i += 64 * NW) {
@@ -578,7 +588,7 @@ void attn_kernel(AttnArgs a) {
     const int lane = threadIdx.x & 63, c = lane & 15;
     const float l = sum_over_groups(at.s.l);
     if (!at.live()) return;
-    const float scale = l == 0.0f ? 0.0f : 1.0f / l;
+    const float scale = l == 0.0f ? 0.0f : 1.0f / l * (1.0f / Elem<T>::kRaise);
 #pragma unroll
     for (int b = 0; b < A::kRuns; ++b)
 #pragma unroll
