@@ -30,3 +30,34 @@ def test_second_derivatives_are_refused(dtype):
     assert all(torch.equal(a, c) for a, c in zip(got, want))
     with pytest.raises(RuntimeError, match="twice"):
         (loss + sum(a.float().pow(2).sum() for a in got)).backward()
+
+
+@pytest.mark.parametrize("dtype,N,V", [(torch.float32, 70000, 5003), (torch.float16, 140000, 5003),
+                                       (torch.bfloat16, 140000, 9001)])
+def test_pieces_of_the_vocabulary(dtype, N, V):
+    """More d than is made at a time (1 GiB): dx is summed over two or three pieces.  dw and
+    dbias, and dx of some rows, against 64 bits in the 2-norm: two roundings to the type
+    (f32: sums of float32, 2^-16 of them at most)."""
+    assert N * (-(-V // 256) * 256) * x_size(dtype) > 1 << 30
+    H = 64
+    x, w, t, b, grad = make(N, V, H, dtype, seed=9)
+    _, lse = lm.token_loss_forward(x, w, t, b)
+    dx, dw, db = lm.token_loss_backward(grad, x, w, t, lse, b)
+    w64, dw64, db64 = w.double(), torch.zeros((V, H), dtype=torch.float64, device="cuda"), 0
+    tol = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -16}[dtype]
+    for a in range(0, N, 20000):
+        z = x[a:a + 20000].double() @ w64.t() + b.double()
+        d = torch.softmax(z, 1)
+        live = torch.nonzero(t[a:a + 20000] >= 0)[:, 0]
+        d[live, t[a:a + 20000][live].long()] -= 1
+        d *= torch.where(t[a:a + 20000] >= 0, grad[a:a + 20000], 0.0).double()[:, None]
+        want = d @ w64
+        assert float((dx[a:a + 20000].double() - want).norm() / want.norm()) < tol
+        dw64 += d.t().contiguous() @ x[a:a + 20000].double()
+        db64 = db64 + d.sum(0)
+    assert float((dw.double() - dw64).norm() / dw64.norm()) < tol
+    assert float((db.double() - db64).norm() / db64.norm()) < 2.0 ** -16
+
+
+def x_size(dtype):
+    return torch.empty((), dtype=dtype).element_size()
