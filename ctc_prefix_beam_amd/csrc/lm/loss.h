@@ -229,13 +229,13 @@ struct GradEpilogue {
       const bool live = n < lg.tokens;
       const int t = live ? __float_as_int(got[BM + k]) : -1;
       const bool in = t >= 0 && t < lg.vocab;
-      // a row without a target: exp(logit - inf) = 0
+      // a row without a target has d = 0, whatever its logits are
       const float gn = in ? sc * got[BM + 2 * BN + k] : 0.0f;
-      const float ln = in ? got[BM + BN + k] : __builtin_huge_valf();
+      const float ln = got[BM + BN + k];
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = gn * exp_of<T>(acc[i][j][r] - ln);
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = in ? gn * exp_of<T>(acc[i][j][r] - ln) : 0.0f;
       if (__any(in && t >= vb && t < vb + TM * 16)) {   // few tiles have a target
 #pragma unroll
         for (int i = 0; i < TM; ++i)

@@ -341,7 +341,8 @@ def token_loss_forward(x, w, targets, bias=None, stream=None):
 def token_loss_backward(grad, x, w, targets, lse, bias=None, need=(True, True, True), stream=None):
     """Gradients (dx, dw, dbias) of sum(grad * loss) for ``token_loss_forward``
     with its lse; grad (rows,) float32.  dx and dw have x's and w's type, dbias
-    is float32 (None without a bias).  `need` says which of them to compute."""
+    is float32 (None without a bias).  `need` says which of them to compute.  Rows
+    whose target is outside the vocabulary add nothing (for dw their x has to be finite)."""
     dev, N, V, H, sizes = _loss_args(x, w, targets, bias)
     _floats(grad, dev, "grad", N)
     _floats(lse, dev, "lse", N)

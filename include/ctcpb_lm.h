@@ -179,7 +179,8 @@ int ctcpb_lm_loss(const ctcpb_lm_loss_args* args, void* workspace, size_t worksp
  * piece from lse:
  *   d[n, v] = grad[n] * (exp(logit[n, v] - lse[n]) - (v == targets[n]))
  *   dx = d w     dw = d^T x     dbias[v] = sum_n d[n, v]
- * Rows without a target have no part in any of them.
+ * Rows without a target have d = 0 and no part in dx and dbias, whatever their x
+ * holds; for dw their x has to be finite, as 0 times infinity is NaN.
  *   grad     device float32 [rows];  lse: as ctcpb_lm_loss left it
  *   dx       device, typed [rows][hidden], contiguous;  dw: device, typed
  *            [vocab][hidden], contiguous;  dbias: device float32 [vocab].  Any

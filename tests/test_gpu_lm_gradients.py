@@ -32,6 +32,22 @@ def test_second_derivatives_are_refused(dtype):
         (loss + sum(a.float().pow(2).sum() for a in got)).backward()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [40, 300])
+@pytest.mark.parametrize("garbage", [float("nan"), float("inf")])
+def test_rows_without_a_target_hold_anything(dtype, N, garbage):
+    """Their x may be NaN or infinite: no part of it gets into dx and dbias."""
+    x, w, t, b, grad = make(N, 500, 64, dtype, pad=0.2)
+    dead = t < 0
+    _, lse = lm.token_loss_forward(x, w, t, b)
+    want = lm.token_loss_backward(grad, x, w, t, lse, b)
+    x[dead] = garbage
+    loss, lse = lm.token_loss_forward(x, w, t, b)
+    dx, _, db = lm.token_loss_backward(grad, x, w, t, lse, b, need=(True, False, True))
+    assert (loss[dead] == 0).all() and (dx[dead] == 0).all()
+    assert torch.equal(dx, want[0]) and torch.equal(db, want[2])
+
+
 @pytest.mark.parametrize("dtype,N,V", [(torch.float32, 70000, 5003), (torch.float16, 140000, 5003),
                                        (torch.bfloat16, 140000, 9001)])
 def test_pieces_of_the_vocabulary(dtype, N, V):
