@@ -373,6 +373,26 @@ bool row_aligned(const void* p, int64_t stride, int es) {
   return aligned(p, 16) && stride * es % 16 == 0 && stride * es <= (1 << 23);
 }
 
+// Rows of a product's result, of `n`, that a launch of it makes.
+int64_t rows_made(const Product& q, int64_t n, bool rest) {
+  if (q.rest.tiles_n == 0) return rest ? 0 : n;
+  return rest ? n - q.n : q.n;
+}
+
+// Floats that the parts of k of a product leave: the two launches use the same place.
+size_t plane_floats(const Product& q, int64_t n, int32_t hidden) {
+  size_t most = 0;
+  for (int rest = 0; rest < 2; ++rest) {
+    const int32_t splits = rest ? q.rest.splits : q.main.splits;
+    if (splits > 1) most = std::max(most, (size_t)splits * rows_made(q, n, rest) * hidden);
+  }
+  return most;
+}
+
+// Also the partial sums for dbias, where it is asked for.
+bool wants_dbias(const ctcpb_lm_loss_args&) { return false; }
+bool wants_dbias(const ctcpb_lm_grad_args& g) { return g.dbias != nullptr; }
+
 template <typename Args>
 LossPlan plan_loss(const Args& g, bool grad) {
   const int32_t rows = g.rows, vocab = g.vocab, hidden = g.hidden;
@@ -399,22 +419,22 @@ LossPlan plan_loss(const Args& g, bool grad) {
     p.pairs = p.es == 2 && rows <= kPairRows;
     p.piece = choose_piece_rows(p.es, p.pairs ? 2 * rows : rows, vocab, p.padded);
     p.pieces = ceil_div(vocab, p.piece);
-    p.whole = choose_piece(p.es, rows, p.pieces > 1 ? p.piece : vocab, p.padded, p.pairs);
-    p.tail =
-        choose_piece(p.es, rows, vocab - (int64_t)(p.pieces - 1) * p.piece, p.padded, p.pairs);
+    const int32_t first = p.pieces > 1 ? p.piece : vocab;
+    const int32_t last = (int32_t)(vocab - (int64_t)(p.pieces - 1) * p.piece);
+    p.whole = choose_piece(p.es, rows, first, p.padded, p.pairs);
+    p.tail = choose_piece(p.es, rows, last, p.padded, p.pairs);
     p.o_d = take((size_t)rows * (p.pairs ? 2 : 1) * p.piece * p.es);
     if (p.pieces > 1) p.o_sums = take((size_t)rows * hidden * sizeof(float));
     size_t planes = 0, parts = 0;
     for (const PieceCuts* c : {&p.whole, &p.tail}) {
-      const size_t sx = std::max(c->dx.main.splits, c->dx.rest.splits);
-      const size_t sw = std::max(c->dw.main.splits, c->dw.rest.splits);
-      if (sx > 1) planes = std::max(planes, sx * rows * hidden);
-      if (sw > 1) planes = std::max(planes, sw * p.piece * hidden);
-      parts =
-          std::max(parts, (size_t)dbias_parts(c->logits.main) + dbias_parts(c->logits.rest));
+      const int32_t made = c == &p.whole ? first : last;   // vocabulary rows
+      const Product& q = c->logits;
+      planes = std::max(
+          {planes, plane_floats(c->dx, rows, hidden), plane_floats(c->dw, made, hidden)});
+      parts = std::max(parts, (size_t)(dbias_parts(q.main) + dbias_parts(q.rest)) * made);
     }
     p.o_planes = take(planes * sizeof(float));
-    p.o_bias = take(parts * p.piece * sizeof(float));
+    if (wants_dbias(g)) p.o_bias = take(parts * sizeof(float));
     p.o_scale = take(2 * sizeof(float));
   }
   p.bytes = at;
@@ -491,15 +511,17 @@ void launch_out(const Operand& a, const Operand& b, int32_t K, const Product& p,
     const Cut& c = second ? p.rest : p.main;
     if (c.tiles_n == 0) continue;
     const int32_t n0 = second ? p.n : 0, n1 = second ? n : p.n;
+    const int32_t r0 = ep.pairs ? n0 / 2 : n0, r1 = ep.pairs ? n1 / 2 : n1;
+    const int64_t from = (int64_t)r0 * ep.M, count = (int64_t)(r1 - r0) * ep.M;
     ep.planes = c.splits > 1 ? planes : nullptr;
+    ep.from = from;
+    ep.pitch = count;
     ep.add = before && c.splits == 1;
     launch_cut<T, false, BKC>(a, rows_of<T, BKC>(b, n0, n1), K, c, n0, ep, st);
     if (c.splits == 1) continue;
-    const int32_t r0 = ep.pairs ? n0 / 2 : n0, r1 = ep.pairs ? n1 / 2 : n1;
-    const int64_t from = (int64_t)r0 * ep.M, count = (int64_t)(r1 - r0) * ep.M;
     const int64_t blocks = (count + 255) / 256;
     planes_kernel<T><<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
-        planes + from, c.splits, (int64_t)ep.N * ep.M, count, before ? before + from : nullptr,
+        planes, c.splits, count, before ? before + from : nullptr,
         ep.last ? nullptr : ep.sums + from, ep.out + from, ep.scale);
   }
 }
@@ -566,7 +588,7 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
     if (g.dx && g.rows) {
       // out[token, h]: m = h, n = token, k = vocabulary
       const Operand a{wp.data, wp.ld, p.padded, false};
-      const OutEpilogue<T> oe{static_cast<T*>(g.dx), sums, nullptr, scale, g.hidden, g.rows,
+      const OutEpilogue<T> oe{static_cast<T*>(g.dx), sums, nullptr, 0, 0, scale, g.hidden, g.rows,
                               p.pairs, false, k == p.pieces - 1};
       launch_out<T, true>(a, dk, nv, cut.dx, oe, planes, k ? sums : nullptr, st);
     }
@@ -574,7 +596,7 @@ void run_grad(const LossPlan& p, const ctcpb_lm_grad_args& g, char* ws, hipStrea
       // out[v, h]: m = h, n = v, k = token
       const Operand a{x.data, x.ld, p.padded, p.pairs}, b{dk.data, ldd, nv, false};
       const OutEpilogue<T> oe{static_cast<T*>(g.dw) + (int64_t)v0 * g.hidden, nullptr, nullptr,
-                              scale, g.hidden, nv, false, false, true};
+                              0, 0, scale, g.hidden, nv, false, false, true};
       launch_out<T, false>(a, b, drows, cut.dw, oe, planes, nullptr, st);
     }
     if (g.dbias)

@@ -304,13 +304,15 @@ __global__ __launch_bounds__(256) void dbias_kernel(const float* part, int32_t p
 
 // Where the sums of a launch go: out[n, m] (m contiguous), rounded, or float32
 // `sums`, added to what earlier pieces of the vocabulary left there (`add`);
-// with k in parts, each part's sums to its own [N][M] plane.  The products are bound by
+// with k in parts, each part's sums to a plane of its own, [the launch's rows][M].  The products are bound by
 // the matrix units, busy in 65 % (dx) and 67 % (dw) of the cycles at 8192 x 50000 x 2048
 // bf16: 1.25 and 1.30 ms, 1345 and 1290 TFLOP/s.
 template <typename T>
 struct OutEpilogue {
   T* out;
   float *sums, *planes;     // or null
+  int64_t from, pitch;      // of the planes: the value of the result that each begins with, and
+                            // the values of one
   const float* scale;       // what d was multiplied by, or null
   int32_t M, N;
   bool pairs;               // the product's rows n = 2i and 2i + 1 add up to row i
@@ -330,7 +332,8 @@ struct OutEpilogue {
     const int g = lane >> 4, c = lane & 15;
     const int mb = (at.m * WM + wm) * TM * 16 + g * 4;
     const float inv = scale ? scale[1] : 1.0f;
-    float* f = planes ? planes + (int64_t)at.split * N * M : last ? nullptr : sums;
+    float* f = planes ? planes : last ? nullptr : sums;
+    const int64_t shift = planes ? at.split * pitch - from : 0;   // of f's values
     // results of 16-bit types whose rows are 16-byte aligned
     const bool wide = sizeof(T) == 2 && !f && M % 8 == 0;
 #pragma unroll
@@ -370,13 +373,13 @@ struct OutEpilogue {
         const int m = mb + i * 16;
         const int64_t to = (int64_t)n * M + m;
         if (f && M % 4 == 0) {   // rows start 4-element aligned: four values or none
-          if (m < M) *reinterpret_cast<f32x4*>(f + to) = acc[i][j];
+          if (m < M) *reinterpret_cast<f32x4*>(f + (to + shift)) = acc[i][j];
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if (m + r >= M) continue;
             if (f)
-              f[to + r] = acc[i][j][r];
+              f[to + shift + r] = acc[i][j][r];
             else
               out[to + r] = (T)(acc[i][j][r] * inv);
           }
@@ -386,20 +389,20 @@ struct OutEpilogue {
   }
 };
 
-// Adds `count` planes of n values (`pitch` apart), in their order, to `before` (if
+// Adds `count` planes of n values, in their order, to `before` (if
 // not null: what earlier pieces of the vocabulary left) and leaves the result in
 // `sums` or, rounded, in `out`.  Bound by memory: 4 planes of 875 x 384 4.8 us, 2 of
 // 848 x 2048 6.9 us.
 template <typename T>
-__global__ __launch_bounds__(256) void planes_kernel(const float* planes, int32_t count,
-                                                     int64_t pitch, int64_t n, const float* before,
-                                                     float* sums, T* out, const float* scale) {
+__global__ __launch_bounds__(256) void planes_kernel(const float* planes, int32_t count, int64_t n,
+                                                     const float* before, float* sums, T* out,
+                                                     const float* scale) {
   const float inv = scale ? scale[1] : 1.0f;
   const int64_t step = (int64_t)gridDim.x * 256;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
     float v = before ? before[i] : 0.0f;
 #pragma unroll 4
-    for (int p = 0; p < count; ++p) v += planes[p * pitch + i];
+    for (int p = 0; p < count; ++p) v += planes[p * n + i];
     if (sums)
       sums[i] = v;
     else

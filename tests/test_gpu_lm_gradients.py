@@ -48,32 +48,53 @@ def test_rows_without_a_target_hold_anything(dtype, N, garbage):
     assert torch.equal(dx, want[0]) and torch.equal(db, want[2])
 
 
+def check_norms(x, w, t, b, grad, got, tol):
+    """Gradients against 64 bits in the 2-norm, dx in blocks of rows."""
+    dx, dw, db = got
+    (N, H), V = x.shape, w.shape[0]
+    w64, dw64 = w.double(), torch.zeros((V, H), dtype=torch.float64, device="cuda")
+    db64 = torch.zeros(V, dtype=torch.float64, device="cuda")
+    for a in range(0, N, 20000):
+        xs, ts = x[a:a + 20000].double(), t[a:a + 20000]
+        z = xs @ w64.t()
+        if b is not None:
+            z += b.double()
+        d = torch.softmax(z, 1)
+        live = torch.nonzero(ts >= 0)[:, 0]
+        d[live, ts[live].long()] -= 1
+        d *= torch.where(ts >= 0, grad[a:a + 20000], 0.0).double()[:, None]
+        want = d @ w64
+        assert float((dx[a:a + 20000].double() - want).norm() / want.norm()) < tol
+        dw64 += d.t().contiguous() @ xs
+        db64 += d.sum(0)
+    assert float((dw.double() - dw64).norm() / dw64.norm()) < tol
+    if b is not None:
+        assert float((db.double() - db64).norm() / db64.norm()) < 2.0 ** -16
+
+
+NORM = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -16}
+
+
 @pytest.mark.parametrize("dtype,N,V", [(torch.float32, 70000, 5003), (torch.float16, 140000, 5003),
                                        (torch.bfloat16, 140000, 9001)])
 def test_pieces_of_the_vocabulary(dtype, N, V):
-    """More d than is made at a time (1 GiB): dx is summed over two or three pieces.  dw and
-    dbias, and dx of some rows, against 64 bits in the 2-norm: two roundings to the type
-    (f32: sums of float32, 2^-16 of them at most)."""
-    assert N * (-(-V // 256) * 256) * x_size(dtype) > 1 << 30
-    H = 64
-    x, w, t, b, grad = make(N, V, H, dtype, seed=9)
+    """More d than is made at a time (1 GiB): dx is summed over two or three pieces.  Two
+    roundings to the type (f32: sums of float32, 2^-16 of them at most)."""
+    x, w, t, b, grad = make(N, V, 64, dtype, seed=9)
+    assert N * (-(-V // 256) * 256) * x.element_size() > 1 << 30
     _, lse = lm.token_loss_forward(x, w, t, b)
-    dx, dw, db = lm.token_loss_backward(grad, x, w, t, lse, b)
-    w64, dw64, db64 = w.double(), torch.zeros((V, H), dtype=torch.float64, device="cuda"), 0
-    tol = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -16}[dtype]
-    for a in range(0, N, 20000):
-        z = x[a:a + 20000].double() @ w64.t() + b.double()
-        d = torch.softmax(z, 1)
-        live = torch.nonzero(t[a:a + 20000] >= 0)[:, 0]
-        d[live, t[a:a + 20000][live].long()] -= 1
-        d *= torch.where(t[a:a + 20000] >= 0, grad[a:a + 20000], 0.0).double()[:, None]
-        want = d @ w64
-        assert float((dx[a:a + 20000].double() - want).norm() / want.norm()) < tol
-        dw64 += d.t().contiguous() @ x[a:a + 20000].double()
-        db64 = db64 + d.sum(0)
-    assert float((dw.double() - dw64).norm() / dw64.norm()) < tol
-    assert float((db.double() - db64).norm() / db64.norm()) < 2.0 ** -16
+    got = lm.token_loss_backward(grad, x, w, t, lse, b)
+    check_norms(x, w, t, b, grad, got, NORM[dtype])
 
 
-def x_size(dtype):
-    return torch.empty((), dtype=dtype).element_size()
+@pytest.mark.parametrize("dtype,N,V,H", [
+    (torch.float32, 2000, 9000, 1024), (torch.float32, 9000, 2000, 1024),
+    (torch.bfloat16, 8192, 17000, 1024), (torch.float16, 17000, 4096, 2048),
+    (torch.bfloat16, 300, 1000, 64), (torch.float32, 875, 1000, 72)])
+def test_products_cut_along_k(dtype, N, V, H):
+    """All of a result, or its last rows (dw: of the vocabulary, dx: of the tokens), as a sum
+    of parts of k.  Roundings as above."""
+    x, w, t, b, grad = make(N, V, H, dtype, bias=False, seed=N)
+    _, lse = lm.token_loss_forward(x, w, t, b)
+    got = lm.token_loss_backward(grad, x, w, t, lse, b)
+    check_norms(x, w, t, b, grad, got, NORM[dtype])

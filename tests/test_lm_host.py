@@ -93,3 +93,22 @@ def test_second_derivatives_of_the_token_loss_are_refused(monkeypatch):
     assert torch.equal(d, torch.full_like(d, 3.0))
     with pytest.raises(RuntimeError, match="twice"):
         (loss + d.pow(2).sum()).backward()
+
+
+def grad_workspace(L, rows, V, H, dtype=0, bias=256):
+    out = ctypes.c_size_t()
+    assert L.ctcpb_lm_loss_grad_workspace(lm._GRAD.pack(
+        256, 256, bias, 256, 256, 256, 256, 256, bias, H, H, dtype, rows, V, H), out) == 0
+    return out.value
+
+
+@pytest.mark.parametrize("dtype,rows,V,H", [(0, 8192, 50000, 2048), (2, 2000, 9000, 1024),
+                                            (2, 9000, 2000, 1024)])
+def test_a_gradient_takes_little_more_than_its_d(L, dtype, rows, V, H):
+    """Sums of parts of k are kept for the rows that are cut along k (808 or 848 here, in 2
+    or 4 parts), not for all of the result: under a tenth of d; the partial sums of dbias,
+    of 32 tokens or more each, only with a bias."""
+    d = rows * (-(-V // 256) * 256) * (4 if dtype == 2 else 2)
+    assert grad_workspace(L, rows, V, H, dtype, bias=0) <= d * 1.1 + 1024
+    more = grad_workspace(L, rows, V, H, dtype) - grad_workspace(L, rows, V, H, dtype, bias=0)
+    assert 0 < more <= -(-rows // 32) * V * 4 + 256 * 64
