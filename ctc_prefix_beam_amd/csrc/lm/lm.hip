@@ -214,8 +214,9 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 // 20000 x 30000 x 1024 bf16 4340 us with 128 MB, 3381 with 512, 3182 with 2 GB;
 // 8192 x 50000 x 2048 4199 us with 512 MB (two pieces), 4035 in one.
 constexpr size_t kPieceBytes = (size_t)1 << 30;
-// Tokens up to which d has two rows each.  64 x 5000 x 512 bf16 20.3 us with them, 21.5
-// without (another cut); 64 x 20000 x 2048 86 and 75; 128 x 20000 x 2048 108 and 89.
+// Tokens up to which d has two rows each without being asked: for precision (see loss.h),
+// where it costs little.  64 x 5000 x 512 bf16 20.3 us with them, 21.5 without (another cut);
+// 64 x 20000 x 2048 86 and 75; 128 x 20000 x 2048 108 and 89.
 constexpr int32_t kPairRows = 64;
 
 // How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
@@ -368,6 +369,10 @@ struct LossPlan {
   size_t o_x, o_w, o_part, o_hit, o_d, o_sums, o_planes, o_bias, o_scale, bytes;
 };
 
+// The element type, without what a gradient's dtype may carry besides.
+int32_t type_of(const ctcpb_lm_loss_args& g) { return g.dtype; }
+int32_t type_of(const ctcpb_lm_grad_args& g) { return g.dtype & ~CTCPB_LM_SPLIT_D; }
+
 bool row_aligned(const void* p, int64_t stride, int es) {
   // within a tile, rows are addressed with 31 bits
   return aligned(p, 16) && stride * es % 16 == 0 && stride * es <= (1 << 23);
@@ -389,15 +394,20 @@ size_t plane_floats(const Product& q, int64_t n, int32_t hidden) {
   return most;
 }
 
-// Also the partial sums for dbias, where it is asked for.
+// What only gradients have: partial sums for dbias, where it is asked for, and d as two
+// values of a 16-bit type, where the caller or the number of rows says so.
 bool wants_dbias(const ctcpb_lm_loss_args&) { return false; }
 bool wants_dbias(const ctcpb_lm_grad_args& g) { return g.dbias != nullptr; }
+bool wants_pairs(const ctcpb_lm_loss_args&) { return false; }
+bool wants_pairs(const ctcpb_lm_grad_args& g) {
+  return elem_size(type_of(g)) == 2 && (g.rows <= kPairRows || (g.dtype & CTCPB_LM_SPLIT_D));
+}
 
 template <typename Args>
 LossPlan plan_loss(const Args& g, bool grad) {
   const int32_t rows = g.rows, vocab = g.vocab, hidden = g.hidden;
   LossPlan p{};
-  p.es = elem_size(g.dtype);
+  p.es = elem_size(type_of(g));
   p.padded = (int)up(hidden, 16 / p.es);
   // a row is read up to its last 16 bytes
   p.pad_x = p.padded != hidden || !row_aligned(g.x, g.stride_x, p.es);
@@ -416,7 +426,7 @@ LossPlan plan_loss(const Args& g, bool grad) {
                     sizeof(float2));
     p.o_hit = take((size_t)rows * sizeof(float));
   } else {
-    p.pairs = p.es == 2 && rows <= kPairRows;
+    p.pairs = wants_pairs(g);
     p.piece = choose_piece_rows(p.es, p.pairs ? 2 * rows : rows, vocab, p.padded);
     p.pieces = ceil_div(vocab, p.piece);
     const int32_t first = p.pieces > 1 ? p.piece : vocab;
@@ -443,13 +453,15 @@ LossPlan plan_loss(const Args& g, bool grad) {
 
 template <typename Args>
 int check_loss(const Args& g) {
-  if (!elem_size(g.dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
+  if (!elem_size(type_of(g))) return fail(CTCPB_ERR_INVALID, kBadType);
   if (g.rows < 0 || g.vocab < 1 || g.hidden < 1)
     return fail(CTCPB_ERR_INVALID, "need rows >= 0, vocab >= 1 and hidden >= 1");
   if (g.stride_x < g.hidden || g.stride_w < g.hidden)
     return fail(CTCPB_ERR_INVALID, "stride_x and stride_w must be >= hidden");
   if (g.hidden > 1 << 20 || g.vocab > 1 << 30 || g.rows > 1 << 30)
     return fail(CTCPB_ERR_UNSUPPORTED, "hidden above 2^20, or vocab or rows above 2^30");
+  if (wants_pairs(g) && g.rows >= 1 << 30)
+    return fail(CTCPB_ERR_UNSUPPORTED, "CTCPB_LM_SPLIT_D with 2^30 rows");
   if ((int64_t)ceil_div(g.vocab, 64) * ceil_div(g.rows, 64) > INT_MAX)
     return fail(CTCPB_ERR_UNSUPPORTED, "too many tiles for one launch");
   return CTCPB_OK;
@@ -845,9 +857,10 @@ int ctcpb_lm_loss_grad(const ctcpb_lm_grad_args* args, void* workspace, size_t w
     const LossPlan p = plan_loss(g, true);
     if (workspace_bytes < p.bytes)
       return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_loss_grad_workspace");
-    const auto f = g.dtype == CTCPB_LM_BF16  ? run_grad<__bf16>
-                   : g.dtype == CTCPB_LM_F16 ? run_grad<_Float16>
-                                             : run_grad<float>;
+    const int32_t type = type_of(g);
+    const auto f = type == CTCPB_LM_BF16  ? run_grad<__bf16>
+                   : type == CTCPB_LM_F16 ? run_grad<_Float16>
+                                          : run_grad<float>;
     f(p, g, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
     return launched("loss gradient kernels");
   });

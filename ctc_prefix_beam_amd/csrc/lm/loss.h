@@ -8,15 +8,19 @@
 // is recomputed, rounded to the inputs' type and kept for the piece only (at most
 // kPieceBytes of workspace); dx += d w and dw = d^T x follow from it.
 //
-// The rounding of d is unbiased, and what it adds to dx and dw is about what their
-// own rounding to that type does.  Two things keep it there.  d is scaled so that
-// the largest |g| is a power of two: the targets' entries, -g (1 - p), the largest
-// of their rows, then lie mostly just below one, where a rounding is smallest for
-// its number (random entries: error of dx 1.33 times that of the result's rounding
-// alone, not 1.41 to 1.6); with f16 it also keeps d in range.  And with up to
-// kPairRows tokens, too few to average over, d is kept as the sum of two values of
-// the type in neighbouring rows (2n and 2n + 1): twice the products, in calls that
-// wait for memory.
+// The rounding of d to 16 bits adds to dx and dw about what their own rounding to that
+// type does.  d is scaled so that the largest |g| is a power of two: the targets' entries,
+// -g (1 - p), the largest of their rows, then lie just below one where rows share that
+// weight, where a rounding is smallest for its number; with f16 it also keeps d in range.
+// Errors of dx and dw over those of rounding the exact results, bf16, 300 to 4096 tokens
+// and 500 to 20000 labels: equal weights 1.02 to 1.23, weights spread evenly over [-1, 1]
+// 1.33 to 1.39, over a factor of 400 1.36 to 1.45; weights of 1 (2 % of the rows) and 0.51,
+// whose targets' entries are all rounded the same way, 1.8 to 2.2.
+//
+// With up to kPairRows tokens, too few to average over, and wherever the caller asks for
+// it, d is kept as the sum of two values of the type in neighbouring rows (2n and 2n + 1):
+// 1.00 in all of these cases, for twice the products of dx and dw, which in small calls wait
+// for memory (8192 x 50000 x 2048 bf16: 4.04 and 7.25 ms, 20000 x 5000 x 1024: 0.63 and 0.96).
 #pragma once
 #include "gemm.h"
 

@@ -33,6 +33,10 @@ extern "C" {
 /* Element types of the tensors documented "typed". */
 enum { CTCPB_LM_BF16 = 0, CTCPB_LM_F16 = 1, CTCPB_LM_F32 = 2 };
 
+/* Added to the dtype of ctcpb_lm_loss_grad and its size query: d as the sum of two
+ * values of a 16-bit type, see there.  Of no account with CTCPB_LM_F32. */
+enum { CTCPB_LM_SPLIT_D = 256 };
+
 /* Status bits of ctcpb_lm_cache_plan. */
 enum {
   CTCPB_LM_NO_PAGE = 1,   /* the pool ran out before the row had its pages */
@@ -187,7 +191,12 @@ int ctcpb_lm_loss(const ctcpb_lm_loss_args* args, void* workspace, size_t worksp
  *            of them may be NULL and is then not computed.
  * With 16-bit types d is rounded to that type before the products, scaled so
  * that the largest |grad| is a power of two (which keeps f16 in range and the
- * rounding small), and to the sum of two such values for up to 64 rows; sums
+ * rounding small): the errors of dx and dw are mostly 1.0 to 1.4 times those of
+ * rounding the exact results, and up to 2.2 times where most rows share a weight that
+ * is not the largest (their targets' entries are then rounded alike).  For up to 64
+ * rows, and for any number with CTCPB_LM_SPLIT_D, d is the sum of two values of the
+ * type, and the errors are those of rounding the results; dx and dw then take twice
+ * the products and d twice the room.  Sums
  * are float32.  The workspace holds up to 1 GiB of d at a time (256 columns of it
  * at least), the sums of dx if d is made in several pieces, those of products that
  * are cut along k, and those of dbias if it is not NULL: 811 MiB at 8192 x 50000 x 2048

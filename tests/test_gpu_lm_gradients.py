@@ -98,3 +98,30 @@ def test_products_cut_along_k(dtype, N, V, H):
     _, lse = lm.token_loss_forward(x, w, t, b)
     got = lm.token_loss_backward(grad, x, w, t, lse, b)
     check_norms(x, w, t, b, grad, got, NORM[dtype])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,V,H", [(65, 700, 64), (300, 5000, 128), (4096, 3001, 257),
+                                   (5000, 9000, 1024)])
+def test_gradients_by_a_split_d_are_off_by_their_own_rounding(dtype, N, V, H):
+    """d as two values is off by 2^-17 of itself (f16: 2^-22), a 256th of what the results
+    lose in their own rounding; 2 % are allowed for it and the float32 sums."""
+    x, w, t, b, grad = make(N, V, H, dtype, seed=N)
+    xs, ws, bs = (a.clone().requires_grad_() for a in (x, w, b))
+    (lm.token_loss(xs, ws, t, bs, split_d=True) * grad).sum().backward()
+    z = torch.softmax(x.double() @ w.double().t() + b.double(), 1)
+    live = torch.nonzero(t >= 0)[:, 0]
+    z[live, t[live].long()] -= 1
+    z *= torch.where(t >= 0, grad, 0.0).double()[:, None]
+    for got, want in ((xs.grad, z @ w.double()), (ws.grad, z.t().contiguous() @ x.double())):
+        least = (want.to(dtype).double() - want).norm()
+        assert float((got.double() - want).norm()) <= 1.02 * float(least)
+    assert float((bs.grad.double() - z.sum(0)).norm() / z.sum(0).norm()) < 2.0 ** -16
+
+
+def test_split_d_of_f32_changes_nothing():
+    x, w, t, b, grad = make(200, 300, 64, torch.float32)
+    _, lse = lm.token_loss_forward(x, w, t, b)
+    got = lm.token_loss_backward(grad, x, w, t, lse, b, split_d=True)
+    want = lm.token_loss_backward(grad, x, w, t, lse, b)
+    assert all(torch.equal(a, c) for a, c in zip(got, want))

@@ -86,7 +86,7 @@ def test_second_derivatives_of_the_token_loss_are_refused(monkeypatch):
     monkeypatch.setattr(lm, "token_loss_forward",
                         lambda x, w, t, b: ((x.detach() ** 3).sum(1), x.detach().sum(1)))
     monkeypatch.setattr(lm, "token_loss_backward",
-                        lambda g, x, w, t, lse, b, need: (g[:, None] * 3 * x ** 2, None, None))
+                        lambda g, x, w, *a, **kw: (g[:, None] * 3 * x ** 2, None, None))
     x = torch.ones((2, 3), requires_grad=True)
     loss = lm.token_loss(x, torch.zeros(4, 3), torch.zeros(2, dtype=torch.int32)).sum()
     (d,) = torch.autograd.grad(loss, x, create_graph=True)
@@ -112,3 +112,17 @@ def test_a_gradient_takes_little_more_than_its_d(L, dtype, rows, V, H):
     assert grad_workspace(L, rows, V, H, dtype, bias=0) <= d * 1.1 + 1024
     more = grad_workspace(L, rows, V, H, dtype) - grad_workspace(L, rows, V, H, dtype, bias=0)
     assert 0 < more <= -(-rows // 32) * V * 4 + 256 * 64
+
+
+def test_a_split_d_has_twice_the_room_and_is_for_gradients_only(L):
+    one, two = (grad_workspace(L, 1000, 5000, 512, dtype, bias=0) for dtype in (0, 256))
+    d = 1000 * 5120 * 2
+    assert one >= d and two >= 2 * d
+    assert grad_workspace(L, 1000, 5000, 512, 258) == grad_workspace(L, 1000, 5000, 512, 2)
+    out = ctypes.c_size_t()
+    args = lm._LOSS.pack(256, 256, 0, 256, 256, 256, 64, 64, 256, 3, 100, 64)
+    assert L.ctcpb_lm_loss_workspace(args, out) == 1
+    args = lm._GRAD.pack(*[256] * 9, 64, 64, 256 + 3, 3, 100, 64)
+    assert L.ctcpb_lm_loss_grad_workspace(args, out) == 1
+    args = lm._GRAD.pack(*[256] * 9, 64, 64, 256, 1 << 30, 1, 64)
+    assert L.ctcpb_lm_loss_grad_workspace(args, out) == 3
