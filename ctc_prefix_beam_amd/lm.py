@@ -76,6 +76,14 @@ def _check(rc: int):
         raise RuntimeError(f"ctcpb_lm error {rc}: {msg}")
 
 
+def _pack(layout, *values):
+    """The argument structure of a call; numbers that it cannot hold are refused."""
+    try:
+        return layout.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"an argument is not a number in its range: {e}") from None
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -125,6 +133,13 @@ def _like(t, index, name, dtype, shape=None):
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and
             (shape is None or t.shape == shape)):
         _check_dev(t, torch.device("cuda", index), name, dtype, shape)
+
+
+def _pool(pool, index):
+    """Entries of a pool of pages."""
+    _gpu(pool, "pool")
+    _i32(pool, index, "pool", (pool.numel(),))
+    return pool.numel()
 
 
 def _tables(tables, index, rows):
@@ -186,20 +201,20 @@ def cache_plan(lengths, counts, tables, pool, taken, page_size: int, total: int,
     _i32(lengths, dev, "lengths", (rows,))
     _i32(counts, dev, "counts", (rows,))
     stride, width = _tables(tables, dev, rows)
-    _i32(pool, dev, "pool", (pool.numel(),))
+    pages = _pool(pool, dev)
     _i32(taken, dev, "taken", (1,))
-    if total < 0:
-        raise ValueError("total must be >= 0")
+    if not 0 <= total <= 1 << 30:
+        raise ValueError("total must be in 0 .. 2^30")
     raw, empty = _on(stream, dev)
     # one allocation for all outputs
     buf = empty((2 * total + 3 * rows + 2,), dtype=torch.int32, device=lengths.device)
     base = buf.data_ptr()
     at = base + 8 * total
-    _check(lib().ctcpb_lm_cache_plan(_PLAN.pack(
-        lengths.data_ptr(), counts.data_ptr(), tables.data_ptr(), pool.data_ptr(),
+    _check(lib().ctcpb_lm_cache_plan(_pack(
+        _PLAN, lengths.data_ptr(), counts.data_ptr(), tables.data_ptr(), pool.data_ptr(),
         taken.data_ptr(), base, base + 4 * total, at, at + 4 * (rows + 1),
-        at + 4 * (2 * rows + 1), at + 4 * (2 * rows + 2), stride, rows, width, pool.numel(),
-        page_size, total), raw))
+        at + 4 * (2 * rows + 1), at + 4 * (2 * rows + 2), stride, rows, width, pages, page_size,
+        total), raw))
     return CachePlan._make(buf.split_with_sizes((total, total, rows + 1, rows, 1, rows)))
 
 
@@ -214,15 +229,14 @@ def cache_release(finished, lengths, tables, pool, taken, page_size: int, stream
     _check_dev(finished, lengths.device, "finished", torch.uint8, (rows,), contiguous=True)
     _i32(lengths, dev, "lengths", (rows,))
     stride, width = _tables(tables, dev, rows)
-    _i32(pool, dev, "pool", (pool.numel(),))
+    pages = _pool(pool, dev)
     _i32(taken, dev, "taken", (1,))
     raw, empty = _on(stream, dev)
     buf = empty((rows + 1,), dtype=torch.int32, device=lengths.device)
     base = buf.data_ptr()
-    _check(lib().ctcpb_lm_cache_release(_RELEASE.pack(
-        finished.data_ptr(), lengths.data_ptr(), tables.data_ptr(), pool.data_ptr(),
-        taken.data_ptr(), base, base + 4 * rows, stride, rows, width, pool.numel(), page_size),
-        raw))
+    _check(lib().ctcpb_lm_cache_release(_pack(
+        _RELEASE, finished.data_ptr(), lengths.data_ptr(), tables.data_ptr(), pool.data_ptr(),
+        taken.data_ptr(), base, base + 4 * rows, stride, rows, width, pages, page_size), raw))
     return buf[:rows], buf[rows:]
 
 
@@ -245,9 +259,9 @@ def cache_store(k, v, slots, k_cache, v_cache, stream=None):
         raise ValueError(f"caches must have {H} heads of {D}, got {(heads, dim)}")
     if T == 0:
         return
-    _check(lib().ctcpb_lm_cache_store(_STORE.pack(
-        k.data_ptr(), v.data_ptr(), slots.data_ptr(), kt, kh, vt, vh, *kc, *vc, dt, T, pages,
-        page_size, H, D), _on(stream, dev)[0]))
+    _check(lib().ctcpb_lm_cache_store(_pack(
+        _STORE, k.data_ptr(), v.data_ptr(), slots.data_ptr(), kt, kh, vt, vh, *kc, *vc, dt, T,
+        pages, page_size, H, D), _on(stream, dev)[0]))
 
 
 def attention(q, k_cache, v_cache, tables, lengths, scale: float | None = None, window: int = 0,
@@ -278,10 +292,10 @@ def attention(q, k_cache, v_cache, tables, lengths, scale: float | None = None, 
         _like(out, dev, "out", q.dtype, shape)
     outr, outh, _ = _rows(out, "out")
     lse = empty((R, Hq), dtype=torch.float32, device=q.device)
-    args = _ATTENTION.pack(
-        q.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), qr, qh,
-        outr, outh, stride, *kc, *vc, dt, R, Hq, Hkv, D, pages, page_size, width, max_len, window,
-        1.0 / math.sqrt(D) if scale is None else scale)
+    args = _pack(
+        _ATTENTION, q.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), qr, qh, outr, outh, stride, *kc, *vc, dt, R, Hq, Hkv, D, pages, page_size,
+        width, max_len, window, 1.0 / math.sqrt(D) if scale is None else scale)
     need = ctypes.c_size_t()
     _check(L.ctcpb_lm_attention_workspace(args, need))
     size = need.value
@@ -330,8 +344,8 @@ def token_loss_forward(x, w, targets, bias=None, stream=None):
     raw, empty = _on(stream, dev)
     loss = empty((N,), dtype=torch.float32, device=x.device)
     lse = empty((N,), dtype=torch.float32, device=x.device)
-    args = _LOSS.pack(x.data_ptr(), w.data_ptr(), _ptr(bias), targets.data_ptr(), loss.data_ptr(),
-                      lse.data_ptr(), *sizes)
+    args = _pack(_LOSS, x.data_ptr(), w.data_ptr(), _ptr(bias), targets.data_ptr(),
+                 loss.data_ptr(), lse.data_ptr(), *sizes)
     need = ctypes.c_size_t()
     _check(L.ctcpb_lm_loss_workspace(args, need))
     ws = empty((need.value,), dtype=torch.uint8, device=x.device)
@@ -363,8 +377,8 @@ def token_loss_backward(grad, x, w, targets, lse, bias=None, need=(True, True, T
     db = None
     if need[2] and bias is not None:
         db = empty((V,), dtype=torch.float32, device=x.device)
-    args = _GRAD.pack(x.data_ptr(), w.data_ptr(), _ptr(bias), targets.data_ptr(), grad.data_ptr(),
-                      lse.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), *sizes)
+    args = _pack(_GRAD, x.data_ptr(), w.data_ptr(), _ptr(bias), targets.data_ptr(),
+                 grad.data_ptr(), lse.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), *sizes)
     size = ctypes.c_size_t()
     _check(L.ctcpb_lm_loss_grad_workspace(args, size))
     ws = empty((size.value,), dtype=torch.uint8, device=x.device)
@@ -428,6 +442,10 @@ class PagedCache:
     def __init__(self, rows: int, max_len: int, kv_heads: int, head_dim: int,
                  dtype=torch.bfloat16, page_size: int = 16, num_pages: int = 0, device="cuda",
                  layers: int = 1):
+        if page_size not in (4, 8, 16, 32, 64, 128, 256):
+            raise ValueError("page_size must be a power of two in 4..256")
+        if min(rows, max_len, num_pages) < 0:
+            raise ValueError("rows, max_len and num_pages must be >= 0")
         width = -(-max_len // page_size)
         num_pages = num_pages or max(1, rows * width)
         self.page_size, self.max_len = page_size, width * page_size

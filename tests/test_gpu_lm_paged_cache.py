@@ -64,3 +64,28 @@ def test_rows_up_to_the_last_place_of_their_last_page(max_len, page, window):
         assert torch.allclose(out[r, 0].cpu().double(), want, atol=1e-5, rtol=0)
         assert abs(float(lse[r, 0]) - float(torch.logsumexp(s, 0))) < 1e-5
     assert c.append(i32(1, 0), 1).status.tolist() == [lm.NO_ENTRY, 0]
+
+
+def test_numbers_that_no_call_can_take_are_refused_as_values():
+    i, one, tab = i32(0, 0), i32(0), torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    for kw in (dict(page_size=1 << 31), dict(page_size=16.0), dict(total=1 << 31),
+               dict(total=(1 << 30) + 1), dict(page_size="16")):
+        with pytest.raises(ValueError):
+            lm.cache_plan(i, i, tab, i, one, **{**dict(page_size=16, total=2), **kw})
+    with pytest.raises(ValueError):
+        lm.cache_release(i.to(torch.uint8), i, tab, i, one, 1 << 40)
+    for pool in (None, [0, 1]):
+        with pytest.raises(ValueError, match="pool"):
+            lm.cache_plan(i, i, tab, pool, one, 16, 2)
+        with pytest.raises(ValueError, match="pool"):
+            lm.cache_release(i.to(torch.uint8), i, tab, pool, one, 16)
+    c = lm.PagedCache(2, 64, 1, 64)
+    q = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(max_len=1 << 31), dict(window=1 << 31), dict(window=-(1 << 40)),
+               dict(window=2.5), dict(scale="1")):
+        with pytest.raises(ValueError):
+            c.attend(q, **kw)
+    with pytest.raises(ValueError):
+        lm.PagedCache(2, 64, 1, 64, page_size=0)
+    with pytest.raises(ValueError):
+        lm.PagedCache(2, -1, 1, 64)
