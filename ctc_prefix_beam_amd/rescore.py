@@ -8,8 +8,9 @@ decodes seeded synthetic utterances, rescores their 8-best lists with a small
 randomly initialised model, takes training steps on its output layer with the
 first-pass best hypotheses as targets, and rescores again.  It runs the
 operators of ``ctc_prefix_beam_amd.lm`` together as a user would: pages and
-slots from the hypotheses' lengths (which never leave the GPU), the store of new
-keys and values, attention over the cache, and token losses with gradients.
+slots from the hypotheses' lengths (of which only the longest is read back), the
+store of new keys and values, attention over the cache, and token losses with
+gradients.
 Projections and normalisations are plain torch.
 """
 from __future__ import annotations
@@ -58,9 +59,11 @@ class LanguageModel:
         return lm.PagedCache(rows, max_len, c.kv_heads, c.head_dim, c.dtype, page_size, num_pages,
                              self.embed.device, layers=c.layers)
 
-    def step(self, tokens, alive, cache):
+    def step(self, tokens, alive, cache, max_len: int = 0):
         """Hidden states (rows, hidden) after one more token of every row with
-        alive[r] (bool); the others' are not meaningful.  tokens: (rows,) int64."""
+        alive[r] (bool); the others' are not meaningful.  tokens: (rows,) int64.
+        `max_len`: what no row holds more tokens than afterwards, where that is known
+        (0: what the cache can hold)."""
         c, rows = self.cfg, tokens.numel()
         before = cache.lengths
         plan = cache.append(alive.to(torch.int32), rows)
@@ -72,7 +75,7 @@ class LanguageModel:
             qkv = (_norm(x) @ self.qkv[i].t()).view(rows, -1, c.head_dim)
             q, k, v = qkv.split((c.q_heads, c.kv_heads, c.kv_heads), 1)
             cache.store(k, v, slots, layer=i)
-            a, _ = cache.attend(q, layer=i)
+            a, _ = cache.attend(q, layer=i, max_len=max_len)
             x = x + a.reshape(rows, -1) @ self.o[i].t()
             x = x + torch.nn.functional.gelu(_norm(x) @ self.up[i].t()) @ self.down[i].t()
         return _norm(x)
@@ -119,7 +122,7 @@ def score(model: LanguageModel, tokens, lengths, keep_states: bool = False):
         alive = lens >= t
         target = toks[:, t] if t < L else torch.full_like(end, -1)
         target = torch.where(lens > t, target, torch.where(lens == t, end, -1)).contiguous()
-        h = model.step(now, alive, cache)
+        h = model.step(now, alive, cache, t + 1)
         loss, _ = lm.token_loss_forward(h, model.out, target, model.bias)
         total -= loss
         if keep_states:
@@ -160,16 +163,22 @@ def train_output(model: LanguageModel, tokens, lengths, steps: int = 10, rate: f
     return torch.stack(losses)
 
 
+def utterances(rows: int, frames: int, vocab: int, seed: int = 0):
+    """Log-probabilities (rows, frames, vocab) as an acoustic model leaves them, a blank or
+    another label ahead in each frame, and their lengths (rows,) int32, on the CPU."""
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn((rows, frames, vocab), generator=g)
+    ahead = torch.randint(1, vocab, (rows, frames), generator=g)
+    ahead[torch.rand((rows, frames), generator=g) < 0.6] = 0
+    z.scatter_add_(2, ahead[..., None], torch.where(ahead == 0, 8.0, 6.0)[..., None])
+    return z.log_softmax(-1), torch.full((rows,), frames, dtype=torch.int32)
+
+
 def main():
-    import os
-    import sys
-    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-    import ctc_prefix_beam_amd as cpb
-    import synth
-    lp, lens = synth.peaky(8, 200, 256, seed=0, p_blank=0.6)
-    dec = cpb.OfflineDecoder(cpb.DecoderConfig(beam=8, nbest=8, blank_threshold=0.999,
-                                               max_out_len=100))
-    tokens, lengths, scores = dec.decode(torch.from_numpy(lp).cuda(), torch.from_numpy(lens).cuda())
+    from . import DecoderConfig, OfflineDecoder
+    lp, lens = utterances(8, 200, 256)
+    dec = OfflineDecoder(DecoderConfig(beam=8, nbest=8, blank_threshold=0.999, max_out_len=100))
+    tokens, lengths, scores = dec.decode(lp.cuda(), lens.cuda())
     model = LanguageModel(ModelConfig(vocab=256))
     order, _ = rescore(model, tokens, lengths, scores)
     print("order before training:", order[0].tolist())

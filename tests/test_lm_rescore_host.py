@@ -35,3 +35,10 @@ def test_no_hypotheses():
     tokens, lens = nbest([[0] * 4], 5)
     got = rescore.score(model(), tokens[:0], lens[:0])
     assert got.shape == (0, 4)
+
+
+def test_utterances():
+    lp, lens = rescore.utterances(2, 30, 16, seed=3)
+    assert lp.shape == (2, 30, 16) and lens.tolist() == [30, 30]
+    assert (lp.exp().sum(-1) - 1).abs().max() < 1e-5
+    assert (lp.argmax(-1) == 0).any() and (lp.argmax(-1) > 0).any()
