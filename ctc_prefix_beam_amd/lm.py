@@ -437,7 +437,11 @@ class PagedCache:
     ``release(finished)`` gives pages back.  `num_pages` (default:
     every request at max_len) may be smaller: a request the pool cannot serve is
     flagged in the plan's status and holds only the tokens that have a slot.  Use
-    one PagedCache per stream, or order its calls."""
+    one PagedCache per stream, or order its calls.
+
+    An append goes on to the plan's new lengths, so a captured one repeats the same
+    step when it is replayed.  To capture a step that moves on, call ``cache_plan``
+    and copy its lengths and `taken` back to the tensors that it reads."""
 
     def __init__(self, rows: int, max_len: int, kv_heads: int, head_dim: int,
                  dtype=torch.bfloat16, page_size: int = 16, num_pages: int = 0, device="cuda",

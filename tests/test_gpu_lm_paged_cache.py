@@ -89,3 +89,65 @@ def test_numbers_that_no_call_can_take_are_refused_as_values():
         lm.PagedCache(2, 64, 1, 64, page_size=0)
     with pytest.raises(ValueError):
         lm.PagedCache(2, -1, 1, 64)
+
+
+def step_inputs(rows, heads, D, steps):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    return [[torch.randn((rows, heads, D), generator=g, device="cuda") for _ in range(3)]
+            for _ in range(steps)]
+
+
+def test_a_captured_step_is_replayed_for_one_token_after_another():
+    """Plan, store and attention in a graph: the plan's lengths and counter are copied back
+    to the buffers that it reads, so each replay appends the next token."""
+    rows, heads, D, steps = 3, 2, 64, 40
+    inputs = step_inputs(rows, heads, D, steps)
+    ones = i32(1, 1, 1)
+    want = lm.PagedCache(rows, 64, heads, D, torch.float32)
+    c = lm.PagedCache(rows, 64, heads, D, torch.float32)
+    for x in (want, c):
+        x.append(i32(0, 3, 7), 10)
+        x.k.zero_()
+        x.v.zero_()
+    q, k, v = (torch.empty_like(t) for t in inputs[0])
+
+    def step():
+        plan = lm.cache_plan(c.lengths, ones, c.tables, c.pool, c.taken, c.page_size, rows)
+        lm.cache_store(k, v, plan.slots, c.k[0], c.v[0])
+        out, lse = lm.attention(q, c.k[0], c.v[0], c.tables, plan.lengths)
+        c.lengths.copy_(plan.lengths)
+        c.taken.copy_(plan.taken)
+        return out, lse, plan.status
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(steps):
+        for a, b in zip((q, k, v), inputs[i]):
+            a.copy_(b)
+        graph.replay()
+        plan = want.append(ones, rows)
+        want.store(inputs[i][1], inputs[i][2], plan.slots)
+        out, lse = want.attend(inputs[i][0])
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse), i
+        assert torch.equal(got[2], plan.status) and torch.equal(c.lengths, want.lengths), i
+        assert torch.equal(c.tables, want.tables) and torch.equal(c.taken, want.taken), i
+    assert c.lengths.tolist() == [steps, steps + 3, steps + 7]
+
+
+def test_a_captured_append_repeats_itself():
+    """PagedCache goes on to new lengths with each append; what was captured reads the old."""
+    c = lm.PagedCache(3, 64, 1, 64, torch.float32)
+    c.append(i32(2, 0, 5), 7)
+    (q, k, v), = step_inputs(3, 1, 64, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = c.append(c.lengths.clone(), 7)   # as many again
+        c.store(k[:1].expand(7, 1, 64), v[:1].expand(7, 1, 64), plan.slots)
+        out, _ = c.attend(q)
+    for i in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert plan.lengths.tolist() == [4, 0, 10] and not plan.status.any(), i
+        assert plan.positions.tolist() == [2, 3, 5, 6, 7, 8, 9], i
+        torch.ones(1000, device="cuda").cumsum(0)

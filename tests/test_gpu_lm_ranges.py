@@ -86,3 +86,19 @@ def test_many_heads_joined_by_one_group_of_threads_each(dtype, Hq, Hkv):
 @pytest.mark.parametrize("Hq,Hkv", [(3, 3), (20, 1)])
 def test_windows_that_begin_inside_a_tile(dtype, window, Hq, Hkv):
     check(*make([9000, 0, 2499, 2501, 7777, 4003], Hq, Hkv, 64, dtype, 16, 600, window), window)
+
+
+@pytest.mark.parametrize("lengths,Hq,Hkv", [([300, 77, 500], 4, 2), ([9000, 700], 3, 1),
+                                            ([40000], 8, 2)])
+@pytest.mark.parametrize("window", [0, 450])
+def test_f32_outputs_in_the_2_norm(lengths, Hq, Hkv, window):
+    """Products of 64 terms reach 32 before their scale of 1 / 8: a rounding is 0.29 of 2^-19 at
+    the root mean square, some 32 of them in a chain that large, so a score, and with it the
+    logarithm of a probability, is off by 0.29 2^-19 sqrt(32) / 8 = 0.2 2^-19; sums in chains
+    of tiles, the exponentials and the division by 2^-22 at most.  Twice that is allowed."""
+    q, kc, vc, tables, lens = make(lengths, Hq, Hkv, 64, torch.float32, 16, 2600, len(lengths))
+    out, lse = lm.attention(q, kc, vc, tables, lens, window=window)
+    want = lm_ref_rows.attention(q, kc, vc, tables, lens, 0.125, window, 16)
+    tol = 2 * (0.2 * 2.0 ** -19 + 2.0 ** -22)
+    assert float((out.cpu().double() - want[0]).norm() / want[0].norm()) <= tol
+    assert ((lse.cpu().double() - want[1]).abs() <= 4 * tol + 2.0 ** -23 * want[1].abs()).all()
