@@ -130,16 +130,28 @@ AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
   const int64_t slots =
       256 * (g.head_dim <= 64 ? 4 : g.head_dim > 128 ? 1 : g.dtype == CTCPB_LM_F32 ? 2 : 3);
   const int64_t steps = ceil_div(std::max<int64_t>(span, 1), kRangeWaves * tile);
-  // Ranges cost some 6 us more than a workgroup to each item (the prefix sums, the
+  // Ranges cost some 4 to 6 us more than a workgroup to each item (the prefix sums, the
   // join), so they are for rows that would keep a workgroup's waves for more than a few
   // tiles each, where uneven lengths leave CUs idle (f32: fewer, its products take
   // longer).  Bytes alone decide once there are many items, and a wave to each then
-  // saves joining waves.  16 query and 4 key/value heads of 64, bf16, rows of up to
-  // 256 tokens (us, ranges / a workgroup each / a wave each): 64 rows 12.0 / 5.8 / 12.1,
-  // 256 17.6 / 12.7 / 14.5, 512 23.7 / 21.4 / 18.1; of up to 2048: 64 rows 23.7 / 18.0 /
-  // 81, 1024 233 / 225 / 245, 4096 886 / 861 / 801; of up to 4096: 16 rows 18.8 / 25.6 /
-  // 144, 256 125 / 138 / 204.
-  // wider heads leave a wave too few registers in workgroups of eight
+  // saves joining waves.  Rows of random lengths up to a bound, in us (ranges / a
+  // workgroup each / a wave each):
+  //   bf16, 16 query and 4 key/value heads of 64: 64 rows up to 256 12.9 / 6.8 / 13.1, up
+  //     to 2048 25.1 / 19.1 / 83, up to 4096 35.1 / 32.1 / 158; 256 rows up to 4096 122 /
+  //     134 / 203; 1024 rows up to 256 38.9 / 40.1 / 30.9; 4096 rows up to 512 283 / 277 / 227
+  //   bf16, 32 and 8 of 128: 16 rows up to 1024 18.9 / 15.6 / 54, up to 2048 27.1 / 26.8,
+  //     up to 4096 35.8 / 43.9; 256 rows up to 512 62.7 / 67.0 / 56.1 (the workgroup is taken),
+  //     1024 rows 254 / 286 / 223
+  //   bf16, 8 and 4 of 256: 16 rows up to 1024 22.1 / 26.8 (the workgroup is taken), up to 2048
+  //     32.7 / 48.1; 64 rows up to 128 12.2 / 8.5 / 16.6 (the wave is taken), up to 1024 33.2 /
+  //     30.9 / 89; 1024 rows up to 512 231 / 248 / 225
+  //   f32, 8 of 64: 16 rows up to 512 17.9 / 13.0 / 46, up to 1024 23.6 / 20.9, up to 2048
+  //     27.7 / 39.0; 64 rows up to 1024 36.7 / 36.3; 256 rows up to 1024 133 / 119 / 145
+  //   f32, 8 and 4 of 256: 16 rows up to 256 22.9 / 20.8, up to 512 31.9 / 37.8, up to 2048
+  //     44 / 122
+  // One short row in wide tables is dearer by ranges (f32, 8 heads of 64, up to 2048: 17.4
+  // / 10.8): a max_len tells.
+  // Wider heads leave a wave too few registers in workgroups of eight.
   const int32_t group_waves = g.head_dim <= 128 ? 8 : 4;
   const int64_t few = (int64_t)group_waves * tile * (g.dtype == CTCPB_LM_F32 ? 4 : 8);
   if (span <= few && p.items * 4 * tile >= slots * span) {

@@ -126,7 +126,9 @@ int ctcpb_lm_cache_store(const ctcpb_lm_store_args* args, void* stream);
  *   s_t = scale * q[r, head] . k[t, kv]      m = max s_t     l = sum exp(s_t - m)
  *   out[r, head] = sum exp(s_t - m) v[t, kv] / l        lse[r, head] = m + log l
  * A row with no token, or with every s_t = -inf, gives zeros and lse = -inf.
- * Slots past a row's length are never used, whatever they hold.
+ * Slots past a row's length are never used, whatever they hold.  Values within it
+ * have to be finite with 16-bit types (probabilities are two numbers there, one of
+ * which may be 0: an infinite value gives NaN).
  *   q, out   device, typed, element (r, head, d) at r*stride_r + head*stride_h + d
  *   lse      device float32 [rows][q_heads], or NULL
  *   tables   as ctcpb_lm_cache_plan leaves them; entries are clamped to the cache
