@@ -226,10 +226,15 @@ void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 // 20000 x 30000 x 1024 bf16 4340 us with 128 MB, 3381 with 512, 3182 with 2 GB;
 // 8192 x 50000 x 2048 4199 us with 512 MB (two pieces), 4035 in one.
 constexpr size_t kPieceBytes = (size_t)1 << 30;
-// Tokens up to which d has two rows each without being asked: for precision (see loss.h),
-// where it costs little.  64 x 5000 x 512 bf16 20.3 us with them, 21.5 without (another cut);
-// 64 x 20000 x 2048 86 and 75; 128 x 20000 x 2048 108 and 89.
+// Tokens, and multiplications of a product, up to which d has two rows for each token without
+// being asked: for precision (see loss.h), where it costs little.  64 x 5000 x 512 bf16 20.3
+// us with them, 21.5 without (another cut); 64 x 20000 x 2048 86 and 75; 128 x 20000 x 2048
+// 108 and 89.  Small calls wait for their launches, of which bf16 has one less so, and take up to
+// 2^26 0.95 to 1.0 times as long with them, f16 1.05 to 1.1 times (65 x 35 x 64 15.3 and 14.7
+// us, f16 15.4 and 16.6; 256 x 500 x 512 21.5 and 21.0, f16 21.4 and 23.4); at twice that up to
+// 1.1 and 1.2 (512 x 500 x 512 23.2 and 25.6, f16 23.3 and 27.9).
 constexpr int32_t kPairRows = 64;
+constexpr int64_t kPairWork = (int64_t)1 << 26;
 
 // How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
 struct TileShape {
@@ -412,7 +417,9 @@ bool wants_dbias(const ctcpb_lm_loss_args&) { return false; }
 bool wants_dbias(const ctcpb_lm_grad_args& g) { return g.dbias != nullptr; }
 bool wants_pairs(const ctcpb_lm_loss_args&) { return false; }
 bool wants_pairs(const ctcpb_lm_grad_args& g) {
-  return elem_size(type_of(g)) == 2 && (g.rows <= kPairRows || (g.dtype & CTCPB_LM_SPLIT_D));
+  if (elem_size(type_of(g)) != 2) return false;
+  return g.rows <= kPairRows || (double)g.rows * g.vocab * g.hidden <= kPairWork ||
+         (g.dtype & CTCPB_LM_SPLIT_D);
 }
 
 template <typename Args>

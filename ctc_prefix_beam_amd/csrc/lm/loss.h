@@ -17,8 +17,8 @@
 // 1.33 to 1.39, over a factor of 400 1.36 to 1.45; weights of 1 (2 % of the rows) and 0.51,
 // whose targets' entries are all rounded the same way, 1.8 to 2.2.
 //
-// With up to kPairRows tokens, too few to average over, and wherever the caller asks for
-// it, d is kept as the sum of two values of the type in neighbouring rows (2n and 2n + 1):
+// With up to kPairRows tokens or kPairWork multiplications, where errors average least, and
+// wherever the caller asks for it, d is kept as the sum of two values of the type in neighbouring rows (2n and 2n + 1):
 // 1.00 in all of these cases, for twice the products of dx and dw, which in small calls wait
 // for memory (8192 x 50000 x 2048 bf16: 4.04 and 7.25 ms, 20000 x 5000 x 1024: 0.63 and 0.96).
 #pragma once

@@ -363,7 +363,7 @@ def token_loss_backward(grad, x, w, targets, lse, bias=None, need=(True, True, T
     With 16-bit types the gradients of the logits are rounded to that type on the
     way: the errors of dx and dw are mostly 1.0 to 1.4 times those of rounding the exact
     results, up to 2.2 times where most rows share a weight that is not the largest.
-    `split_d` keeps them as the sum of two such values (as is done for up to 64 rows
+    `split_d` keeps them as the sum of two such values (as is done in small calls
     anyway), which leaves the results' own rounding, at twice the products."""
     dev, N, V, H, sizes = _loss_args(x, w, targets, bias)
     if split_d:

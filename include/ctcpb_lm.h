@@ -196,8 +196,8 @@ int ctcpb_lm_loss(const ctcpb_lm_loss_args* args, void* workspace, size_t worksp
  * rounding small): the errors of dx and dw are mostly 1.0 to 1.4 times those of
  * rounding the exact results, and up to 2.2 times where most rows share a weight that
  * is not the largest (their targets' entries are then rounded alike).  For up to 64
- * rows, and for any number with CTCPB_LM_SPLIT_D, d is the sum of two values of the
- * type, and the errors are those of rounding the results; dx and dw then take twice
+ * rows or rows * vocab * hidden of 2^26, and at any size with CTCPB_LM_SPLIT_D, d is the
+ * sum of two values of the type, and the errors are those of rounding the results; dx and dw then take twice
  * the products and d twice the room.  Sums
  * are float32.  The workspace holds up to 1 GiB of d at a time (256 columns of it
  * at least), the sums of dx if d is made in several pieces, those of products that

@@ -119,6 +119,25 @@ def test_gradients_by_a_split_d_are_off_by_their_own_rounding(dtype, N, V, H):
     assert float((bs.grad.double() - z.sum(0)).norm() / z.sum(0).norm()) < 2.0 ** -16
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,V,H", [(65, 35, 64), (167, 35, 73), (300, 500, 64), (100, 5000, 128),
+                                   (2000, 29, 512)])
+def test_small_calls_are_off_by_their_own_rounding(dtype, N, V, H):
+    """As with a split d, without being asked; two weights, one of them seldom, whose
+    targets' entries would all be rounded the same way."""
+    x, w, t, b, _ = make(N, V, H, dtype, seed=N)
+    grad = torch.where(torch.arange(N, device="cuda") % 50 == 7, 1.0, 0.51)
+    _, lse = lm.token_loss_forward(x, w, t, b)
+    dx, dw, _ = lm.token_loss_backward(grad, x, w, t, lse, b)
+    z = torch.softmax(x.double() @ w.double().t() + b.double(), 1)
+    live = torch.nonzero(t >= 0)[:, 0]
+    z[live, t[live].long()] -= 1
+    z *= torch.where(t >= 0, grad, 0.0).double()[:, None]
+    for got, want in ((dx, z @ w.double()), (dw, z.t().contiguous() @ x.double())):
+        least = (want.to(dtype).double() - want).norm()
+        assert float((got.double() - want).norm()) <= 1.02 * float(least)
+
+
 def test_split_d_of_f32_changes_nothing():
     x, w, t, b, grad = make(200, 300, 64, torch.float32)
     _, lse = lm.token_loss_forward(x, w, t, b)
