@@ -6,7 +6,7 @@
 // loss_join_kernel joins them.  Backward: a piece of the vocabulary at a time,
 //   d[n, v] = g[n] (exp(logit[n, v] - lse[n]) - [v = t[n]])
 // is recomputed, rounded to the inputs' type and kept for the piece only (at most
-// kPieceBytes of workspace); dx += d w and dw = d^T x follow from it.
+// kPieceBytes of workspace, or 256 labels); dx += d w and dw = d^T x follow from it.
 //
 // The rounding of d to 16 bits adds to dx and dw about what their own rounding to that
 // type does.  d is scaled so that the largest |g| is a power of two: the targets' entries,
@@ -69,8 +69,9 @@ struct TilePair {
 
 // The loss is bound by the matrix product, and then by the exponentials of its epilogue,
 // which the matrix units wait for (a quarter-rate instruction for each logit): 20000 x
-// 5000 x 1024 bf16 187 us a call, 1095 TFLOP/s, of which 166 without the epilogue (in a
-// copy); 8192 x 50000 x 2048 1.36 ms, 1230 TFLOP/s, and 1.24.  The matrix units are
+// 5000 x 1024 bf16 192 us a call (187 to 199 from card to card), 1070 TFLOP/s, of which 166
+// without the epilogue (in a copy) where the whole took 187; 8192 x 50000 x 2048 1.26 to 1.36
+// ms, 1330 to 1230 TFLOP/s, and 1.24 where it took 1.36.  The matrix units are
 // busy in 63 % of the cycles of the latter.
 //
 // The epilogues of the logits run with the next item's fetches under way, which

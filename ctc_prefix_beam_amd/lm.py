@@ -137,9 +137,12 @@ def _like(t, index, name, dtype, shape=None):
 
 def _pool(pool, index):
     """Entries of a pool of pages."""
-    _gpu(pool, "pool")
-    _i32(pool, index, "pool", (pool.numel(),))
-    return pool.numel()
+    if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.int32 and pool.dim() == 1 and
+            pool.get_device() == index and pool.is_contiguous()):
+        _gpu(pool, "pool")
+        _check_dev(pool, torch.device("cuda", index), "pool", torch.int32, (pool.numel(),),
+                   contiguous=True)
+    return pool.shape[0]
 
 
 def _tables(tables, index, rows):
