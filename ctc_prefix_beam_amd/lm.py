@@ -175,6 +175,13 @@ def _rows(t, name):
     raise ValueError(f"{name} must have three axes, the last one with unit stride")
 
 
+def _apart(t, strides, name):
+    """Raise ValueError if elements of a tensor that is written share memory (an expanded
+    axis): which of their values stays would be a matter of chance."""
+    if 0 in strides and any(n > 1 and s == 0 for n, s in zip(t.shape, strides)):
+        raise ValueError(f"{name} is written, and must not have expanded axes")
+
+
 def _type(t, name):
     dt = _TYPES.get(t.dtype)
     if dt is None:
@@ -258,6 +265,8 @@ def cache_store(k, v, slots, k_cache, v_cache, stream=None):
     kc = _cache(k_cache, dev, "k_cache", k.dtype)
     pages, page_size, heads, dim = cs = k_cache.shape
     vc = _cache(v_cache, dev, "v_cache", k.dtype, cs)
+    _apart(k_cache, kc[1:], "k_cache")
+    _apart(v_cache, vc[1:], "v_cache")
     if heads != H or dim != D:
         raise ValueError(f"caches must have {H} heads of {D}, got {(heads, dim)}")
     if T == 0:
@@ -294,6 +303,7 @@ def attention(q, k_cache, v_cache, tables, lengths, scale: float | None = None, 
     else:
         _like(out, dev, "out", q.dtype, shape)
     outr, outh, _ = _rows(out, "out")
+    _apart(out, (outr, outh), "out")
     lse = empty((R, Hq), dtype=torch.float32, device=q.device)
     args = _pack(
         _ATTENTION, q.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),

@@ -17,6 +17,7 @@
  * ctcpb_lm_last_error().  On error nothing was enqueued, except
  * CTCPB_ERR_DEVICE, reported when a launch fails.  Each call takes its operands
  * in a structure that it reads before it returns.  Strides are in elements.
+ * Elements of a tensor that is written must not share memory.
  * Results do not depend on the order in which workgroups run: two calls on the
  * same inputs give the same bits.
  */

@@ -151,3 +151,19 @@ def test_a_captured_append_repeats_itself():
         assert plan.lengths.tolist() == [4, 0, 10] and not plan.status.any(), i
         assert plan.positions.tolist() == [2, 3, 5, 6, 7, 8, 9], i
         torch.ones(1000, device="cuda").cumsum(0)
+
+
+def test_expanded_tensors_are_not_written():
+    q = torch.zeros((2, 4, 64), dtype=torch.float16, device="cuda")
+    c = torch.zeros((3, 16, 2, 64), dtype=q.dtype, device="cuda")
+    tab, lens = torch.zeros((2, 1), dtype=torch.int32, device="cuda"), i32(3, 4)
+    for out in (q[:1].expand(2, 4, 64), q[:, :1].expand(2, 4, 64)):
+        with pytest.raises(ValueError, match="out is written"):
+            lm.attention(q, c, c, tab, lens, out=out)
+    lm.attention(q[:1], c, c, tab[:1], lens[:1], out=q[1:].expand(1, 4, 64))
+    for wide in (c[:1].expand(3, 16, 2, 64), c[:, :1].expand(3, 16, 2, 64),
+                 c[:, :, :1].expand(3, 16, 2, 64)):
+        for kc, vc, name in ((wide, c, "k_cache"), (c, wide, "v_cache")):
+            with pytest.raises(ValueError, match=name + " is written"):
+                lm.cache_store(q[:, :2], q[:, :2], i32(0, 1), kc, vc)
+        lm.attention(q, wide, wide, tab, lens)   # read, they may be
