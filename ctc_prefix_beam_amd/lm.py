@@ -6,10 +6,10 @@ the pages and slots of a paged key/value cache from device-resident lengths
 (``cache_store``), the attention of one new token per request over the cache
 (``attention``), and token losses over a large vocabulary without keeping the
 logits, with their gradients (``token_loss``).  ``PagedCache`` holds the tensors
-of a cache.  Every step
-runs in the library's HIP kernels; PyTorch provides device memory and the
-current stream.  If the library is missing the calls raise; there is no CPU
-fallback.
+of a cache.  Every step runs in the library's HIP kernels; PyTorch provides
+device memory and the current stream.  A call's `stream` (a torch stream, default
+the current one) is where it runs: its inputs have to be ready there, and its
+results are.  If the library is missing the calls raise; there is no CPU fallback.
 """
 from __future__ import annotations
 
