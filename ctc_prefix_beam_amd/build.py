@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "ctcpb.hip")
 LIB = os.path.join(HERE, "libctcpb.so")
-LM_SRC = os.path.join(HERE, "csrc", "lm", "lm.hip")
+LM_SRC = [os.path.join(HERE, "csrc", "lm", name) for name in ("lm.hip", "lm8.hip")]
 LM_LIB = os.path.join(HERE, "libctcpb_lm.so")
 
 # -ffp-contract=off: every float operation rounds once (the decoder's numerics
@@ -24,10 +24,12 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-ffp
 LM_FLAGS = [f for f in FLAGS if f != "-ffp-contract=off"]
 
 
-def _compile(flags, src: str, lib: str, verbose: bool) -> str:
+def _compile(flags, src, lib: str, verbose: bool) -> str:
+    """Compiles one source, or several one after another, into `lib`."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = lib + ".tmp"
-    proc = subprocess.run([hipcc, *flags, src, "-o", tmp], capture_output=True, text=True)
+    proc = subprocess.run([hipcc, *flags, *([src] if isinstance(src, str) else src),
+                           "-o", tmp], capture_output=True, text=True)
     out = "\n".join(l for l in (proc.stdout + proc.stderr).splitlines()
                     if "packed-fp32-ops' is not a recognized feature" not in l)
     if proc.returncode != 0:

@@ -47,7 +47,7 @@
 // hundred tokens: 12 us, the latency of a handful of dependent loads (lengths, table,
 // keys, values) and the join of eight waves.
 #pragma once
-#include "cache.h"
+#include "common.h"
 
 namespace ctcpb_lm {
 
@@ -129,6 +129,13 @@ template <int NA>
 struct WaveState {
   float m, l;      // scores stay in natural units: times log2(e), the lowest float is -inf
   f32x4 acc[NA];   // kRaise times the sums; acc[j][r]: see the tile functions for the d
+
+  __device__ void reset() {
+    m = neg_inf();
+    l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NA; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  }
 };
 
 // The page of token t's group of four.  It does not wait for the request's length:
@@ -148,12 +155,25 @@ struct Spot {
 // ---- 16-bit types: 32 tokens x DP (64, 128 or 256) -----------------------
 template <typename T, int DP>
 struct Tile {
+  typedef T Type;
+  typedef AttnArgs Args;
+  static constexpr int kDP = DP;
+  static constexpr int kAloneWaves = DP == 64 ? 4 : 1;   // on a SIMD: a wave to an item
+  static constexpr int kRangeOnSimd = DP == 64 ? 4 : DP == 128 ? 3 : 1;   // and ranges
   static constexpr int kTokens = 32;
   static constexpr int kK = DP / 32;            // k-steps of the score product
   static constexpr int kV = DP >= 128 ? 8 : 4;  // values a lane loads at once
   static constexpr int kH = DP / 16 / kV;       // such loads per token
   static constexpr int kAcc = DP / 16;
   typedef typename Elem<T>::V8 V8;
+  typedef WaveState<kAcc> State;
+
+  // what takes the sums' factor away
+  static __device__ float lower(const State&) { return 1.0f / Elem<T>::kRaise; }
+  // neighbouring items that are done on the same XCD
+  static __device__ int together(const Args& a) { return a.head_tiles; }
+
+  __device__ void head(const Args&, int) {}
 
   V8 q[kK], kf[2][kK];
   uint32_t vr[8][kH][kV / 2];
@@ -302,10 +322,24 @@ struct Tile {
 // ---- f32: 16 tokens x DP -------------------------------------------------
 template <int DP>
 struct Tile<float, DP> {
+  typedef float Type;
+  typedef AttnArgs Args;
+  static constexpr int kDP = DP;
+  static constexpr int kAloneWaves = DP == 64 ? 4 : 1;
+  static constexpr int kRangeOnSimd = DP == 64 ? 4 : 1;
   static constexpr int kTokens = 16;
   static constexpr int kK = DP / 16;
   static constexpr int kH = DP / 64;
   static constexpr int kAcc = DP / 16;
+
+  typedef WaveState<kAcc> State;
+
+  // what takes the sums' factor away
+  static __device__ float lower(const State&) { return 1.0f / Elem<float>::kRaise; }
+  // neighbouring items that are done on the same XCD
+  static __device__ int together(const Args& a) { return a.head_tiles; }
+
+  __device__ void head(const Args&, int) {}
 
   f32x4 q[kK], kf[kK], vf[4][kH];
 
@@ -418,15 +452,19 @@ template <typename T, int N>
 __device__ inline void store_run(const AttnArgs& a, int row, int head, int d, const float (&v)[N]) {
   if (d >= a.D) return;
   T* to = reinterpret_cast<T*>(a.out) + row * a.out_r + head * a.out_h + d;
-  typedef T TN __attribute__((ext_vector_type(N)));
-  TN t;
+  constexpr int M = N * (int)sizeof(T) <= 16 ? N : 16 / (int)sizeof(T);   // 16 bytes at most
+  typedef T TM __attribute__((ext_vector_type(M)));
 #pragma unroll
-  for (int i = 0; i < N; ++i) t[i] = (T)v[i];
-  if (a.wide_out) {
-    *reinterpret_cast<TN*>(to) = t;
-  } else {
+  for (int x = 0; x < N; x += M) {
+    TM t;
 #pragma unroll
-    for (int i = 0; i < N; ++i) to[i] = t[i];
+    for (int i = 0; i < M; ++i) t[i] = (T)v[x + i];
+    if (a.wide_out) {
+      *reinterpret_cast<TM*>(to + x) = t;
+    } else {
+#pragma unroll
+      for (int i = 0; i < M; ++i) to[x + i] = t[i];
+    }
   }
 }
 
@@ -439,36 +477,32 @@ __device__ inline void store_lse(const AttnArgs& a, int row, int head, float m, 
 }
 
 // What the waves of a workgroup do for one head tile of one key/value head.
-template <typename T, int DP>
+template <typename TL>
 struct Attend {
-  typedef Tile<T, DP> TL;
+  typedef typename TL::Type T;
+  typedef typename TL::Args Args;
+  static constexpr int DP = TL::kDP;
   static constexpr int kRun = TL::kRun, kRuns = TL::kAcc / kRun;
   static constexpr int kPitch = DP + 4;   // a head's place in LDS, and in `part` D + 2
 
   int head0, nh;
   const char *kbase, *vbase;
   TL tile;
-  WaveState<TL::kAcc> s;
+  typename TL::State s;
 
-  __device__ void head(const AttnArgs& a, int hh) {
+  __device__ void head(const Args& a, int hh) {
     const int kvh = hh / a.head_tiles, ht = hh % a.head_tiles;
     nh = min(16, a.group - ht * 16);
     head0 = kvh * a.group + ht * 16;
     kbase = a.kc.data + kvh * a.kc.head;
     vbase = a.vc.data + kvh * a.vc.head;
+    tile.head(a, kvh);
   }
 
   __device__ bool live() const { return (int)(threadIdx.x & 15) < nh; }
 
-  __device__ void reset() {
-    s.m = neg_inf();
-    s.l = 0.0f;
-#pragma unroll
-    for (int j = 0; j < TL::kAcc; ++j) s.acc[j] = f32x4{0, 0, 0, 0};
-  }
-
   // The tiles at at.t0, then.t0, and so on every `step` tokens, before `end`.
-  __device__ void tiles(const AttnArgs& a, const int32_t* table, int row, const Range& rg, Spot at,
+  __device__ void tiles(const Args& a, const int32_t* table, int row, const Range& rg, Spot at,
                         Spot then, int step, int32_t end) {
     if (at.t0 >= end) return;
     tile.load_keys(a, kbase, at);
@@ -491,9 +525,9 @@ struct Attend {
 
   // Joins the states of NW waves through LDS ([NW][nh][kPitch] sums, then (m, l)
   // pairs): to the result, or to `part` ([nh][D], then [nh] pairs) if not null.  The
-  // sums lose their factor kRaise here.
+  // sums lose their factor here.
   template <int NW>
-  __device__ void join(const AttnArgs& a, int row, int wave, float* lds, float* part) {
+  __device__ void join(const Args& a, int row, int wave, float* lds, float* part) {
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const float l = sum_over_groups(s.l);
     float* ml = lds + NW * nh * kPitch;
@@ -512,7 +546,7 @@ struct Attend {
             *reinterpret_cast<f32x4*>(mine + TL::run_of(b, r) + j) =
                 f32x4{s.acc[b * kRun + j][r], s.acc[b * kRun + j + 1][r],
                       s.acc[b * kRun + j + 2][r], s.acc[b * kRun + j + 3][r]} *
-                (1.0f / Elem<T>::kRaise);
+                TL::lower(s);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < nh * (DP / 4); i += 64 * NW) {
@@ -546,30 +580,29 @@ struct Attend {
 // head tiles of one key/value head come eight apart: they find its keys and values in
 // the same L2 (32 requests of 8000 tokens, one key/value head of 128, bf16: 128 query
 // heads 159 us with neighbouring workgroups, 91 so; 32 heads 53 and 41).
-__device__ inline int item_of(int block, int blocks, int head_tiles) {
-  if (head_tiles == 1) return block;
-  const int first = block / (8 * head_tiles) * 8;   // of the key/value heads
-  const int wide = min(8, blocks / head_tiles - first), o = block - first * head_tiles;
-  return (first + o % wide) * head_tiles + o / wide;
+__device__ inline int item_of(int block, int blocks, int together) {
+  if (together == 1) return block;
+  const int first = block / (8 * together) * 8;   // of the key/value heads
+  const int wide = min(8, blocks / together - first), o = block - first * together;
+  return (first + o % wide) * together + o / wide;
 }
 
 // NW waves to an item (row, key/value head, head tile); with one, a workgroup's
 // four waves have four items.  Eight waves against a wave to an item, key/value heads
 // of 64, bf16, in us: 64 requests of up to 256 tokens with 4 heads 5.8 and 12.1, 4096 of
 // up to 512 268 and 223; f32, one request of 300 tokens with 8 heads: 9.1 and 28.7.
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW, NW == 1 && DP == 64 ? 4 : 1)
-void attn_kernel(AttnArgs a) {
-  typedef Attend<T, DP> A;
-  typedef typename A::TL TL;
+template <typename TL, int NW>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW, NW == 1 ? TL::kAloneWaves : 1)
+void attn_kernel(typename TL::Args a) {
+  typedef Attend<TL> A;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = NW == 1 ? (int)blockIdx.x * 4 + wave
-                           : item_of(blockIdx.x, gridDim.x, a.head_tiles);
+                           : item_of(blockIdx.x, gridDim.x, TL::together(a));
   if (NW == 1 && item >= a.items) return;
   const int all = a.kv_heads * a.head_tiles, row = item / all;
   A at;
   at.head(a, item % all);
-  at.reset();
+  at.s.reset();
   const int32_t* table = a.tables + row * a.table_stride;
   constexpr int kStep = NW * TL::kTokens;
   const int32_t mine = (NW == 1 ? 0 : wave) * TL::kTokens;
@@ -591,7 +624,7 @@ void attn_kernel(AttnArgs a) {
     const int lane = threadIdx.x & 63, c = lane & 15;
     const float l = sum_over_groups(at.s.l);
     if (!at.live()) return;
-    const float scale = l == 0.0f ? 0.0f : 1.0f / l * (1.0f / Elem<T>::kRaise);
+    const float scale = l == 0.0f ? 0.0f : 1.0f / l * TL::lower(at.s);
 #pragma unroll
     for (int b = 0; b < A::kRuns; ++b)
 #pragma unroll
@@ -599,7 +632,7 @@ void attn_kernel(AttnArgs a) {
         float v[A::kRun];
 #pragma unroll
         for (int j = 0; j < A::kRun; ++j) v[j] = at.s.acc[b * A::kRun + j][r] * scale;
-        store_run<T, A::kRun>(a, row, at.head0 + c, TL::run_of(b, r), v);
+        store_run<typename TL::Type, A::kRun>(a, row, at.head0 + c, TL::run_of(b, r), v);
       }
     if (lane < 16) store_lse(a, row, at.head0 + c, at.s.m, l);
   }
@@ -630,18 +663,17 @@ __device__ inline float* part_at(const AttnArgs& a, int range, int hh, bool insi
   return a.part + slot * part_floats(a.group, a.D);
 }
 
-template <typename T, int DP>
-__global__ __launch_bounds__(64 * kRangeWaves, DP == 64 ? 4 : DP == 128 && sizeof(T) == 2 ? 3 : 1)
-void attn_range_kernel(AttnArgs a) {
-  typedef Attend<T, DP> A;
-  typedef typename A::TL TL;
+template <typename TL>
+__global__ __launch_bounds__(64 * kRangeWaves, TL::kRangeOnSimd)
+void attn_range_kernel(typename TL::Args a) {
+  typedef Attend<TL> A;
   constexpr int kTile = TL::kTokens, kStep = kRangeWaves * kTile, kThreads = 64 * kRangeWaves;
   extern __shared__ float lds[];
   int32_t* scan = reinterpret_cast<int32_t*>(lds);   // before the first join needs it
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int all = a.kv_heads * a.head_tiles;
-  const int item = item_of(blockIdx.x, gridDim.x, a.head_tiles);
+  const int item = item_of(blockIdx.x, gridDim.x, TL::together(a));
   const int range = item / all, hh = item % all;
   // prefix sums of the rows' steps: a thread has `per` neighbouring rows
   const int per = (a.rows + kThreads - 1) / kThreads;
@@ -696,7 +728,7 @@ void attn_range_kernel(AttnArgs a) {
       one = TL::spot(a, table, t0);
       two = TL::spot(a, table, t0 + kStep);
     }
-    s.reset();
+    s.s.reset();
     s.tiles(a, table, row, rg, one, two, kStep, end);
     const bool whole = from == 0 && to == n;
     s.template join<kRangeWaves>(a, row, wave, lds,
@@ -715,8 +747,10 @@ void attn_range_kernel(AttnArgs a) {
 // head's parts, taken in turn, and are joined in their order.  Bound by latency: 6.6 us
 // behind 256 ragged requests (8192 heads, most with one or two parts), 8.8 us behind
 // three long ones (192 heads of some 40 parts).
-template <typename T, int LANES>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int ways) {
+template <typename TL>
+__global__ __launch_bounds__(256) void join_kernel(typename TL::Args a, int ways) {
+  typedef typename TL::Type T;
+  constexpr int LANES = TL::kDP / 4;
   constexpr int kGroups = 256 / LANES;
   __shared__ f32x4 sums[kGroups][LANES];
   __shared__ float2 stats[kGroups];

@@ -245,11 +245,6 @@ __global__ __launch_bounds__(kPlanThreads) void release_kernel(ReleaseArgs a) {
 }
 
 // ----------------------------------------------------------------- store --
-struct CacheView {
-  char* data;
-  int64_t page, token, head;   // strides in bytes
-};
-
 struct StoreArgs {
   const char *k, *v;
   int64_t k_t, k_h, v_t, v_h;   // strides in bytes

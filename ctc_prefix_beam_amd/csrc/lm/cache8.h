@@ -1,0 +1,327 @@
+// A paged key/value cache held in 8 bits, with a scale for each page and head: keys and
+// values quantised as they are stored, and read back.
+#pragma once
+#include "codes.h"
+
+namespace ctcpb_lm {
+
+struct ScaleView {
+  float* data;
+  int64_t page, head;   // strides in floats
+};
+
+struct Cache8Args {
+  char *k, *v;                  // read by the store, written by the load
+  int64_t k_t, k_h, v_t, v_h;   // strides in bytes
+  const int32_t* slots;
+  CacheView kc, vc;
+  ScaleView ks, vs;
+  int32_t tokens, heads, dim;
+  int32_t page_log, num_slots;
+  int32_t per;                  // pieces of a head's row
+  int32_t chunk;                // store: tokens of a wave
+};
+
+// Maximum over the wave of `most`, magnitudes of T as Values::raise leaves them.
+template <typename T>
+__device__ inline uint32_t wave_magnitude(uint32_t most) {
+  uint32_t m = Values<T, 1>::magnitude(most);
+  for (int x = 1; x < 64; x <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, x));
+  return m;
+}
+
+// ----------------------------------------------------------------- store --
+//
+// For the tokens t of the call that go to page p, and head h:
+//   scale[p, h] = max(old, least power of two u with max_t |x[t, h]| <= top u)
+//   code = nearest code to x / scale
+// where old is 0 if a token goes to slot 0 of the page, which begins it anew, else what the
+// page has.  Where a page's scale grows, its codes are multiplied by old / new first.
+//
+// A wave makes a page's scale and codes by itself, so nothing crosses waves: tokens of one
+// page follow one another in the call, and the wave that has the first of them in its chunk
+// of `chunk` tokens (the one before with a slot lies in another page) does the page's whole
+// run, for one head of the keys or of the values.  A run's values stay in registers
+// between the two passes (maximum, codes) up to kHeld pieces a lane.
+//
+// Bound by memory for prompts and by latency for a step of single tokens.
+constexpr int kStoreHeld = 4;
+
+// The page of the nearest token with a slot before token t, -1 if there is none.
+__device__ inline int32_t page_before(const Cache8Args& a, int32_t t, int lane) {
+  for (int32_t end = t; end > 0; end -= 64) {
+    const int32_t i = end - 64 + lane;
+    const int32_t s = i >= 0 ? a.slots[i] : -1;
+    const uint64_t in = __ballot((uint32_t)s < (uint32_t)a.num_slots);
+    if (in) return __builtin_amdgcn_readlane(s, 63 - __builtin_clzll(in)) >> a.page_log;
+  }
+  return -1;
+}
+
+template <typename T, typename C, int N>
+struct StoreRun {
+  static constexpr int U = kStoreHeld;
+  const char* src;          // the head's row of token 0
+  int64_t src_t;
+  char* page;               // the head's row of slot 0
+  int64_t token;
+  const int32_t* slots;     // of the run's first token
+  int32_t count, num_slots, mask, per;
+  int lane;
+
+  // The lane's piece number i: token and piece of its row.
+  struct At {
+    int32_t t, j;
+  };
+  __device__ At first() const { return At{lane / per, lane % per}; }
+  __device__ void next(At& at) const {
+    at.t += 64 / per;
+    at.j += 64 % per;
+    if (at.j >= per) {
+      at.j -= per;
+      ++at.t;
+    }
+  }
+
+  Values<T, N> x[U];
+  int32_t slot[U];
+
+  // Loads U pieces from `at` on, which moves past them.
+  __device__ void load(At& at) {
+    At b = at;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      slot[u] = b.t < count ? slots[b.t] : -1;
+      next(b);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a token without a slot is not read: it may hold anything
+      if ((uint32_t)slot[u] < (uint32_t)num_slots) {
+        x[u].load(src + at.t * src_t + at.j * (int)(N * sizeof(T)));
+      } else {
+        slot[u] = -1;
+#pragma unroll
+        for (uint32_t& w : x[u].w) w = 0;
+      }
+      next(at);
+    }
+  }
+
+  __device__ void raise(uint32_t& most) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].raise(most);
+  }
+
+  // Writes the codes of the pieces that load() took from `at` on.
+  __device__ void write(At at, float inverse) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (slot[u] >= 0) {
+        char* to = page + (slot[u] & mask) * token + at.j * N;
+        if constexpr (N == 1) {
+          // a scale that is not finite has codes of 0, whatever the values
+          const float v = inverse == 0.0f ? 0.0f : x[u].at(0) * inverse;
+          *reinterpret_cast<uint8_t*>(to) = (uint8_t)C::round4(v, 0, 0, 0);
+        } else {
+          uint32_t w[N / 4];
+#pragma unroll
+          for (int i = 0; i < N / 4; ++i) {
+            float v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = x[u].at(4 * i + r) * inverse;
+            w[i] = inverse == 0.0f ? 0 : C::round4(v[0], v[1], v[2], v[3]);
+          }
+          if constexpr (N == 8)
+            *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+          else
+            *reinterpret_cast<uint32_t*>(to) = w[0];
+        }
+      }
+      next(at);
+    }
+  }
+
+  // Multiplies the page's codes by `ratio`, a power of two below one.
+  __device__ void rescale(float ratio) const {
+    At at = first();
+    for (; at.t <= mask; next(at)) {
+      char* p = page + at.t * token + at.j * N;
+      if constexpr (N == 1) {
+        float v[4];
+        C::values4(*reinterpret_cast<uint8_t*>(p), v);
+        *reinterpret_cast<uint8_t*>(p) = (uint8_t)C::round4(v[0] * ratio, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+          uint32_t* q = reinterpret_cast<uint32_t*>(p) + i;
+          float v[4];
+          C::values4(*q, v);
+          *q = C::round4(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+        }
+      }
+    }
+  }
+};
+
+// N: values of a piece, 8 (16-bit types) or 4 (f32) where rows and strides allow, else 1.
+template <typename T, typename C, int N>
+__global__ __launch_bounds__(256) void store8_kernel(Cache8Args a) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;   // (chunk, head, keys or values)
+  const int64_t chunk = unit / (2 * a.heads);
+  const int64_t begin = chunk * a.chunk;
+  if (begin >= a.tokens) return;
+  const int32_t head = (int32_t)(unit % (2 * a.heads)) >> 1;
+  const bool values = unit & 1;
+  const int32_t t0 = (int32_t)begin, n = min(a.chunk, a.tokens - t0);
+
+  const int32_t slot = lane < n ? a.slots[t0 + lane] : -1;
+  const int32_t prev = t0 > 0 ? a.slots[t0 - 1] : -1;
+  const bool in = (uint32_t)slot < (uint32_t)a.num_slots;
+  const int32_t mine = in ? slot >> a.page_log : -1;
+  const uint64_t all = __ballot(in);
+  if (all == 0) return;
+  // the page of the token with a slot before the lane's own
+  const uint64_t below = all & ((1ull << lane) - 1);
+  int32_t before = __shfl(mine, below ? 63 - __builtin_clzll(below) : 0);
+  // mostly it is the one right in front of the chunk, asked for along with the chunk's
+  const int32_t outside = (uint32_t)prev < (uint32_t)a.num_slots ? prev >> a.page_log
+                                                                 : page_before(a, t0 - 1, lane);
+  if (!below) before = outside;
+  uint64_t leaders = __ballot(in && mine != before);
+
+  const CacheView& c = values ? a.vc : a.kc;
+  const ScaleView& sc = values ? a.vs : a.ks;
+  const int32_t mask = (1 << a.page_log) - 1;
+  while (leaders) {
+    const int first = __builtin_ctzll(leaders);
+    leaders &= leaders - 1;
+    const int32_t page = __builtin_amdgcn_readlane(mine, first);
+    // The run: up to the last token of the page before another one begins.
+    const uint64_t until = leaders ? (1ull << __builtin_ctzll(leaders)) - 1 : ~0ull;
+    const uint64_t same = all & until & ~((1ull << first) - 1);
+    int32_t last = t0 + 63 - __builtin_clzll(same), held = __popcll(same);
+    bool begun = (__ballot(in && (slot & mask) == 0) & same) != 0;
+    if (!leaders) {
+      // it may go on past the chunk, for as many tokens as the page has slots
+      for (int32_t t = t0 + n; t < a.tokens && held <= mask; t += 64) {
+        const int32_t i = t + lane, s = i < a.tokens ? a.slots[i] : -1;
+        const uint64_t there = __ballot((uint32_t)s < (uint32_t)a.num_slots);
+        const uint64_t other = there & __ballot(s >> a.page_log != page);
+        const uint64_t ours = there & (other ? (other & -other) - 1 : ~0ull);
+        if (ours) {
+          last = t + 63 - __builtin_clzll(ours);
+          held += __popcll(ours);
+          begun = begun || (ours & __ballot((s & mask) == 0)) != 0;
+        }
+        if (other) break;
+      }
+    }
+    StoreRun<T, C, N> run;
+    const int32_t from = t0 + first;
+    run.src_t = values ? a.v_t : a.k_t;
+    run.src = (values ? a.v + head * a.v_h : a.k + head * a.k_h) + from * run.src_t;
+    run.page = c.data + page * c.page + head * c.head;
+    run.token = c.token;
+    run.slots = a.slots + from;
+    run.count = last - from + 1;
+    run.num_slots = a.num_slots;
+    run.mask = mask;
+    run.per = a.per;
+    run.lane = lane;
+    float* scale = sc.data + page * sc.page + head * sc.head;
+    const float old = begun ? 0.0f : *scale;
+    // lane 0's pieces are the first of each load: the loop is the same for all lanes
+    const int64_t pieces = (int64_t)run.count * a.per;
+    const int64_t batches = (pieces + 64 * run.U - 1) / (64 * run.U);
+    typename StoreRun<T, C, N>::At at = run.first();
+    const auto at0 = at;
+    uint32_t most = 0;
+    for (int64_t b = 0; b < batches; ++b) {
+      run.load(at);
+      run.raise(most);
+    }
+    const float need = bits_f32(unit_bits<C>(wave_magnitude<T>(most)));
+    // (a NaN stays, whichever of the two it is)
+    const float now = old != old ? old : need != need || need > old ? need : old;
+    if (now > old && old > 0.0f) {
+      run.rescale(old / now);
+      // the new codes go over some of these
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const float inverse = inverse_unit(now);
+    if (batches == 1) {
+      run.write(at0, inverse);
+    } else {
+      at = at0;
+      for (int64_t b = 0; b < batches; ++b) {
+        const auto here = at;
+        run.load(at);
+        run.write(here, inverse);
+      }
+    }
+    if (lane == 0) *scale = now;
+  }
+}
+
+// ------------------------------------------------------------------ load --
+//
+// k[t, h] = code * scale of the token's slot, in T; zeros for a token without a slot.  A
+// copy, bound by memory.  A thread makes 16 bytes of a key's row and the same of the value's.
+template <typename T, typename C, int N>
+__global__ __launch_bounds__(256) void load8_kernel(Cache8Args a) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  const int32_t row = a.heads * a.per;
+  const int64_t pieces = (int64_t)a.tokens * row;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += step) {
+    const int32_t t = (int32_t)(i / row), rest = (int32_t)(i % row);
+    const int32_t h = rest / a.per, p = rest % a.per;
+    const int32_t slot = a.slots[t];
+    const bool in = (uint32_t)slot < (uint32_t)a.num_slots;
+    const int64_t page = in ? slot >> a.page_log : 0, at = slot & ((1 << a.page_log) - 1);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const CacheView& c = half ? a.vc : a.kc;
+      const ScaleView& sc = half ? a.vs : a.ks;
+      T* to = reinterpret_cast<T*>((half ? a.v + t * a.v_t + h * a.v_h
+                                         : a.k + t * a.k_t + h * a.k_h)) + p * N;
+      T out[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) out[j] = (T)0.0f;
+      if (in) {
+        const char* from = c.data + page * c.page + at * c.token + h * c.head + p * N;
+        const float scale = sc.data[page * sc.page + h * sc.head];
+        float v[4];
+        if constexpr (N == 1) {
+          C::values4(*reinterpret_cast<const uint8_t*>(from), v);
+          out[0] = (T)(v[0] * scale);
+        } else {
+          uint32_t w[N / 4];
+          if constexpr (N == 8) {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(from);
+            w[0] = x[0];
+            w[1] = x[1];
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(from);
+          }
+#pragma unroll
+          for (int b = 0; b < N / 4; ++b) {
+            C::values4(w[b], v);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[4 * b + r] = (T)(v[r] * scale);
+          }
+        }
+      }
+      if constexpr (N == 1) {
+        *to = out[0];
+      } else {
+        static_assert(N * sizeof(T) == 16, "a piece is 16 bytes");
+        *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, out);
+      }
+    }
+  }
+}
+
+}  // namespace ctcpb_lm

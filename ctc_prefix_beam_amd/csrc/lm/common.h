@@ -7,6 +7,7 @@
 namespace ctcpb_lm {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -37,5 +38,11 @@ __device__ inline float sum_over_groups(float v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
+
+// A paged cache of keys or values.
+struct CacheView {
+  char* data;
+  int64_t page, token, head;   // strides in bytes
+};
 
 }  // namespace ctcpb_lm

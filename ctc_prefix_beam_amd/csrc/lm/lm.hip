@@ -3,117 +3,18 @@
 #include "ctcpb_lm.h"
 
 #include <algorithm>
-#include <climits>
-#include <exception>
-#include <string>
 #include <type_traits>
 
-#include "attention.h"
+#include "attention_host.h"
 #include "cache.h"
-#include "ctcpb.h"
+#include "gemm_host.h"
 #include "loss.h"
 
 using namespace ctcpb_lm;
 
 namespace {
 
-thread_local std::string g_err;
-
-int ok() {
-  g_err.clear();
-  return CTCPB_OK;
-}
-
-int fail(int code, const char* msg) {
-  g_err = msg;
-  return code;
-}
-
-int launched(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return ok();
-  g_err = std::string(what) + " launch failed: " + hipGetErrorString(e);
-  return CTCPB_ERR_DEVICE;
-}
-
-// No C++ exception leaves a C entry point (the only ones possible here are
-// allocation failures of the error text).
-template <typename F>
-int guarded(F f) {
-  try {
-    return f();
-  } catch (...) {
-    return CTCPB_ERR_DEVICE;
-  }
-}
-
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-int32_t ceil_div(int64_t a, int64_t b) { return (int32_t)((a + b - 1) / b); }
-
-int log2_of(int32_t v) {
-  int n = 0;
-  while ((1 << n) < v) ++n;
-  return n;
-}
-
-bool page_size_ok(int32_t ps) { return ps >= 4 && ps <= 256 && (ps & (ps - 1)) == 0; }
-
-int elem_size(int32_t dtype) {
-  return dtype == CTCPB_LM_BF16 || dtype == CTCPB_LM_F16 ? 2 : dtype == CTCPB_LM_F32 ? 4 : 0;
-}
-
-constexpr const char* kBadPage = "page_size must be a power of two in 4..256";
-constexpr const char* kBadType = "dtype must be CTCPB_LM_BF16, CTCPB_LM_F16 or CTCPB_LM_F32";
-constexpr const char* kNull = "a required pointer is NULL";
-constexpr const char* kNoArgs = "args is NULL";
-
-int check_table(int32_t rows, int64_t stride, int32_t width, int32_t page_size) {
-  if (rows < 0 || width < 0) return fail(CTCPB_ERR_INVALID, "rows and table_width must be >= 0");
-  if (!page_size_ok(page_size)) return fail(CTCPB_ERR_INVALID, kBadPage);
-  if (stride < width) return fail(CTCPB_ERR_INVALID, "table_stride must be >= table_width");
-  if ((int64_t)width * page_size > (1 << 30))
-    return fail(CTCPB_ERR_INVALID, "table_width * page_size must be at most 2^30");
-  return CTCPB_OK;
-}
-
-int check_pages(int32_t num_pages, int32_t page_size) {
-  if (!page_size_ok(page_size)) return fail(CTCPB_ERR_INVALID, kBadPage);
-  if (num_pages < 1 || (int64_t)num_pages * page_size > INT_MAX)
-    return fail(CTCPB_ERR_INVALID, "num_pages must be >= 1 and num_pages * page_size below 2^31");
-  return CTCPB_OK;
-}
-
-int check_cache(const ctcpb_lm_cache& c) {
-  if (!c.data) return fail(CTCPB_ERR_INVALID, kNull);
-  if (c.stride_page < 0 || c.stride_token < 0 || c.stride_head < 0)
-    return fail(CTCPB_ERR_INVALID, "cache strides must be >= 0");
-  return CTCPB_OK;
-}
-
-CacheView view(const ctcpb_lm_cache& c, int es) {
-  return CacheView{static_cast<char*>(c.data), c.stride_page * es, c.stride_token * es,
-                   c.stride_head * es};
-}
-
-bool wide_cache(const CacheView& v) {
-  return aligned(v.data, 16) && v.page % 16 == 0 && v.token % 16 == 0 && v.head % 16 == 0;
-}
-
 // ------------------------------------------------------------- attention --
-
-// The launch plan of an attention call, a function of sizes only (the lengths
-// stay on the device).
-struct AttnPlan {
-  int32_t head_tiles, max_len, waves, ranges;
-  int64_t items;
-  size_t o_part, bytes;   // workspace: the rows' prefix sums, then the parts
-};
-
-int32_t length_bound(const ctcpb_lm_attention_args& g) {
-  const int32_t held = g.table_width * g.page_size;
-  return g.max_len == 0 || g.max_len > held ? held : g.max_len;
-}
 
 AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
   AttnPlan p{};
@@ -168,56 +69,14 @@ AttnPlan plan_attention(const ctcpb_lm_attention_args& g) {
   return p;
 }
 
-int check_attention(const ctcpb_lm_attention_args& g) {
-  if (!elem_size(g.dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
-  if (g.kv_heads < 1 || g.q_heads < g.kv_heads || g.q_heads % g.kv_heads)
-    return fail(CTCPB_ERR_INVALID, "q_heads must be a multiple of kv_heads >= 1");
-  if (g.head_dim < 8 || g.head_dim % 8)
-    return fail(CTCPB_ERR_INVALID, "head_dim must be a multiple of 8");
-  if (g.head_dim > 256) return fail(CTCPB_ERR_UNSUPPORTED, "head_dim above 256");
-  if (g.max_len < 0 || g.window < 0)
-    return fail(CTCPB_ERR_INVALID, "max_len and window must be >= 0");
-  return check_table(g.rows, g.table_stride, g.table_width, g.page_size);
-}
-
-template <typename K>
-void launch_with_lds(K kernel, unsigned blocks, int threads, size_t lds, const AttnArgs& a,
-                     hipStream_t st) {
-  if (lds > 65536)   // more dynamic LDS than a kernel has unasked
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  kernel<<<blocks, threads, lds, st>>>(a);
-}
-
-template <typename T, int DP>
-void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const size_t state = (size_t)std::min(16, a.group) * (DP + 6) * sizeof(float);
-  if (p.waves == 1) {
-    attn_kernel<T, DP, 1><<<(unsigned)((p.items + 3) / 4), 256, 0, st>>>(a);
-  } else if (p.waves) {
-    constexpr int NW = DP <= 128 ? 8 : 4;
-    launch_with_lds(attn_kernel<T, DP, NW>, (unsigned)p.items, 64 * NW, NW * state, a, st);
-  } else {
-    launch_with_lds(attn_range_kernel<T, DP>,
-                    (unsigned)((int64_t)p.ranges * a.kv_heads * a.head_tiles), 64 * kRangeWaves,
-                    kRangeWaves * state, a, st);
-    if (p.ranges == 1) return;   // no row is split
-    constexpr int LANES = DP / 4, kGroups = 256 / LANES;
-    const int64_t heads = (int64_t)a.rows * a.heads;
-    // a workgroup to each head while that does not make more than a few to a CU
-    const int ways = heads <= 1024 ? kGroups : 1, per = kGroups / ways;
-    join_kernel<T, LANES><<<(unsigned)((heads + per - 1) / per), 256, 0, st>>>(a, ways);
-  }
-}
-
 template <typename T>
 void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   if (a.D <= 64)
-    launch_attention<T, 64>(a, p, st);
+    launch_tiles_of<Tile<T, 64>>(a, p, st);
   else if (a.D <= 128)
-    launch_attention<T, 128>(a, p, st);
+    launch_tiles_of<Tile<T, 128>>(a, p, st);
   else
-    launch_attention<T, 256>(a, p, st);
+    launch_tiles_of<Tile<T, 256>>(a, p, st);
 }
 
 // ------------------------------------------------------------------ loss --
@@ -235,103 +94,6 @@ constexpr size_t kPieceBytes = (size_t)1 << 30;
 // 1.1 and 1.2 (512 x 500 x 512 23.2 and 25.6, f16 23.3 and 27.9).
 constexpr int32_t kPairRows = 64;
 constexpr int64_t kPairWork = (int64_t)1 << 26;
-
-// How a product is cut up: tiles of BM (its m) x BN (its n), k in parts.
-struct TileShape {
-  int bm, bn, wn;   // wn: waves along n (dbias sums per token tile)
-};
-enum { kSmall = 0, kMiddle = 1, kLarge = 2 };
-constexpr TileShape kShapes[3] = {{64, 64, 2}, {128, 128, 2}, {256, 256, 4}};
-constexpr int kResident[3] = {4, 2, 1};   // workgroups that share a CU
-constexpr int kCUs = 256;
-// f32 sums in two levels, which leaves no registers for the large tiles.
-constexpr int largest(int es) { return es == 4 ? kMiddle : kLarge; }
-
-struct Cut {
-  int shape;
-  int32_t tiles_m, tiles_n, splits, part;
-};
-
-size_t up(size_t v, size_t n) { return (v + n - 1) / n * n; }
-
-// Estimated time (us) of a cut.  What decides is how well the tiles feed the
-// matrix units against how evenly the items fill the CUs.  Measured with bf16 and
-// f32 on products of 10^8 to 10^12 multiplications, for each shape: the time that
-// a k-tile of an item takes of its CU when CUs are full (`unit`; 256x256: 1430
-// TFLOP/s with bf16, 145 with f32), and when the item is alone on it (`alone`: its
-// fetches' latency), and a launch's beginning and end (`ends`).
-double cut_time(int es, const Cut& c, int64_t m, int64_t n) {
-  constexpr double unit[2][3] = {{0.26, 0.56, 1.5}, {0.56, 2.05, 0}};
-  constexpr double alone[2][3] = {{0.5, 0.73, 1.5}, {0.73, 2.28, 0}};
-  constexpr double ends[3] = {2.5, 5.0, 8.0};
-  const int type = es == 4;
-  const int64_t items = (int64_t)c.tiles_m * c.tiles_n * c.splits;
-  const int64_t slots = kCUs * kResident[c.shape], rest = items % slots;
-  const auto round = [&](int64_t shared) {   // one item each for `shared` workgroups of a CU
-    const double full = (double)shared * unit[type][c.shape], one = alone[type][c.shape];
-    return (full > one ? full : one) * (c.part * es / 128.0) + 2.5;
-  };
-  double time = ends[c.shape] + (double)(items / slots) * round(kResident[c.shape]);
-  if (rest) time += round((rest + kCUs - 1) / kCUs);
-  // planes are written, and read and added by a launch of its own
-  if (c.splits > 1) time += 4.5 + (double)c.splits * m * n * 8 / 3.3e6;
-  return time;
-}
-
-// The cut of an m x n x K product; only those with `split` may divide k (what
-// they leave are sums that can be added).
-Cut choose_cut(int es, int64_t m, int64_t n, int64_t K, bool split, double* time = nullptr) {
-  const int64_t bk = 128 / es;
-  Cut best{};
-  double least = 0;
-  for (int shape = kSmall; shape <= largest(es); ++shape) {
-    const int32_t tm = ceil_div(m, kShapes[shape].bm), tn = ceil_div(n, kShapes[shape].bn);
-    // parts of k fill a last round at most when there are many tiles
-    const int most = !split ? 1 : (int64_t)tm * tn >= 1024 ? 2 : 16;
-    for (int splits = 1; splits <= most; ++splits) {
-      Cut c{shape, tm, tn, splits, 0};
-      c.part = (int32_t)(ceil_div(ceil_div(K, splits), bk) * bk);
-      if (c.part < bk) c.part = (int32_t)bk;   // K = 0: one empty part
-      c.splits = K > 0 ? ceil_div(K, c.part) : 1;
-      const double t = cut_time(es, c, m, n);
-      if (best.part == 0 || t < least) {
-        best = c;
-        least = t;
-      }
-    }
-  }
-  if (time) *time = least;
-  return best;
-}
-
-// A product in up to two launches: rows [0, n) of its n by `main`, the others by
-// `rest`, which has no tiles where there are none.  Large tiles that fill whole
-// rounds of the CUs, and smaller ones for what would be a last, mostly empty round:
-// 20000 x 5000 x 1024 bf16 204 us in one launch, 193 in two.
-struct Product {
-  Cut main, rest;
-  int32_t n;
-  double time;
-};
-Product choose_product(int es, int64_t m, int64_t n, int64_t K, bool split, bool one = false) {
-  Product p{};
-  p.main = choose_cut(es, m, n, K, split, &p.time);
-  p.n = (int32_t)n;
-  for (int shape = kMiddle; shape <= largest(es) && !one; ++shape) {
-    const TileShape& t = kShapes[shape];
-    const int64_t tm = ceil_div(m, t.bm), tn = ceil_div(n, t.bn);
-    const int64_t slots = kCUs * kResident[shape], rounds = tm * tn / slots;
-    const int64_t columns = rounds * slots / tm;   // of whole rounds
-    if (columns == 0 || columns * t.bn >= n) continue;
-    const int32_t bk = 128 / es;
-    const Cut c{shape, (int32_t)tm, (int32_t)columns, 1, std::max(ceil_div(K, bk), 1) * bk};
-    double time;
-    const Cut rest = choose_cut(es, m, n - columns * t.bn, K, split, &time);
-    time += cut_time(es, c, m, columns * t.bn) + 2.0;
-    if (time < p.time) p = Product{c, rest, (int32_t)(columns * t.bn), time};
-  }
-  return p;
-}
 
 // Sums per token tile and wave that a logits product leaves for dbias.
 int32_t dbias_parts(const Cut& c) { return c.tiles_n * kShapes[c.shape].wn; }
@@ -500,36 +262,6 @@ Operand aligned_rows(const void* data, int64_t stride, int32_t rows, int32_t hid
                                                   reinterpret_cast<U*>(copy), rows, hidden,
                                                   p.padded);
   return Operand{copy, (int64_t)p.padded * (int)sizeof(T), rows, false};
-}
-
-template <typename T, int BM, int BN, int WM, int WN, bool AKC, bool BKC, typename Epilogue>
-void launch_tiles(const GemmArgs& g, const Epilogue& ep, int resident, hipStream_t st) {
-  const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits, slots = kCUs * resident;
-  gemm_kernel<T, BM, BN, WM, WN, AKC, BKC, Epilogue>
-      <<<(unsigned)(items < slots ? items : slots), 64 * WM * WN, 0, st>>>(g, ep);
-}
-
-// The product of a and b over K, cut as `c`; the epilogue's n begins at n0.
-template <typename T, bool AKC, bool BKC, typename Epilogue>
-void launch_cut(const Operand& a, const Operand& b, int32_t K, const Cut& c, int32_t n0,
-                const Epilogue& ep, hipStream_t st) {
-  const GemmArgs g{a, b, K, c.tiles_m, c.tiles_n, c.splits, c.part, n0};
-  if constexpr (sizeof(T) == 2)
-    if (c.shape == kLarge)
-      return launch_tiles<T, 256, 256, 2, 4, AKC, BKC>(g, ep, kResident[kLarge], st);
-  if (c.shape == kMiddle)
-    launch_tiles<T, 128, 128, 2, 2, AKC, BKC>(g, ep, kResident[kMiddle], st);
-  else
-    launch_tiles<T, 64, 64, 2, 2, AKC, BKC>(g, ep, kResident[kSmall], st);
-}
-
-// Rows [n0, n1) of an operand along n.
-template <typename T, bool KC>
-Operand rows_of(const Operand& b, int32_t n0, int32_t n1) {
-  Operand r = b;
-  r.data += KC ? n0 * b.ld : (int64_t)n0 * (int)sizeof(T);
-  r.rows = n1 - n0;
-  return r;
 }
 
 // Both launches of a product whose result is a matrix (OutEpilogue); parts of k are
@@ -758,59 +490,12 @@ int ctcpb_lm_attention(const ctcpb_lm_attention_args* args, void* workspace,
     if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
     const ctcpb_lm_attention_args& g = *args;
     if (int rc = check_attention(g)) return rc;
-    if (int rc = check_pages(g.num_pages, g.page_size)) return rc;
-    if (g.q_stride_r < 0 || g.q_stride_h < 0 || g.out_stride_r < 0 || g.out_stride_h < 0)
-      return fail(CTCPB_ERR_INVALID, "strides must be >= 0");
-    if (int rc = check_cache(g.k_cache)) return rc;
-    if (int rc = check_cache(g.v_cache)) return rc;
-    const int es = elem_size(g.dtype);
-    AttnArgs a{};
-    a.kc = view(g.k_cache, es);
-    a.vc = view(g.v_cache, es);
-    if (!wide_cache(a.kc) || !wide_cache(a.vc))
-      return fail(CTCPB_ERR_INVALID,
-                  "caches must be 16-byte aligned, with strides that are multiples of 16 bytes");
-    if (g.rows == 0) return ok();
-    if (!g.q || !g.out || !g.lengths || (!g.tables && g.table_width))
-      return fail(CTCPB_ERR_INVALID, kNull);
     const AttnPlan p = plan_attention(g);
-    if (p.bytes && (!workspace || !aligned(workspace, 16)))
-      return fail(CTCPB_ERR_INVALID, "workspace must be 16-byte aligned and not NULL");
-    if (workspace_bytes < p.bytes)
-      return fail(CTCPB_ERR_TOO_SMALL, "workspace smaller than ctcpb_lm_attention_workspace");
-    // steps of all rows are counted with 31 bits
-    if (p.items > INT_MAX || (int64_t)g.rows * g.q_heads > INT_MAX ||
-        (int64_t)g.rows * (p.max_len / 64 + 1) > INT_MAX)
-      return fail(CTCPB_ERR_UNSUPPORTED, "too many rows for one launch");
-    a.q = static_cast<const char*>(g.q);
-    a.out = static_cast<char*>(g.out);
-    a.lse = g.lse;
-    a.prefix = static_cast<int32_t*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.o_part);
-    a.tables = g.tables;
-    a.lengths = g.lengths;
-    a.q_r = g.q_stride_r;
-    a.q_h = g.q_stride_h;
-    a.out_r = g.out_stride_r;
-    a.out_h = g.out_stride_h;
-    a.table_stride = g.table_stride;
-    a.rows = g.rows;
-    a.heads = g.q_heads;
-    a.kv_heads = g.kv_heads;
-    a.group = g.q_heads / g.kv_heads;
-    a.head_tiles = p.head_tiles;
-    a.D = g.head_dim;
-    a.width = g.table_width;
-    a.page_log = log2_of(g.page_size);
-    a.num_pages = g.num_pages;
-    a.max_len = p.max_len;
-    a.window = g.window;
-    a.items = (int32_t)p.items;
-    a.ranges = p.ranges;
-    a.wide_q = aligned(g.q, 16) && g.q_stride_r * es % 16 == 0 && g.q_stride_h * es % 16 == 0;
-    a.wide_out =
-        aligned(g.out, 16) && g.out_stride_r * es % 16 == 0 && g.out_stride_h * es % 16 == 0;
-    a.scale = g.scale;
+    AttnArgs a{};
+    if (int rc = attention_args(g, p, elem_size(g.dtype), workspace, workspace_bytes,
+                                "workspace smaller than ctcpb_lm_attention_workspace", a))
+      return rc;
+    if (g.rows == 0) return ok();
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (g.dtype == CTCPB_LM_BF16)
       launch_attention<__bf16>(a, p, st);

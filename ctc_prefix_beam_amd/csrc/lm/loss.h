@@ -45,28 +45,6 @@ __device__ inline void add_bias(f32x4 (&acc)[TM][TN], const float* bias) {
   }
 }
 
-// Two neighbouring 16 x 16 tiles of a wave's sums as 16-bit values in rows of
-// memory: lane (g, c) has rows' places 4g .. 4g+3 of both in column c.  Swapping the
-// odd lane groups of the first with the even ones of the second gives every lane
-// eight neighbouring values, and a row's 32 values (64 bytes) to the same store:
-// half as many requests to the L2 as with eight bytes a lane.
-template <typename T>
-struct TilePair {
-  u32x4 bits;
-  static __device__ uint32_t two(float a, float b) {
-    typedef T T2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, T2{(T)a, (T)b});
-  }
-  __device__ TilePair(const f32x4& x, const f32x4& y) {
-    const auto a = __builtin_amdgcn_permlane16_swap(two(x[0], x[1]), two(y[0], y[1]), false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(two(x[2], x[3]), two(y[2], y[3]), false, false);
-    bits = u32x4{a[0], b[0], a[1], b[1]};
-  }
-  // where the lane's eight values begin, from the first tile's first row
-  static __device__ int at(int g) { return (g & 1) * 16 + (g >> 1) * 8; }
-  __device__ void store(T* to) const { *reinterpret_cast<u32x4*>(to) = bits; }
-};
-
 // The loss is bound by the matrix product, and then by the exponentials of its epilogue,
 // which the matrix units wait for (a quarter-rate instruction for each logit): 20000 x
 // 5000 x 1024 bf16 192 us a call (187 to 199 from card to card), 1070 TFLOP/s, of which 166
@@ -444,20 +422,6 @@ __global__ __launch_bounds__(1024) void scale_kernel(const float* grad, const in
   const float s = m > 0.0f ? fminf(fmaxf(top / m, 1e-30f), 1e30f) : 1.0f;
   scale[0] = s;
   scale[1] = 1.0f / s;
-}
-
-// Rows of `width` elements to rows of `padded` (zeros behind them): operands
-// whose rows are not 16-byte aligned.  A copy: 5000 rows of 509 bf16 7.4 us, in front of
-// 30 of the product at 4000 tokens.
-template <typename U>
-__global__ __launch_bounds__(256) void pad_kernel(const U* in, int64_t stride, U* out, int64_t rows,
-                                                  int32_t width, int32_t padded) {
-  const int64_t step = (int64_t)gridDim.x * 256, all = rows * padded;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
-    const int64_t r = i / padded;
-    const int32_t c = (int32_t)(i % padded);
-    out[i] = c < width ? in[r * stride + c] : (U)0;
-  }
 }
 
 }  // namespace ctcpb_lm

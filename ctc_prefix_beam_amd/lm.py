@@ -6,7 +6,10 @@ the pages and slots of a paged key/value cache from device-resident lengths
 (``cache_store``), the attention of one new token per request over the cache
 (``attention``), and token losses over a large vocabulary without keeping the
 logits, with their gradients (``token_loss``).  ``PagedCache`` holds the tensors
-of a cache.  Every step runs in the library's HIP kernels; PyTorch provides
+of a cache.  The same in 8 bits: a cache of int8 or float8_e4m3fn codes with a scale
+for each page and head (``cache_store8``, ``cache_load8``, ``attention8``), and linear
+layers of int8 weights with a scale for each channel (``quantize_rows``, ``linear8``);
+these carry no gradients.  Every step runs in the library's HIP kernels; PyTorch provides
 device memory and the current stream.  A call's `stream` (a torch stream, default
 the current one) is where it runs: its inputs have to be ready there, and its
 results are.  If the library is missing the calls raise; there is no CPU fallback.
@@ -29,9 +32,14 @@ LIB_PATH = os.path.join(_HERE, "libctcpb_lm.so")
 EXPORTS = ("ctcpb_lm_cache_plan", "ctcpb_lm_cache_release", "ctcpb_lm_cache_store",
            "ctcpb_lm_attention_workspace", "ctcpb_lm_attention", "ctcpb_lm_loss_workspace",
            "ctcpb_lm_loss", "ctcpb_lm_loss_grad_workspace", "ctcpb_lm_loss_grad",
-           "ctcpb_lm_last_error")
+           "ctcpb_lm_cache_store8", "ctcpb_lm_cache_load8", "ctcpb_lm_attention8_workspace",
+           "ctcpb_lm_attention8", "ctcpb_lm_quantize_rows", "ctcpb_lm_linear8_workspace",
+           "ctcpb_lm_linear8", "ctcpb_lm_last_error")
 NO_PAGE, NO_ENTRY, NO_SLOT = 1, 2, 4   # status bits of cache_plan
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_CODES_X = 3     # CTCPB_LM_CODES
+_READABLE = 1    # CTCPB_LM_READABLE
 _SPLIT_D = 256   # CTCPB_LM_SPLIT_D
 
 # The argument structures of include/ctcpb_lm.h, in order (native sizes and
@@ -42,6 +50,10 @@ _STORE = struct.Struct("3P4qP3qP3q6i")
 _ATTENTION = struct.Struct("5P5qP3qP3q10if4x")
 _LOSS = struct.Struct("6P2q4i")
 _GRAD = struct.Struct("9P2q4i")
+_CACHE8 = struct.Struct("3P4qP3qP3qP2qP2q7i4x")
+_ATTENTION8 = struct.Struct(_ATTENTION.format + "P2qP2qi4x")
+_QUANTIZE = struct.Struct("3P2q3i4x")
+_LINEAR8 = struct.Struct("6P3q6i")
 
 _lib = None
 
@@ -55,9 +67,10 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         p, sz = ctypes.c_void_p, ctypes.c_size_t
         args = ctypes.c_char_p   # the packed structure
-        for name in ("cache_plan", "cache_release", "cache_store"):
+        for name in ("cache_plan", "cache_release", "cache_store", "cache_store8", "cache_load8",
+                     "quantize_rows"):
             getattr(L, "ctcpb_lm_" + name).argtypes = [args, p]
-        for name in ("attention", "loss", "loss_grad"):
+        for name in ("attention", "loss", "loss_grad", "attention8", "linear8"):
             getattr(L, f"ctcpb_lm_{name}_workspace").argtypes = [args, ctypes.POINTER(sz)]
             getattr(L, "ctcpb_lm_" + name).argtypes = [args, p, sz, p]
         for name in EXPORTS[:-1]:   # all but the string getter
@@ -438,6 +451,211 @@ def token_loss(x, w, targets, bias=None, split_d: bool = False):
     return _TokenLoss.apply(x, w, targets, bias, split_d)
 
 
+def _codes(t, name):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be int8 or float8_e4m3fn, got {t.dtype}")
+    return code
+
+
+def _cache8(k_cache, v_cache, k_scale, v_scale, index, written):
+    """(code, (pages, page_size, heads, dim), the caches' and scales' addresses and strides)."""
+    _gpu(k_cache, "k_cache")
+    code = _codes(k_cache, "k_cache")
+    kc = _cache(k_cache, index, "k_cache", k_cache.dtype)
+    shape = k_cache.shape
+    vc = _cache(v_cache, index, "v_cache", k_cache.dtype, shape)
+    _like(k_scale, index, "k_scale", torch.float32, (shape[0], shape[2]))
+    _like(v_scale, index, "v_scale", torch.float32, (shape[0], shape[2]))
+    ks, vs = k_scale.stride(), v_scale.stride()
+    if written:
+        _apart(k_cache, kc[1:], "k_cache")
+        _apart(v_cache, vc[1:], "v_cache")
+        _apart(k_scale, ks, "k_scale")
+        _apart(v_scale, vs, "v_scale")
+    return code, shape, kc + vc, (k_scale.data_ptr(), *ks, v_scale.data_ptr(), *vs)
+
+
+def _no_gradient(name, *tensors):
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
+                                       for t in tensors):
+        raise ValueError(f"{name} carries no gradients: call it under torch.no_grad() or on "
+                         "detached tensors")
+
+
+def cache_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """``cache_store`` to caches of 8-bit codes (int8 or float8_e4m3fn, (pages, page_size,
+    kv_heads, head_dim)) with float32 scales (pages, kv_heads).  A page's scale is the least
+    power of two with which the largest code (127 or 448) reaches all that was written to it; it
+    starts with the token of slot 0, which begins the page anew, and later tokens can only raise
+    it: what the page holds is then rescaled.  Slots are distinct, and the tokens of a page follow
+    one another, as ``cache_plan`` lays them out.  Values are at most half a step off, rescaled
+    ones less than one; one that is not finite makes its page's scale NaN, until the page
+    begins anew."""
+    dev = _gpu(k, "k")
+    _no_gradient("cache_store8", k, v)
+    dt = _type(k, "k")
+    kt, kh, shape = _rows(k, "k")
+    _like(v, dev, "v", k.dtype, shape)
+    vt, vh, _ = _rows(v, "v")
+    T, H, D = shape
+    _i32(slots, dev, "slots", (T,))
+    code, (pages, page_size, heads, dim), caches, scales = _cache8(
+        k_cache, v_cache, k_scale, v_scale, dev, True)
+    if heads != H or dim != D:
+        raise ValueError(f"caches must have {H} heads of {D}, got {(heads, dim)}")
+    if T == 0:
+        return
+    _check(lib().ctcpb_lm_cache_store8(_pack(
+        _CACHE8, k.data_ptr(), v.data_ptr(), slots.data_ptr(), kt, kh, vt, vh, *caches, *scales, dt,
+        code, T, pages, page_size, H, D), _on(stream, dev)[0]))
+
+
+def cache_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloat16, stream=None):
+    """(k, v), both (tokens, kv_heads, head_dim) of `dtype`: what the slots (int32 (tokens,)) of
+    an 8-bit cache hold, code times scale; zeros for a token without a slot (-1)."""
+    dev = _gpu(slots, "slots")
+    T = slots.numel()
+    _i32(slots, dev, "slots", (T,))
+    dt = _TYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    code, (pages, page_size, H, D), caches, scales = _cache8(
+        k_cache, v_cache, k_scale, v_scale, dev, False)
+    raw, empty = _on(stream, dev)
+    both = empty((2, T, H, D), dtype=dtype, device=slots.device)
+    at = both.data_ptr()
+    _check(lib().ctcpb_lm_cache_load8(_pack(
+        _CACHE8, at, at + both.stride(0) * both.element_size(), slots.data_ptr(), H * D, D, H * D, D,
+        *caches, *scales, dt, code, T, pages, page_size, H, D), raw))
+    return both.unbind(0)
+
+
+def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: float | None = None,
+               window: int = 0, max_len: int = 0, out=None, stream=None):
+    """``attention`` over caches of 8-bit codes (int8 or float8_e4m3fn) with float32 scales
+    (pages, kv_heads) >= 0: keys and values are code times scale of their page and head.  q and
+    out are bfloat16, float16 or float32; head_dim is a multiple of 16."""
+    dev = _gpu(q, "q")
+    _no_gradient("attention8", q)
+    dt = _type(q, "q")
+    qr, qh, shape = _rows(q, "q")
+    R, Hq, D = shape
+    code, (pages, page_size, Hkv, Dk), caches, scales = _cache8(
+        k_cache, v_cache, k_scale, v_scale, dev, False)
+    if Dk != D:
+        raise ValueError(f"caches must have heads of {D}, got {Dk}")
+    stride, width = _tables(tables, dev, R)
+    _i32(lengths, dev, "lengths", (R,))
+    L = lib()
+    raw, empty = _on(stream, dev)
+    if out is None:
+        out = empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _like(out, dev, "out", q.dtype, shape)
+    outr, outh, _ = _rows(out, "out")
+    _apart(out, (outr, outh), "out")
+    lse = empty((R, Hq), dtype=torch.float32, device=q.device)
+    args = _pack(
+        _ATTENTION8, q.data_ptr(), tables.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), qr, qh, outr, outh, stride, *caches, dt, R, Hq, Hkv, D, pages, page_size,
+        width, max_len, window, 1.0 / math.sqrt(D) if scale is None else scale, *scales, code)
+    need = ctypes.c_size_t()
+    _check(L.ctcpb_lm_attention8_workspace(args, need))
+    size = need.value
+    # freed on return: the stream's later work may have it, after this call
+    ws = empty((size,), dtype=torch.uint8, device=q.device) if size else None
+    _check(L.ctcpb_lm_attention8(args, ws.data_ptr() if size else None, size, raw))
+    return out, lse
+
+
+def _matrix(t, name, columns=None):
+    """(row stride, rows, columns) of a matrix with unit stride over its columns."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must have two axes, the last one with unit stride")
+    rows, n = t.shape
+    if columns is not None and n != columns:
+        raise ValueError(f"{name} must have {columns} columns, got {n}")
+    # a single row's stride is of no account, and may be anything
+    return (t.stride(0) if rows > 1 else n), rows, n
+
+
+def quantize_rows(x, stream=None):
+    """(codes, scales) of the rows of x (rows, hidden): codes int8 (rows, hidden), x = codes *
+    scales[:, None] up to half a step, scales float32 (rows,) = max |x| / 127 of each row.  A row
+    with a value that is not finite has the scale NaN.  Rows of codes begin on 16 bytes, with
+    zeros behind them, as ``linear8`` reads them best."""
+    dev = _gpu(x, "x")
+    _no_gradient("quantize_rows", x)
+    dt = _type(x, "x")
+    sx, N, H = _matrix(x, "x")
+    if H == 0:
+        raise ValueError("x must have columns")
+    raw, empty = _on(stream, dev)
+    wide = -(-H // 16) * 16
+    codes = empty((N, wide), dtype=torch.int8, device=x.device)
+    scales = empty((N,), dtype=torch.float32, device=x.device)
+    _check(lib().ctcpb_lm_quantize_rows(_pack(
+        _QUANTIZE, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), sx, wide, dt, N, H), raw))
+    return (codes if wide == H else codes[:, :H]), scales
+
+
+def _readable(t, stride, rows, columns):
+    """Whether the last row of codes, too, can be read up to the next multiple of 16."""
+    wide = -(-columns // 16) * 16
+    return (wide == columns or
+            t.storage_offset() + (rows - 1) * stride + wide <= t.untyped_storage().nbytes())
+
+
+def linear8(x, w, w_scale, bias=None, x_scale=None, dtype=None, out=None, stream=None):
+    """x times 8-bit weights: (sum over hidden of codes) * x_scale * w_scale + bias, (rows,
+    features).  w int8 (features, hidden) with w_scale float32 (features,), as
+    ``quantize_rows`` makes them of a weight.  x (rows, hidden) is either bfloat16, float16
+    or float32, and quantised by row on the way (out then has its type), or int8 codes with their
+    x_scale float32 (rows,), and `dtype` (default bfloat16) is that of out.  bias: float32
+    (features,) or None.  Sums of codes are exact; hidden is at most 131071."""
+    dev = _gpu(x, "x")
+    _no_gradient("linear8", x, w_scale, bias, x_scale)
+    sx, N, H = _matrix(x, "x")
+    _like(w, dev, "w", torch.int8)
+    sw, M, _ = _matrix(w, "w", H)
+    _floats(w_scale, dev, "w_scale", M)
+    if bias is not None:
+        _floats(bias, dev, "bias", M)
+    flags = _READABLE if _readable(w, sw, M, H) else 0
+    if x.dtype is torch.int8:
+        if x_scale is None:
+            raise ValueError("x of int8 codes needs x_scale")
+        _floats(x_scale, dev, "x_scale", N)
+        xt, dtype = _CODES_X, dtype or torch.bfloat16
+    else:
+        if x_scale is not None:
+            raise ValueError("x_scale is for x of int8 codes")
+        xt = _type(x, "x")
+        if dtype not in (None, x.dtype):
+            raise ValueError(f"out has x's type, {x.dtype}; dtype is for x of int8 codes")
+        dtype = x.dtype
+    dt = _TYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    L = lib()
+    raw, empty = _on(stream, dev)
+    if out is None:
+        out = empty((N, M), dtype=dtype, device=x.device)
+    else:
+        _like(out, dev, "out", dtype, (N, M))
+    so, _, _ = _matrix(out, "out")
+    _apart(out, out.stride(), "out")
+    args = _pack(_LINEAR8, x.data_ptr(), _ptr(x_scale), w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
+                 out.data_ptr(), sx, sw, so, xt, dt, N, M, H, flags)
+    need = ctypes.c_size_t()
+    _check(L.ctcpb_lm_linear8_workspace(args, need))
+    size = need.value
+    ws = empty((size,), dtype=torch.uint8, device=x.device) if size else None
+    _check(L.ctcpb_lm_linear8(args, ws.data_ptr() if size else None, size, raw))
+    return out
+
+
 class PagedCache:
     """The paged key/value cache of a model's attention layers and its page
     allocator, for `rows` requests of at most `max_len` tokens each, rounded up to
@@ -451,6 +669,10 @@ class PagedCache:
     every request at max_len) may be smaller: a request the pool cannot serve is
     flagged in the plan's status and holds only the tokens that have a slot.  Use
     one PagedCache per stream, or order its calls.
+
+    With `dtype` int8 or float8_e4m3fn the cache holds codes, and ``k_scale`` and ``v_scale``
+    (layers, num_pages, kv_heads) their scales: ``store`` quantises (``cache_store8``), ``attend``
+    is ``attention8``, and ``load(slots, layer)`` reads tokens back in 16 or 32 bits.
 
     An append goes on to the plan's new lengths, so a captured one repeats the same
     step when it is replayed.  To capture a step that moves on, call ``cache_plan``
@@ -466,9 +688,19 @@ class PagedCache:
         width = -(-max_len // page_size)
         num_pages = num_pages or max(1, rows * width)
         self.page_size, self.max_len = page_size, width * page_size
-        self.k = torch.empty((layers, num_pages, page_size, kv_heads, head_dim), dtype=dtype,
-                             device=device)
-        self.v = torch.empty_like(self.k)
+        self.k_scale = self.v_scale = None
+        if dtype in _CODES:
+            # head by head: rows are short, and a page's of one head then lie together, as do
+            # its two scales
+            both = [torch.empty((layers, num_pages, kv_heads, page_size, head_dim), dtype=dtype,
+                                device=device).transpose(2, 3) for _ in range(2)]
+            self.k, self.v = both
+            scales = torch.zeros((layers, num_pages, kv_heads, 2), device=device)
+            self.k_scale, self.v_scale = scales.unbind(-1)
+        else:
+            self.k = torch.empty((layers, num_pages, page_size, kv_heads, head_dim), dtype=dtype,
+                                 device=device)
+            self.v = torch.empty_like(self.k)
         self.tables = torch.full((rows, width), -1, dtype=torch.int32, device=device)
         self.pool = torch.arange(num_pages, dtype=torch.int32, device=device)
         self.lengths = torch.zeros(rows, dtype=torch.int32, device=device)
@@ -490,14 +722,36 @@ class PagedCache:
         self.lengths, self.taken = plan.lengths, plan.taken
         return plan
 
+    def _codes(self, layer):
+        """A layer's codes and scales."""
+        return self.k[layer], self.v[layer], self.k_scale[layer], self.v_scale[layer]
+
     def store(self, k, v, slots, layer: int = 0, stream=None):
-        cache_store(k, v, slots, self.k[layer], self.v[layer], stream)
-        self._keep(stream, self.k, self.v)
+        if self.k_scale is None:
+            cache_store(k, v, slots, self.k[layer], self.v[layer], stream)
+            self._keep(stream, self.k, self.v)
+        else:
+            cache_store8(k, v, slots, *self._codes(layer), stream)
+            self._keep(stream, self.k, self.v, self.k_scale, self.v_scale)
+
+    def load(self, slots, layer: int = 0, dtype=torch.bfloat16, stream=None):
+        """(k, v) of the tokens in `slots`, of an 8-bit cache."""
+        if self.k_scale is None:
+            raise ValueError("load is for caches of int8 or float8_e4m3fn")
+        got = cache_load8(slots, *self._codes(layer), dtype, stream)
+        self._keep(stream, self.k, self.v, self.k_scale, self.v_scale)
+        return got
 
     def attend(self, q, layer: int = 0, scale=None, window: int = 0, max_len: int = 0, stream=None):
-        got = attention(q, self.k[layer], self.v[layer], self.tables, self.lengths, scale, window,
-                        max_len, stream=stream)
-        self._keep(stream, self.k, self.v, self.tables, self.lengths)
+        if self.k_scale is None:
+            got = attention(q, self.k[layer], self.v[layer], self.tables, self.lengths, scale,
+                            window, max_len, stream=stream)
+            self._keep(stream, self.k, self.v, self.tables, self.lengths)
+        else:
+            got = attention8(q, *self._codes(layer), self.tables, self.lengths, scale, window,
+                             max_len, stream=stream)
+            self._keep(stream, self.k, self.v, self.k_scale, self.v_scale, self.tables,
+                       self.lengths)
         return got
 
     def release(self, finished, stream=None):

@@ -8,6 +8,11 @@
  *   attention                    one new token per request over the cache
  *   loss / loss_grad             token losses over a large vocabulary without
  *                                keeping the logits, and their gradients
+ *   cache_store8 / cache_load8   new tokens' keys and values to a cache of 8
+ *                                bits a value, and back
+ *   attention8                   one new token per request over that cache
+ *   quantize_rows, linear8       rows as 8-bit codes with a scale each, and the
+ *                                products of such rows
  *
  * Conventions are those of ctcpb.h: device pointers are the caller's, the
  * library allocates no device memory and keeps no state between calls, every
@@ -33,6 +38,10 @@ extern "C" {
 
 /* Element types of the tensors documented "typed". */
 enum { CTCPB_LM_BF16 = 0, CTCPB_LM_F16 = 1, CTCPB_LM_F32 = 2 };
+
+/* Codes of 8 bits: whole numbers (of a store: -127..127), or floats of 4 bits of exponent
+ * and 3 of fraction without infinities, up to 448.  A code stands for itself times a scale. */
+enum { CTCPB_LM_INT8 = 0, CTCPB_LM_E4M3 = 1 };
 
 /* Added to the dtype of ctcpb_lm_loss_grad and its size query: d as the sum of two
  * values of a 16-bit type, see there.  Of no account with CTCPB_LM_F32. */
@@ -157,6 +166,60 @@ int ctcpb_lm_attention_workspace(const ctcpb_lm_attention_args* args, size_t* ou
 int ctcpb_lm_attention(const ctcpb_lm_attention_args* args, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* The scales of a paged cache of 8-bit codes: that of (page, head) at
+ * data[page*stride_page + head*stride_head]. */
+typedef struct {
+  float* data;           /* device */
+  int64_t stride_page, stride_head;
+} ctcpb_lm_scales;
+
+/* Keys and values to their slots of a cache of 8-bit codes, and back.  Of what a
+ * store writes to page p for a head:
+ *   scale[p] = max(old, the least power of two u with |x| <= top u for all of
+ *              them), top the largest code, 127 or 448
+ *   code = x / scale, rounded to the nearest code (ties to the even one)
+ * old is 0 where a token goes to the page's slot 0, which begins the page anew (its
+ * other slots then hold nothing), else the page's scale, which has to have been
+ * set.  Codes of a page whose scale grows are multiplied by old / new and rounded
+ * again, which with scales from here leaves them less than one step off their value (e4m3: half a step
+ * as ever, and less than one of the smallest codes').  A value that is not finite
+ * makes the scale NaN, which the page keeps until it begins anew.
+ *   k, v     device, typed: element (t, head, d) at t*stride_t + head*stride_h + d;
+ *            read by the store, written by the load (code * scale, rounded)
+ *   slots    device int32 [tokens]; tokens whose slot is outside
+ *            [0, num_pages*page_size) are left out by the store, zeros by the
+ *            load.  For the store they are distinct, and tokens of one page
+ *            follow one another, as ctcpb_lm_cache_plan lays them out (in any order within
+ *            the page, and with tokens without a slot between them): a page that comes
+ *            twice, with another one between, gets either scale and mixed codes.
+ *   code     CTCPB_LM_INT8 or CTCPB_LM_E4M3; strides of the caches in codes
+ * Wide accesses are used where pointers and strides allow, else single elements. */
+typedef struct {
+  void *k, *v;
+  const int32_t* slots;
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  ctcpb_lm_cache k_cache, v_cache;
+  ctcpb_lm_scales k_scale, v_scale;
+  int32_t dtype, code, tokens, num_pages, page_size, kv_heads, head_dim;
+} ctcpb_lm_cache8_args;
+int ctcpb_lm_cache_store8(const ctcpb_lm_cache8_args* args, void* stream);
+int ctcpb_lm_cache_load8(const ctcpb_lm_cache8_args* args, void* stream);
+
+/* ctcpb_lm_attention over a cache of 8-bit codes, whose keys and values are code *
+ * scale: `base` as there (its dtype that of q and out, its caches' strides in codes), but
+ * head_dim is a multiple of 16.  Scales are any finite numbers >= 0.  Codes and scales of slots
+ * past a row's length, or before its window in another page, are never used, whatever
+ * they hold.  Nothing is rounded on the way to fewer than 22 bits. */
+typedef struct {
+  ctcpb_lm_attention_args base;
+  ctcpb_lm_scales k_scale, v_scale;
+  int32_t code;
+} ctcpb_lm_attention8_args;
+/* Reads no pointer of `args`, only sizes. */
+int ctcpb_lm_attention8_workspace(const ctcpb_lm_attention8_args* args, size_t* out_bytes);
+int ctcpb_lm_attention8(const ctcpb_lm_attention8_args* args, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* Token losses of an output layer, the vocabulary taken in pieces:
  *   logit[n, v] = x[n] . w[v] + bias[v]     lse[n] = log sum_v exp(logit[n, v])
  *   loss[n] = lse[n] - logit[n, targets[n]]
@@ -218,6 +281,56 @@ typedef struct {
 int ctcpb_lm_loss_grad_workspace(const ctcpb_lm_grad_args* args, size_t* out_bytes);
 int ctcpb_lm_loss_grad(const ctcpb_lm_grad_args* args, void* workspace, size_t workspace_bytes,
                        void* stream);
+
+/* Rows as 8-bit whole numbers with a scale each:
+ *   scales[n] = max_k |x[n, k]| / 127 as a float32 number, or NaN where a value of the row is
+ *   not finite;  codes[n, k] = x[n, k] / scales[n], the exact quotient rounded to the nearest
+ *   whole number (ties to the even one; 0 where the scale is 0 or NaN)
+ *   x        device, typed, row stride stride_x >= 0
+ *   codes    device, row stride stride_codes >= hidden; of what a row has behind `hidden`, up to
+ *            the next multiple of 16 is zeroed
+ *   scales   device float32 [rows] */
+typedef struct {
+  const void* x;
+  int8_t* codes;
+  float* scales;
+  int64_t stride_x, stride_codes;
+  int32_t dtype, rows, hidden;
+} ctcpb_lm_quantize_args;
+int ctcpb_lm_quantize_rows(const ctcpb_lm_quantize_args* args, void* stream);
+
+/* x_dtype of ctcpb_lm_linear8 where x holds codes. */
+enum { CTCPB_LM_CODES = 3 };
+/* Flag of ctcpb_lm_linear8: the rows of w can be read up to the next multiple of 16 codes, the
+ * last row's too (as ctcpb_lm_quantize_rows leaves them in rows of such a stride), whatever is
+ * there.  Without it, rows whose length is no such multiple are copied to the workspace. */
+enum { CTCPB_LM_READABLE = 1 };
+
+/* A linear layer of 8-bit operands:
+ *   out[n, m] = (sum_k xc[n, k] w[m, k]) * xs[n] * w_scale[m] + bias[m]
+ * with codes xc and scales xs of x as ctcpb_lm_quantize_rows makes them, or as given.  The sum
+ * is exact, the rest float32 with one rounding to out's type.
+ *   x        device, x_dtype, row stride stride_x >= 0;  x_scale: device float32 [rows], with
+ *            CTCPB_LM_CODES only
+ *   w        device int8 [features][hidden], row stride stride_w >= 0;  w_scale: device
+ *            float32 [features];  bias: device float32 [features] or NULL
+ *   out      device, typed (dtype), row stride stride_out >= features
+ *   hidden   at most 131071
+ *   workspace  device, 256-byte aligned, contents on entry do not matter; calls that share it
+ *            must not overlap.  Its size depends on the addresses and strides of x and w too;
+ *            the size query does not read them. */
+typedef struct {
+  const void* x;
+  const float* x_scale;
+  const int8_t* w;
+  const float *w_scale, *bias;
+  void* out;
+  int64_t stride_x, stride_w, stride_out;
+  int32_t x_dtype, dtype, rows, features, hidden, flags;
+} ctcpb_lm_linear8_args;
+int ctcpb_lm_linear8_workspace(const ctcpb_lm_linear8_args* args, size_t* out_bytes);
+int ctcpb_lm_linear8(const ctcpb_lm_linear8_args* args, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /* Human-readable description of the last error on this thread ("" if none). */
 const char* ctcpb_lm_last_error(void);

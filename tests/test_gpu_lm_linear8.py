@@ -1,0 +1,233 @@
+"""Rows as 8-bit codes, and the products of such rows, against 64 bits."""
+import math
+
+import pytest
+import torch
+
+import lm_ref8
+from ctc_prefix_beam_amd import lm
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def rows(N, H, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((N, H), generator=g) * torch.exp2(torch.randint(-5, 6, (N, 1), generator=g))
+    return x.to(dtype).cuda()
+
+
+def weight(M, H, seed=1):
+    """Codes of every kind, -128 too, in rows that end where they end, and scales."""
+    g = torch.Generator().manual_seed(seed)
+    w = torch.randint(-128, 128, (M, H), generator=g, dtype=torch.int32).to(torch.int8)
+    return w.cuda(), (torch.rand(M, generator=g) + 0.5).cuda() / 4000
+
+
+def check(x, w, ws, bias=None, **kw):
+    out = lm.linear8(x, w, ws, bias, **kw)
+    codes, scales = lm_ref8.quantize(x)
+    want, tol = lm_ref8.linear(codes, scales, w, ws, bias, x.dtype)
+    assert out.dtype == x.dtype
+    assert ((out.cpu().double() - want).abs() <= tol).all(), float(
+        ((out.cpu().double() - want).abs() / tol).max())
+    return out
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [1, 3, 16, 100, 387, 512, 2048, 4096, 5003, 17000, 40008])
+def test_codes_and_scales(dtype, H):
+    for N in (1, 70, 1100) if H < 6000 else (3,):
+        x = rows(N, H, dtype, H)
+        codes, scales = lm.quantize_rows(x)
+        want, s = lm_ref8.quantize(x)
+        assert torch.equal(scales.cpu(), s)
+        assert torch.equal(codes.cpu().double(), want)
+        assert codes.stride(0) % 16 == 0
+        whole = codes.as_strided((N, codes.stride(0)), (codes.stride(0), 1))
+        assert (whole[:, H:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quotients_next_to_a_half(dtype):
+    """Every value is n + 1/2 steps, or a neighbour of that in the type: halves go to the even
+    code, the others to their own side."""
+    g = torch.Generator().manual_seed(0)
+    N, H = 200, 256
+    most = (torch.rand((N, 1), generator=g) + 0.5).to(dtype)
+    step = most.float() / 127
+    n = torch.arange(H - 1).float() % 127 + 0.5
+    x = (n * step).to(dtype)
+    off = torch.randint(-1, 2, x.shape, generator=g)
+    up, down = torch.nextafter(x, x * 2), torch.nextafter(x, x * 0)
+    x = torch.where(off > 0, up, torch.where(off < 0, down, x)).clamp(max=most)
+    x = torch.cat((x, most), 1)
+    x = torch.cat((x, -x, x), 0)
+    x[2 * N:, :-1] = (n / 127).to(dtype)       # a scale of 1/127 of one
+    x[2 * N:, -1] = 1
+    extra = torch.cat((torch.arange(-127, 127).float() + 0.5, torch.tensor([127.0, 0.0])))
+    x = torch.cat((x, extra.to(dtype)[None], extra.to(dtype)[None] * 2.0 ** -3)).cuda()
+    codes, scales = lm.quantize_rows(x)
+    want, s = lm_ref8.quantize(x)
+    assert torch.equal(scales.cpu(), s) and torch.equal(codes.cpu().double(), want)
+    assert want[-1, :4].tolist() == [-126, -126, -124, -124]   # exact halves: a scale of 1/8
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_at_the_ends_of_the_type(dtype):
+    info = torch.finfo(dtype)
+    x = torch.zeros((9, 24), dtype=dtype)
+    x[1, 3], x[1, 4] = info.max, -info.max
+    x[2] = torch.arange(24).to(dtype) * info.smallest_normal
+    x[3] = torch.arange(24).to(dtype) * (info.smallest_normal * 2.0 ** -6)
+    x[4, 5], x[5, 6], x[6, 7] = math.nan, math.inf, -math.inf
+    x[4, 0] = 3.0
+    x[7] = -0.0
+    x[8] = torch.arange(24).to(dtype) - 12
+    codes, scales = lm.quantize_rows(x.cuda())
+    want, s = lm_ref8.quantize(x)
+    assert torch.equal(scales.cpu().nan_to_num(-1), s.nan_to_num(-1))
+    assert torch.equal(codes.cpu().double(), want)
+    w, ws = weight(33, 24)
+    out = lm.linear8(x.cuda(), w, ws)
+    bad = torch.isnan(s)
+    assert bad.tolist() == [False] * 4 + [True] * 3 + [False] * 2
+    assert torch.isnan(out.cpu()[bad]).all()
+    if dtype != torch.float16:
+        assert torch.isfinite(out.cpu()[~bad]).all()
+    assert (out[0] == 0).all() and (out[7] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,M,H", [
+    (1, 1, 1), (1, 29, 64), (1, 5000, 512), (3, 319, 1377), (5, 7, 16), (16, 64, 128), (17, 65, 130),
+    (32, 5000, 512), (33, 1000, 2048), (64, 128, 8192), (65, 35, 64), (100, 256, 4096),
+    (255, 257, 259), (256, 512, 512), (875, 1531, 387), (1000, 100, 1000), (2000, 2000, 600)])
+def test_sizes(dtype, N, M, H):
+    x = rows(N, H, dtype, N)
+    w, ws = weight(M, H)
+    g = torch.Generator().manual_seed(2)
+    bias = torch.randn(M, generator=g).cuda()
+    check(x, w, ws)
+    check(x, w, ws, bias)
+
+
+@pytest.mark.parametrize("N,M,H", [(1, 40, 131071), (3, 70, 100000), (300, 40, 65536)])
+def test_long_sums_stay_whole(N, M, H):
+    """Sums of up to 2^31 - 128^2, exact in 32 bits."""
+    x = torch.full((N, H), 2.5, device="cuda")
+    w = torch.full((M, H), -128, dtype=torch.int8, device="cuda")
+    one = torch.ones(M, device="cuda")
+    out = lm.linear8(x, w, one)
+    want = -128.0 * 127 * H * float(torch.tensor(2.5) / 127)
+    assert ((out.double() - want).abs() <= 2.0 ** -22 * abs(want)).all()
+    xs = torch.ones(N, device="cuda")
+    out = lm.linear8(w[:1].expand(N, H), w, one, x_scale=xs, dtype=torch.float32)
+    assert (out.double() == 128.0 * 128 * H).all() or H % 2   # (131071: 2^31 - 2^14, 17 bits)
+    assert ((out.double() - 128.0 * 128 * H).abs() <= 2.0 ** -23 * 128.0 * 128 * H).all()
+
+
+def test_large_tiles_against_products_in_pieces():
+    """Sizes that fill the card with the largest tiles, with ends that do not, against exact
+    float64 products on the GPU."""
+    for N, M, H in ((8192, 8192, 512), (20000, 1000, 1024), (4097, 5003, 640)):
+        x = rows(N, H, torch.bfloat16)
+        w, ws = weight(M, H)
+        out = lm.linear8(x, w, ws)
+        codes, s = lm.quantize_rows(x)
+        for a in range(0, N, 4096):
+            y = torch.mm(codes[a:a + 4096].double(), w.double().t())
+            y *= s[a:a + 4096].double()[:, None] * ws.double()
+            assert ((out[a:a + 4096].double() - y).abs() <= (2.0 ** -8 + 2.0 ** -21) * y.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_codes_as_input(dtype):
+    x = rows(70, 130, torch.float32)
+    codes, s = lm.quantize_rows(x)
+    w, ws = weight(45, 130)
+    bias = torch.randn(45).cuda()
+    out = lm.linear8(codes, w, ws, bias, x_scale=s, dtype=dtype)
+    assert out.dtype == dtype
+    assert torch.equal(out, lm.linear8(codes.contiguous(), w, ws, bias, x_scale=s, dtype=dtype))
+    assert torch.equal(out.float() if dtype == torch.float32 else out,
+                       lm.linear8(x, w, ws, bias).to(dtype))
+    assert lm.linear8(codes, w, ws, x_scale=s).dtype == torch.bfloat16
+    # parts of wider rows, whose other codes have no part in the sums
+    wide = [torch.full((n, 160), 77, dtype=torch.int8, device="cuda") for n in (70, 45)]
+    for t, c in zip(wide, (codes, w)):
+        t[:, :130] = c
+    got = lm.linear8(wide[0][:, :130], wide[1][:, :130], ws, bias, x_scale=s, dtype=dtype)
+    assert torch.equal(got, out)
+    assert torch.equal(lm.linear8(x, wide[1][:, :130], ws, bias), lm.linear8(x, w, ws, bias))
+
+
+def test_strides():
+    """Rows of x, w, out that lie apart, begin anywhere and end at the end of their memory."""
+    g = torch.Generator().manual_seed(0)
+    big = torch.randn((40, 333), generator=g).cuda()
+    w, ws = weight(50, 300)
+    wide = torch.zeros((50, 320), dtype=torch.int8, device="cuda")
+    for at in (0, 1, 16, 20):
+        x = big[::2, at + 1:at + 301]
+        part = wide[:, at:at + 300]
+        part.copy_(w)
+        space = torch.full((20, 64), 9.0, device="cuda")
+        out = lm.linear8(x, part, ws, out=space[:, 3:53])
+        assert torch.equal(out, check(x.contiguous(), w, ws))
+        assert (space[:, :3] == 9).all() and (space[:, 53:] == 9).all()
+        half = torch.full((20, 56), 9.0, dtype=torch.float16, device="cuda")
+        got = lm.linear8(x.half(), part, ws, out=half[:, :50])
+        assert torch.equal(got, check(x.half(), w, ws)) and (half[:, 50:] == 9).all()
+    one = big[:1, :300].expand(5, 300)   # read, rows may share their memory
+    assert torch.equal(lm.linear8(one, w, ws)[4:], check(one.contiguous(), w, ws)[:1])
+
+
+def test_graphs_streams_and_no_rows():
+    x = rows(300, 2048, torch.bfloat16)
+    w, ws = weight(200, 2048)
+    want = check(x, w, ws)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = lm.linear8(x, w, ws, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = lm.linear8(x, w, ws)
+        codes, s = lm.quantize_rows(x)
+    for i in range(4):
+        got.zero_()
+        codes.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        again, t = lm.quantize_rows(x)
+        assert torch.equal(again, codes) and torch.equal(s, t)
+    assert lm.linear8(x[:0], w, ws).shape == (0, 200)
+    codes, s = lm.quantize_rows(x[:0])
+    assert codes.shape == (0, 2048) and s.shape == (0,)
+
+
+def test_refusals():
+    x = rows(4, 32, torch.float16)
+    w, ws = weight(8, 32)
+    codes, s = lm.quantize_rows(x)
+    good = dict(x=x, w=w, w_scale=ws)
+    for kw in (dict(x=x.double()), dict(x=x[:, :31]), dict(x=x[0]), dict(x=x.t()), dict(w=w.short()),
+               dict(w=w.t()), dict(w_scale=ws[:7]), dict(w_scale=ws.half()), dict(bias=ws.half()),
+               dict(bias=ws[:3]), dict(x=codes), dict(x_scale=s), dict(x=codes, x_scale=s[:2]),
+               dict(dtype=torch.float32), dict(x=codes, x_scale=s, dtype=torch.int8),
+               dict(out=torch.zeros((4, 8), device="cuda")),
+               dict(out=torch.zeros((1, 8), dtype=x.dtype, device="cuda").expand(4, 8)),
+               dict(out=torch.zeros((8, 4), dtype=x.dtype, device="cuda").t()),
+               dict(x=x.clone().requires_grad_()), dict(w=w[:, :0], x=x[:, :0]), dict(w=w.cpu()),
+               dict(w=w[:0], w_scale=ws[:0])):
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            lm.linear8(**{**good, **kw})
+    with pytest.raises(RuntimeError, match="131071"):
+        lm.linear8(torch.zeros((1, 131072), device="cuda"),
+                   torch.zeros((1, 131072), dtype=torch.int8, device="cuda"), ws[:1])
+    for bad in (x.double(), x[0], x[:, :0], x.t(), codes, x.clone().requires_grad_()):
+        with pytest.raises(ValueError):
+            lm.quantize_rows(bad)
