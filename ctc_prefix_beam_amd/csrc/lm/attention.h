@@ -161,6 +161,7 @@ struct Tile {
   static constexpr int kAloneWaves = DP == 64 ? 4 : 1;   // on a SIMD: a wave to an item
   static constexpr int kRangeOnSimd = DP == 64 ? 4 : DP == 128 ? 3 : 1;   // and ranges
   static constexpr int kTokens = 32;
+  static constexpr bool kWalks = false;   // has a loop over tiles of its own
   static constexpr int kK = DP / 32;            // k-steps of the score product
   static constexpr int kV = DP >= 128 ? 8 : 4;  // values a lane loads at once
   static constexpr int kH = DP / 16 / kV;       // such loads per token
@@ -203,7 +204,7 @@ struct Tile {
     return b * 16 * kV + (((threadIdx.x & 63) >> 4) * 4 + r) * kV;
   }
 
-  static __device__ Spot spot(const AttnArgs& a, const int32_t* table, int32_t t0) {
+  static __device__ Spot spot(const AttnArgs& a, const int32_t* table, int32_t t0, int) {
     return Spot{t0, group_page(a, table, t0 + (threadIdx.x & 7) * 4)};
   }
 
@@ -328,6 +329,7 @@ struct Tile<float, DP> {
   static constexpr int kAloneWaves = DP == 64 ? 4 : 1;
   static constexpr int kRangeOnSimd = DP == 64 ? 4 : 1;
   static constexpr int kTokens = 16;
+  static constexpr bool kWalks = false;
   static constexpr int kK = DP / 16;
   static constexpr int kH = DP / 64;
   static constexpr int kAcc = DP / 16;
@@ -363,7 +365,7 @@ struct Tile<float, DP> {
     return b * 64 + (((threadIdx.x & 63) >> 4) * 4 + r) * 4;
   }
 
-  static __device__ Spot spot(const AttnArgs& a, const int32_t* table, int32_t t0) {
+  static __device__ Spot spot(const AttnArgs& a, const int32_t* table, int32_t t0, int) {
     return Spot{t0, group_page(a, table, t0 + (threadIdx.x & 3) * 4)};
   }
 
@@ -505,21 +507,25 @@ struct Attend {
   __device__ void tiles(const Args& a, const int32_t* table, int row, const Range& rg, Spot at,
                         Spot then, int step, int32_t end) {
     if (at.t0 >= end) return;
-    tile.load_keys(a, kbase, at);
-    const int c = threadIdx.x & 15;
-    tile.load_query(a, reinterpret_cast<const T*>(a.q) + row * a.q_r +
-                           (int64_t)(head0 + (live() ? c : 0)) * a.q_h, live());
-    tile.load_values(a, vbase, at);
-    for (;;) {
-      f32x4 sc[2];
-      tile.scores(sc);
-      const bool more = then.t0 < end;
-      if (more) tile.load_keys(a, kbase, then);
-      tile.add(a, at.t0, rg, sc, s);
-      if (!more) break;
-      tile.load_values(a, vbase, then);
-      at = then;
-      then = TL::spot(a, table, at.t0 + step);
+    const T* q = reinterpret_cast<const T*>(a.q) + row * a.q_r +
+                 (int64_t)(head0 + (live() ? threadIdx.x & 15 : 0)) * a.q_h;
+    if constexpr (TL::kWalks) {
+      tile.walk(a, table, q, live(), rg, at, step, end, s);
+    } else {
+      tile.load_keys(a, kbase, at);
+      tile.load_query(a, q, live());
+      tile.load_values(a, vbase, at);
+      for (;;) {
+        f32x4 sc[2];
+        tile.scores(sc);
+        const bool more = then.t0 < end;
+        if (more) tile.load_keys(a, kbase, then);
+        tile.add(a, at.t0, rg, sc, s);
+        if (!more) break;
+        tile.load_values(a, vbase, then);
+        at = then;
+        then = TL::spot(a, table, at.t0 + step, step);
+      }
     }
   }
 
@@ -608,13 +614,13 @@ void attn_kernel(typename TL::Args a) {
   const int32_t mine = (NW == 1 ? 0 : wave) * TL::kTokens;
   Spot first{mine, 0}, second{mine + kStep, 0};
   if (a.window == 0 && a.width > 0) {   // the first pages are asked for along with the length
-    first = TL::spot(a, table, mine);
-    second = TL::spot(a, table, mine + kStep);
+    first = TL::spot(a, table, mine, kStep);
+    second = TL::spot(a, table, mine + kStep, kStep);
   }
   const Range rg = attn_range_uniform(a, row, TL::kTokens);
   if (a.window && a.width > 0) {
-    first = TL::spot(a, table, rg.base + mine);
-    second = TL::spot(a, table, rg.base + mine + kStep);
+    first = TL::spot(a, table, rg.base + mine, kStep);
+    second = TL::spot(a, table, rg.base + mine + kStep, kStep);
   }
   at.tiles(a, table, row, rg, first, second, kStep, rg.hi);
   if constexpr (NW > 1) {
@@ -725,8 +731,8 @@ void attn_range_kernel(typename TL::Args a) {
     const int32_t end = min(rg.hi, rg.base + to * kStep);
     Spot one{t0, 0}, two{t0 + kStep, 0};
     if (a.width > 0) {
-      one = TL::spot(a, table, t0);
-      two = TL::spot(a, table, t0 + kStep);
+      one = TL::spot(a, table, t0, kStep);
+      two = TL::spot(a, table, t0 + kStep, kStep);
     }
     s.s.reset();
     s.tiles(a, table, row, rg, one, two, kStep, end);

@@ -21,6 +21,8 @@
 // d = 64 k + 16 g (which two k-steps of the product take in that order, q alike) and, of the
 // values of tokens 8g .. 8g+7, DP / 16 bytes at d = c DP / 16.
 #pragma once
+#include <type_traits>
+
 #include "attention.h"
 #include "cache8.h"
 
@@ -28,6 +30,8 @@ namespace ctcpb_lm {
 
 struct Attn8Args : AttnArgs {
   ScaleView ks, vs;
+  uint32_t k_page, v_page, k_token, v_token;   // strides of the caches in bytes
+  uint32_t ks_page, vs_page;                   // and of the scales in bytes
 };
 
 // The power of two that takes a magnitude to 2^14 .. 2^15, between 2^-113 and 2^126.
@@ -58,9 +62,10 @@ struct Tile8 {
   typedef T Type;
   typedef Attn8Args Args;
   static constexpr int kDP = DP;
-  static constexpr int kAloneWaves = DP <= 128 ? 4 : 2;
-  static constexpr int kRangeOnSimd = DP <= 128 ? 4 : 2;
+  static constexpr int kAloneWaves = DP == 64 ? 4 : DP == 128 ? 3 : 2;
+  static constexpr int kRangeOnSimd = DP == 64 ? 4 : DP == 128 ? 3 : 2;
   static constexpr int kTokens = 32;
+  static constexpr bool kWalks = true;
   static constexpr int kK = DP / 64;       // 16-byte loads of a key's row for a lane
   static constexpr int kV = DP / 16;       // bytes of a value's row
   static constexpr int kAcc = DP / 16;
@@ -73,14 +78,96 @@ struct Tile8 {
 
   f16x8 q[kQ][2 * kK];
   u32x4 kf[2][kK];
-  uint32_t vr[8][kV / 4];
-  const float *kscales, *vscales;
-  float kscale, vscale;   // of the lane's group of four tokens
+  typedef uint32_t Row __attribute__((ext_vector_type(kV / 4 > 1 ? kV / 4 : 2)));
+  typedef typename std::conditional<kV == 4, uint32_t, Row>::type ValueRow;
+  ValueRow vr[8];
+  __device__ uint32_t word(int i, int x) const {
+    if constexpr (kV == 4)
+      return vr[i];
+    else
+      return vr[i][x];
+  }
   float qscale;
 
+  // Where the lane's rows lie in page 0 for a tile at a page's first token: keys of the two
+  // products, values of the two groups of four tokens.  A tile's first token is a multiple
+  // of 32, so pages of up to 32 tokens differ by the page alone, longer ones also by t0 & mask,
+  // the same for all lanes.
+  const char *krow[2], *vrow[2];
+  const char *kscales, *vscales;
+
   __device__ void head(const Args& a, int kvh) {
-    kscales = a.ks.data + kvh * a.ks.head;
-    vscales = a.vs.data + kvh * a.vs.head;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int32_t mask = (1 << a.page_log) - 1;
+    kscales = reinterpret_cast<const char*>(a.ks.data + kvh * a.ks.head);
+    vscales = reinterpret_cast<const char*>(a.vs.data + kvh * a.vs.head);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int kt = (c >> 2) * 8 + h * 4 + (c & 3), vt = g * 8 + h * 4;
+      krow[h] = a.kc.data + kvh * a.kc.head + (kt & mask) * a.kc.token + g * 16;
+      // (what lies past the head's values is computed and not kept: any will do)
+      vrow[h] = a.vc.data + kvh * a.vc.head + (vt & mask) * a.vc.token +
+                (c * kV < a.D ? c * kV : 0);
+    }
+  }
+
+  // Pages and scales are looked up for eight tiles at a time, eight groups of four tokens to
+  // each: lane 8 i + j has those of group j of tile i of the block that begins at t0.  This is the
+  // table's entry as it is; it need not wait for the request's length, for what is past the
+  // last token is masked whatever its page holds.
+  static __device__ Spot spot(const Args& a, const int32_t* table, int32_t t0, int step) {
+    const int lane = threadIdx.x & 63;
+    const int32_t t = t0 + (lane >> 3) * step + (lane & 7) * 4;
+    return Spot{t0, table[min(t >> a.page_log, a.width - 1)]};
+  }
+  struct Block {
+    uint32_t page;
+    float kscale, vscale;
+  };
+  __device__ Block block(const Args& a, int32_t entry) const {
+    Block b;
+    b.page = min((uint32_t)entry, (uint32_t)(a.num_pages - 1));
+    b.kscale = *reinterpret_cast<const float*>(kscales + (uint64_t)b.page * a.ks_page);
+    b.vscale = *reinterpret_cast<const float*>(vscales + (uint64_t)b.page * a.vs_page);
+    return b;
+  }
+
+  // The tiles at at.t0, at.t0 + step and so on before `end`.
+  __device__ void walk(const Args& a, const int32_t* table, const T* query, bool live,
+                       const Range& rg, Spot at, int step, int32_t end, State& s) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    Block now = block(a, at.page), next = now;
+    int32_t t0 = at.t0, entry = 0;
+    if (t0 + 8 * step < end) entry = spot(a, table, t0 + 8 * step, step).page;
+    const auto of = [&](int tile, int group) { return tile * 8 + group; };
+    load_keys(a, __shfl(now.page, of(0, (c >> 2) * 2)), __shfl(now.page, of(0, (c >> 2) * 2 + 1)),
+              t0);
+    load_query(a, query, live);
+    load_values(a, __shfl(now.page, of(0, g * 2)), __shfl(now.page, of(0, g * 2 + 1)), t0);
+    for (int i = 0;; i = (i + 1) & 7) {
+      f32x4 sc[2];
+      scores(sc);
+      const float vscale[2] = {__shfl(now.vscale, of(i, g * 2)),
+                               __shfl(now.vscale, of(i, g * 2 + 1))};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sc[h] *= __shfl(now.kscale, of(i, g * 2 + h)) * qscale;
+      const int32_t then = t0 + step;
+      const bool more = then < end;
+      // the next block's entries have had four tiles to arrive, its scales have four more
+      if (i == 3 && t0 + 5 * step < end) next = block(a, entry);
+      if (i == 7 && more) {
+        now = next;
+        if (then + 8 * step < end) entry = spot(a, table, then + 8 * step, step).page;
+      }
+      const int j = (i + 1) & 7;
+      if (more)
+        load_keys(a, __shfl(now.page, of(j, (c >> 2) * 2)),
+                  __shfl(now.page, of(j, (c >> 2) * 2 + 1)), then);
+      add(a, t0, rg, sc, vscale, s);
+      if (!more) break;
+      load_values(a, __shfl(now.page, of(j, g * 2)), __shfl(now.page, of(j, g * 2 + 1)), then);
+      t0 = then;
+    }
   }
 
   __device__ void load_query(const Args& a, const T* src, bool live) {
@@ -136,58 +223,31 @@ struct Tile8 {
     return (((threadIdx.x & 63) >> 4) * 4 + r) * kV;
   }
 
-  static __device__ Spot spot(const Args& a, const int32_t* table, int32_t t0) {
-    return Spot{t0, group_page(a, table, t0 + (threadIdx.x & 7) * 4)};
-  }
-
-  __device__ void load_keys(const Args& a, const char* base, const Spot& at) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-    const int32_t mask = (1 << a.page_log) - 1;
-    kscale = kscales[at.page * a.ks.page];
+  __device__ void load_keys(const Args& a, uint32_t page0, uint32_t page1, int32_t t0) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const uint32_t first = (t0 & ((1 << a.page_log) - 1)) * a.k_token;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int grp = (c >> 2) * 2 + h;
-      const int64_t page = __shfl(at.page, grp);
-      const int32_t t = at.t0 + grp * 4 + (c & 3);
-      const char* p = base + page * a.kc.page + (int64_t)(t & mask) * a.kc.token;
+      const char* p = krow[h] + (uint64_t)(h ? page1 : page0) * a.k_page + first;
 #pragma unroll
       for (int k = 0; k < kK; ++k) {
-        const int d = k * 64 + g * 16;
-        kf[h][k] = u32x4{0, 0, 0, 0};
-        if (d < a.D) kf[h][k] = *reinterpret_cast<const u32x4*>(p + d);
+        // q is zero for what lies past the head's values: any of the row's will do (half of
+        // DP is always there, but for the smallest)
+        const bool there = (DP > 64 && 2 * k < kK) || k * 64 + g * 16 < a.D;
+        const int d = there ? k * 64 : -g * 16;
+        kf[h][k] = *reinterpret_cast<const u32x4*>(p + d);
       }
     }
   }
 
-  __device__ void load_values(const Args& a, const char* base, const Spot& at) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-    const int32_t mask = (1 << a.page_log) - 1;
-    vscale = vscales[at.page * a.vs.page];
+  __device__ void load_values(const Args& a, uint32_t page0, uint32_t page1, int32_t t0) {
+    const uint32_t first = (t0 & ((1 << a.page_log) - 1)) * a.v_token;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int grp = g * 2 + h;
-      const int64_t page = __shfl(at.page, grp);
+      const char* p = vrow[h] + (uint64_t)(h ? page1 : page0) * a.v_page + first;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t t = at.t0 + grp * 4 + i;
-        const char* p = base + page * a.vc.page + (int64_t)(t & mask) * a.vc.token + c * kV;
-        uint32_t (&to)[kV / 4] = vr[h * 4 + i];
-#pragma unroll
-        for (int x = 0; x < kV / 4; ++x) to[x] = 0;
-        if (c * kV < a.D) {
-          if constexpr (kV == 16) {
-            const u32x4 z = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) to[x] = z[x];
-          } else if constexpr (kV == 8) {
-            const u32x2 z = *reinterpret_cast<const u32x2*>(p);
-            to[0] = z[0];
-            to[1] = z[1];
-          } else {
-            to[0] = *reinterpret_cast<const uint32_t*>(p);
-          }
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        vr[h * 4 + i] = *reinterpret_cast<const ValueRow*>(p + i * a.v_token);
     }
   }
 
@@ -200,9 +260,8 @@ struct Tile8 {
     return __builtin_bit_cast(f16x8, x);
   }
 
-  // Scores of the lane's eight tokens t0 + 8g .. for head c.
+  // Products of the lane's eight tokens t0 + 8g .. with head c.
   __device__ void scores(f32x4 (&sc)[2]) const {
-    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       sc[h] = f32x4{0, 0, 0, 0};
@@ -215,32 +274,32 @@ struct Tile8 {
           for (int y = kQ - 1; y >= 0; --y)
             sc[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, q[y][2 * k + x], sc[h], 0, 0, 0);
         }
-      sc[h] *= __shfl(kscale, g * 2 + h) * qscale;
     }
   }
 
-  __device__ void add(const Args& a, int32_t t0, const Range& rg, const f32x4 (&sc)[2], State& s) {
+  __device__ void add(const Args& a, int32_t t0, const Range& rg, const f32x4 (&sc)[2],
+                      const float (&vscale)[2], State& s) {
     const int g = (threadIdx.x & 63) >> 4;
-    const bool whole = t0 >= rg.lo && t0 + 32 <= rg.hi;
-    const float scale[2] = {__shfl(vscale, g * 2), __shfl(vscale, g * 2 + 1)};
     float p[8], w[8];
-    float top = neg_inf();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       p[i] = sc[i >> 2][i & 3];
-      w[i] = scale[i >> 2];
-      if (!whole) {
-        const int32_t t = t0 + g * 8 + i;
-        if (t < rg.lo || t >= rg.hi) {
-          p[i] = neg_inf();
-          // a masked slot may hold anything, as may its page's scale, and 0 * NaN is NaN
-          w[i] = 0.0f;
-#pragma unroll
-          for (int x = 0; x < kV / 4; ++x) vr[i][x] = 0;
-        }
-      }
-      top = fmaxf(top, p[i]);
+      w[i] = vscale[i >> 2];
     }
+    if (t0 < rg.lo || t0 + 32 > rg.hi) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int32_t t = t0 + g * 8 + i;
+        const bool in = t >= rg.lo && t < rg.hi;
+        p[i] = in ? p[i] : neg_inf();
+        // a masked slot may hold anything, as may its page's scale, and 0 * NaN is NaN
+        w[i] = in ? w[i] : 0.0f;
+        if (C::kNan) vr[i] = in ? vr[i] : ValueRow(0);
+      }
+    }
+    float top = neg_inf();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i]);
     const float m = fmaxf(s.m, max_over_groups(top));
     const float m0 = m == neg_inf() ? 0.0f : m;   // nothing seen yet: avoid inf - inf
     const float alpha = exp_of<T>(s.m - m0);
@@ -267,31 +326,32 @@ struct Tile8 {
     }
 #pragma unroll
     for (int x = 0; x < kV / 4; ++x) {
+      uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vr[i][x] = C::prepared(vr[i][x]);
-      add_four<0>(x, change, hi, lo, s);
-      add_four<2>(x, change, hi, lo, s);
+      for (int i = 0; i < 8; ++i) v[i] = C::prepared(word(i, x));
+      add_two<0>(v, &s.acc[4 * x], change, hi, lo);
+      add_two<2>(v, &s.acc[4 * x + 2], change, hi, lo);
     }
   }
 
-  // Two of a word's values (J and J + 1) of the eight tokens.
+  // Two of the values of a word (J and J + 1), of eight tokens.
   template <int J>
-  __device__ void add_four(int x, float change, const f16x8& hi, const f16x8& lo, State& s) {
+  static __device__ void add_two(const uint32_t (&w)[8], f32x4* acc, float change, const f16x8& hi,
+                                 const f16x8& lo) {
     f16x2 v[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f16x2 two[2];
-      C::template across<J>(vr[2 * i][x], vr[2 * i + 1][x], two);
+      C::template across<J>(w[2 * i], w[2 * i + 1], two);
       v[0][i] = two[0];
       v[1][i] = two[1];
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const f16x8 vf = __builtin_bit_cast(f16x8, v[j]);
-      f32x4& acc = s.acc[4 * x + J + j];
-      f32x4 o = acc * change;
+      f32x4 o = acc[j] * change;
       o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi, o, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo, o, 0, 0, 0);
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo, o, 0, 0, 0);
     }
   }
 };

@@ -57,6 +57,7 @@ struct Int8 {
   // As f16 operands of a product, codes are 1 / kUnit of themselves: a byte with its sign bit
   // turned is code + 128, as the bits of an f16 value that times 2^-24; one multiplication
   // and subtraction make the code of it, two at a time.
+  static constexpr bool kNan = false;   // every code is a number
   static constexpr float kUnit = 512.0f;
   static __device__ f16x2 centred(uint32_t two) {
     const f16x2 up = {(_Float16)32768.0f, (_Float16)32768.0f};
@@ -94,6 +95,7 @@ struct E4m3 {
     v[3] = b[1];
   }
 
+  static constexpr bool kNan = true;
   static constexpr float kUnit = 1.0f;
   static __device__ uint32_t prepared(uint32_t w) { return w; }
   template <bool HIGH>

@@ -120,7 +120,7 @@ AttnPlan plan_attention8(const ctcpb_lm_attention_args& g) {
   if (g.window > 0) span = std::min<int64_t>(span, (int64_t)g.window + tile);
   const int64_t all = (int64_t)g.kv_heads * p.head_tiles;
   p.items = g.rows * all;
-  const int64_t slots = 256 * (g.head_dim <= 128 ? 4 : 2);
+  const int64_t slots = 256 * (g.head_dim <= 64 ? 4 : g.head_dim <= 128 ? 3 : 2);
   const int64_t steps = ceil_div(std::max<int64_t>(span, 1), kRangeWaves * tile);
   const int32_t group_waves = g.head_dim <= 128 ? 8 : 4;
   const int64_t few = (int64_t)group_waves * tile * 8;
@@ -365,6 +365,15 @@ int ctcpb_lm_attention8(const ctcpb_lm_attention8_args* args, void* workspace,
     if (g.rows == 0) return ok();
     a.ks = view(args->k_scale);
     a.vs = view(args->v_scale);
+    const int64_t page = std::max(std::max(a.kc.page, a.vc.page), 4 * std::max(a.ks.page, a.vs.page));
+    if (page > UINT32_MAX || std::max(a.kc.token, a.vc.token) > 1 << 23)
+      return fail(CTCPB_ERR_UNSUPPORTED, "pages 4 GiB apart, or tokens of a page more than 8 MiB");
+    a.k_page = (uint32_t)a.kc.page;
+    a.v_page = (uint32_t)a.vc.page;
+    a.k_token = (uint32_t)a.kc.token;
+    a.v_token = (uint32_t)a.vc.token;
+    a.ks_page = (uint32_t)(4 * a.ks.page);
+    a.vs_page = (uint32_t)(4 * a.vs.page);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (g.dtype == CTCPB_LM_BF16)
       launch_attention8<__bf16>(a, p, args->code, st);
