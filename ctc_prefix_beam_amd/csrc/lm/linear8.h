@@ -66,63 +66,89 @@ __device__ inline void quantize_piece(const Values<T, N>& x, float up, float uni
   }
 }
 
+// What a row's largest magnitude (as bits) makes of it.
+struct RowScale {
+  float scale, up, unit, inverse;
+  bool some;   // it has codes other than 0
+  __device__ RowScale(uint32_t most) {
+    const bool finite = most < kInfBits;
+    scale = finite ? bits_f32(most) / 127.0f : bits_f32(kNanBits);
+    // away from the subnormal numbers, where reciprocals overflow
+    up = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+    unit = scale * up;
+    some = finite && scale > 0.0f;
+    inverse = some ? 1.0f / unit : 0.0f;
+  }
+};
+
+// A row's pieces lane, lane + LANES, .. : their largest magnitude, of which a caller with several
+// waves to a row makes the row's.  The last kQuantHeld of them are kept for write().
+constexpr int kQuantHeld = 8;
+template <typename T, int N, int LANES>
+struct RowPieces {
+  static constexpr int U = kQuantHeld;
+  Values<T, N> held[U];
+
+  __device__ uint32_t largest(const char* x, int32_t per, int lane) {
+    uint32_t most = 0;
+    for (int32_t p0 = 0; p0 < per; p0 += U * LANES) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t p = p0 + u * LANES + lane;
+        if (p < per) {
+          held[u].load(x + (int64_t)p * (N * (int)sizeof(T)));
+        } else {
+#pragma unroll
+          for (uint32_t& w : held[u].w) w = 0;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) held[u].raise(most);
+    }
+    most = Values<T, N>::magnitude(most);
+    for (int s = 1; s < 64; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
+    return most;
+  }
+
+  __device__ void write(const char* x, int32_t per, int lane, const RowScale& r, int8_t* codes) {
+    const bool again = per > U * LANES;
+    for (int32_t p0 = 0; p0 < per; p0 += U * LANES)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t p = p0 + u * LANES + lane;
+        if (p >= per) continue;
+        if (again) held[u].load(x + (int64_t)p * (N * (int)sizeof(T)));
+        if (!r.some) {
+#pragma unroll
+          for (uint32_t& w : held[u].w) w = 0;
+        }
+        quantize_piece<T, N>(held[u], r.up, r.unit, r.inverse, codes + p * N);
+      }
+  }
+};
+
 // W waves to a row: one, and four rows to a workgroup, or four.  Bound by memory.
-constexpr int kQuantHeld = 8;   // pieces a lane keeps between the two passes
 template <typename T, int N, int W>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
-  constexpr int U = kQuantHeld, kLanes = 64 * W;
+  constexpr int kLanes = 64 * W;
   __shared__ uint32_t part[4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   if (row >= a.rows) return;   // (of W = 4, no workgroup)
   const int lane = threadIdx.x % kLanes;
   const char* x = a.x + row * a.x_row;
-  Values<T, N> held[U];
-  uint32_t most = 0;
-  for (int32_t p0 = 0; p0 < a.per; p0 += U * kLanes) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t p = p0 + u * kLanes + lane;
-      if (p < a.per) {
-        held[u].load(x + (int64_t)p * (N * (int)sizeof(T)));
-      } else {
-#pragma unroll
-        for (uint32_t& w : held[u].w) w = 0;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) held[u].raise(most);
-  }
-  most = Values<T, N>::magnitude(most);
-  for (int s = 1; s < 64; s <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, s));
+  RowPieces<T, N, kLanes> pieces;
+  uint32_t most = pieces.largest(x, a.per, lane);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) part[wave] = most;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < W; ++w) most = max(most, part[w]);
   }
-  const bool finite = most < kInfBits;
-  const float scale = finite ? bits_f32(most) / 127.0f : bits_f32(kNanBits);
-  if (lane == 0) a.scales[row] = scale;
-  // away from the subnormal numbers, where reciprocals overflow
-  const float up = scale < 0x1p-60f ? 0x1p64f : 1.0f;
-  const float unit = scale * up;
-  const bool some = finite && scale > 0.0f;
-  const float inverse = some ? 1.0f / unit : 0.0f;
+  const RowScale r(most);
+  if (lane == 0) a.scales[row] = r.scale;
   int8_t* codes = a.codes + row * a.codes_row;
-  const bool again = a.per > U * kLanes;
-  for (int32_t p0 = 0; p0 < a.per; p0 += U * kLanes)
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t p = p0 + u * kLanes + lane;
-      if (p >= a.per) continue;
-      if (again) held[u].load(x + (int64_t)p * (N * (int)sizeof(T)));
-      if (!some) {
-#pragma unroll
-        for (uint32_t& w : held[u].w) w = 0;
-      }
-      quantize_piece<T, N>(held[u], up, unit, inverse, codes + p * N);
-    }
+  pieces.write(x, a.per, lane, r, codes);
   for (int32_t k = a.hidden + lane; k < a.padded; k += kLanes) codes[k] = 0;
 }
 
@@ -136,7 +162,16 @@ struct TwoFactors {
                                    second(s > 0x1p64f ? 0x1p64f : 1.0f) {}
 };
 
-// What follows the sums: scales and bias, in float32, and one rounding.
+// What follows a sum: scales and bias, in float32.  Every kernel rounds alike (no product is
+// contracted with the sum but the last, by a power of two), so that a row's results do not
+// depend on how many rows there are.
+__device__ inline float finish(int32_t sum, const TwoFactors& x, float w, float bias) {
+#pragma clang fp contract(off)
+  float y = __builtin_fmaf((float)sum * x.first * w, x.second, bias);
+  asm("" : "+v"(y));   // a float32 value: else f16 results may be rounded from the exact sum
+  return y;
+}
+
 template <typename T>
 struct Linear8Epilogue {
   T* out;
@@ -195,7 +230,8 @@ struct Linear8Epilogue {
         f32x4 y[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          y[h] = __builtin_convertvector(acc[i + h][j], f32x4) * sx.first * sw[h] * sx.second + b[h];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[h][r] = finish(acc[i + h][j][r], sx, sw[h][r], b[h][r]);
         T* to = out + n * ld;
         if (sizeof(T) == 2 && wide) {
           if constexpr (sizeof(T) == 2) {
@@ -239,8 +275,178 @@ __global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T> ep
     for (int r = 0; r < 4; ++r)
       if (m + r < ep.M)
         ep.out[n * ep.ld + m + r] =
-            (T)((float)sum[r] * sx.first * ep.w_scale[m + r] * sx.second +
-                (ep.bias ? ep.bias[m + r] : 0.0f));
+            (T)finish(sum[r], sx, ep.w_scale[m + r], ep.bias ? ep.bias[m + r] : 0.0f);
+  }
+}
+
+// ---------------------------------------------------------- few rows ----
+//
+// Up to 16 * NT rows of x against all of w, in one launch: what it cannot do without is reading
+// w once, and for small layers a launch.  A workgroup of 16 waves to a CU takes the codes of x into
+// LDS, and quantises them for itself from up to kFewValues values (which costs less than a launch of
+// its own).  Then KW waves share the k of a tile of 16 channels, 16 / KW tiles at a time; the next
+// tiles' first weights are on their way while the waves' sums are added.  Weights go from
+// memory straight into the registers of the matrix instruction, kFewHeld of them a lane at a time.
+constexpr int32_t kFewValues = 8192, kFewCodes = 131072;
+constexpr int kFewHeld = 8;
+constexpr int kFewPieces = 256;   // of a row that is quantised here
+
+struct FewArgs {
+  const char* x;
+  int64_t x_row;           // bytes
+  const float *x_scale;    // of codes, else null
+  const int8_t* w;
+  int64_t w_row;
+  const float *w_scale, *bias;
+  char* out;
+  int64_t out_row;         // elements
+  int32_t rows, hidden, features;
+  int32_t padded;          // bytes of a row of w that can be read
+  int32_t per;             // pieces of a row of x
+};
+
+// Codes and scales of rows first, first + step, .. below a.rows, several of them at a time: P pieces a
+// lane to each, and 8 / P rows, so that their loads and reductions overlap.
+template <typename X, int N, int P>
+__device__ inline void quantize_few(const FewArgs& a, int first, int step, int lane, int8_t* codes,
+                                    int pitch, float* sx) {
+  constexpr int R = kQuantHeld / P;
+  for (int n0 = first; n0 < a.rows; n0 += R * step) {
+    Values<X, N> held[R][P];
+    uint32_t most[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int n = min(n0 + r * step, a.rows - 1);   // (the last row again: not kept)
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (p * 64 + lane < a.per) {
+          held[r][p].load(a.x + n * a.x_row + (p * 64 + lane) * (N * (int)sizeof(X)));
+        } else {
+#pragma unroll
+          for (uint32_t& w : held[r][p].w) w = 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      most[r] = 0;
+#pragma unroll
+      for (int p = 0; p < P; ++p) held[r][p].raise(most[r]);
+      most[r] = Values<X, N>::magnitude(most[r]);
+    }
+    for (int s = 1; s < 64; s <<= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) most[r] = max(most[r], (uint32_t)__shfl_xor((int)most[r], s));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int n = n0 + r * step;
+      const RowScale q(most[r]);
+      if (n < a.rows) {
+        if (lane == 0) sx[n] = q.scale;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (!q.some) {
+#pragma unroll
+            for (uint32_t& w : held[r][p].w) w = 0;
+          }
+          if (p * 64 + lane < a.per)
+            quantize_piece<X, N>(held[r][p], q.up, q.unit, q.inverse,
+                                 codes + n * pitch + (p * 64 + lane) * N);
+        }
+      }
+    }
+  }
+}
+
+// X: type of x (int8_t: codes), N: its values to a piece; KW: 4, or 16 for few channels.
+template <typename T, typename X, int N, int NT, int KW>
+__global__ __launch_bounds__(1024) void linear8_few_kernel(FewArgs a) {
+  constexpr int U = kFewHeld, G = 16 / KW;
+  extern __shared__ __align__(16) char few_lds[];
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave % KW, mine = wave / KW;   // of a tile's k, and of the G tiles
+  const int steps = (a.padded + 63) / 64;
+  const int pitch = steps * 64 + 16;   // rows begin in different banks
+  int8_t* codes = reinterpret_cast<int8_t*>(few_lds);
+  i32x4* parts = reinterpret_cast<i32x4*>(few_lds + a.rows * pitch);   // [wave][NT][lane]
+  float* sx = reinterpret_cast<float*>(parts + 16 * NT * 64);
+  const int tiles = (a.features + 15) / 16;
+  u32x4 held[U];
+  // the lane's weights of U steps of a tile from step s on, every KW-th one
+  const auto load = [&](int tile, int s) {
+    const int8_t* row = a.w + (int64_t)min(tile * 16 + c, a.features - 1) * a.w_row;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (s + KW * u) * 64 + g * 16;
+      held[u] = u32x4{0, 0, 0, 0};
+      if (k < a.padded) held[u] = *reinterpret_cast<const u32x4*>(row + k);
+    }
+  };
+  int first = blockIdx.x * G;   // of the G tiles
+  load(first + mine, part);
+  if constexpr (sizeof(X) == 1) {
+    for (int n = wave; n < a.rows; n += 16) {
+      const char* x = a.x + n * a.x_row;
+#pragma unroll 4
+      for (int p = lane; p < a.per; p += 64) {
+        if constexpr (N == 16)
+          reinterpret_cast<u32x4*>(codes + n * pitch)[p] = reinterpret_cast<const u32x4*>(x)[p];
+        else
+          codes[n * pitch + p] = static_cast<int8_t>(x[p]);
+      }
+      if (lane == 0) sx[n] = a.x_scale[n];
+    }
+  } else if (a.per <= 64) {
+    quantize_few<X, N, 1>(a, wave, 16, lane, codes, pitch, sx);
+  } else if (a.per <= 128) {
+    quantize_few<X, N, 2>(a, wave, 16, lane, codes, pitch, sx);
+  } else {
+    quantize_few<X, N, 4>(a, wave, 16, lane, codes, pitch, sx);
+  }
+  for (int n = wave; n < a.rows; n += 16)
+    for (int k = a.hidden + lane; k < steps * 64; k += 64) codes[n * pitch + k] = 0;
+  __syncthreads();
+  for (; first < tiles; first += gridDim.x * G) {
+    i32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+    for (int s = part;; s += KW * U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (s + KW * u < steps) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            // rows past the last one repeat it, and are not kept
+            const int n = min(t * 16 + c, a.rows - 1);
+            const i32x4 xf = *reinterpret_cast<const i32x4*>(codes + n * pitch +
+                                                             (s + KW * u) * 64 + g * 16);
+            acc[t] = Frag<int8_t>::mac(__builtin_bit_cast(i32x4, held[u]), xf, acc[t]);
+          }
+        }
+      }
+      if (s + KW * U >= steps) break;
+      load(first + mine, s + KW * U);
+    }
+    if (first + (int)gridDim.x * G < tiles) load(first + gridDim.x * G + mine, part);
+    __syncthreads();   // the tiles before have been added
+#pragma unroll
+    for (int t = 0; t < NT; ++t) parts[(wave * NT + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    // a thread has a channel and a row of x: 16 * G channels, of which 16 to a tile, next to
+    // each other in out
+    for (int i = threadIdx.x; i < 256 * NT * G; i += 1024) {
+      const int m = i % (16 * G), n = i / (16 * G);
+      const int64_t at = (int64_t)first * 16 + m;
+      if (n >= a.rows || at >= a.features) continue;
+      int32_t sum = 0;
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+        sum += reinterpret_cast<const int32_t*>(
+            parts + ((m / 16 * KW + w) * NT + (n >> 4)) * 64 + ((m & 15) >> 2) * 16 + (n & 15))[m & 3];
+      reinterpret_cast<T*>(a.out)[n * a.out_row + at] =
+          (T)finish(sum, TwoFactors(sx[n]), a.w_scale[at], a.bias ? a.bias[at] : 0.0f);
+    }
   }
 }
 

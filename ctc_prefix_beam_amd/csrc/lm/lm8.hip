@@ -124,9 +124,27 @@ AttnPlan plan_attention8(const ctcpb_lm_attention_args& g) {
   const int64_t steps = ceil_div(std::max<int64_t>(span, 1), kRangeWaves * tile);
   const int32_t group_waves = g.head_dim <= 128 ? 8 : 4;
   const int64_t few = (int64_t)group_waves * tile * 8;
-  if (span <= few && p.items * 4 * tile >= slots * span) {
+  // As for 16-bit caches, whose reasons hold: few and short rows a workgroup each, many short
+  // ones a wave each, the rest by ranges.  Rows of random lengths up to a bound, in us (a wave
+  // each / a workgroup each / ranges):
+  //   bf16, e4m3, 16 query and 4 key/value heads of 64: 16 rows up to 1024 31.5 / 10.7 / 17.5,
+  //     up to 4096 108 / 23.4 / 18.6; 256 rows up to 256 13.2 / 13.7 / 18.2, up to 512 20.0 /
+  //     17.1 / 23.2, up to 2048 59.4 / 34.3 / 38.8; 1024 rows up to 512 35.1 / 46.4 / 44.0, up to
+  //     2048 130 / 110 / 121; 4096 rows up to 512 123 / 183 / 168
+  //   bf16, int8, 32 and 8 of 128: 16 rows up to 1024 43.5 / 15.1 / 21.9, up to 4096 179 / 38.1 /
+  //     28.6; 256 rows up to 256 24.3 / 42.0 / 34.4, up to 512 38.9 / 50.7 / 43.9, up to 1024 71.4
+  //     / 72.6 / 63.0; 1024 rows up to 512 129 / 192 / 153
+  //   bf16, int8, 8 and 4 of 256: 64 rows up to 512 36.0 / 18.2 / 24.4; 256 rows up to 512 39.6 /
+  //     50.9 / 42.4
+  //   f32, int8, 8 of 64: 64 rows up to 1024 46.3 / 21.9 / 31.0; 256 rows up to 512 34.0 / 42.8 /
+  //     39.4, up to 1024 59.9 / 58.7 / 51.0
+  // Wide heads and f32 leave registers for one workgroup of eight waves on a CU at a time, so
+  // that many of them are slower than ranges (not with heads of 64 in 16 bits).
+  const bool crowded = (g.head_dim > 64 || g.dtype == CTCPB_LM_F32) &&
+                       p.items * group_waves >= 16 * slots;
+  if (span <= few && p.items * 8 * tile >= slots * span) {
     p.waves = 1;
-  } else if (span <= few) {
+  } else if (span <= few && !crowded) {
     p.waves = group_waves;
   } else {
     p.ranges = (int32_t)std::max<int64_t>(1, std::min(slots / all, g.rows * steps));
@@ -170,17 +188,21 @@ constexpr int32_t kMostHidden = 131071;   // 128 * 128 * it is below 2^31
 struct LinearPlan {
   int32_t padded;             // hidden up to 16 bytes
   bool quantize, pad_x, pad_w;
+  bool few;                   // one launch for few rows
   Cut cut;
   int32_t pitch;
   size_t o_x, o_scale, o_w, o_planes, bytes;
 };
 
-int code_size(int32_t dtype) { return dtype == CTCPB_LM_CODES ? 1 : elem_size(dtype); }
-
 // Whether rows of codes begin where they can be read 16 bytes at a time (their addresses
 // within a tile have 31 bits).
 bool codes_aligned(const void* p, int64_t stride) {
   return aligned(p, 16) && stride % 16 == 0 && stride <= 1 << 23;
+}
+
+// Whether rows of values begin on 16 bytes.
+bool rows_aligned(const ctcpb_lm_linear8_args& g) {
+  return aligned(g.x, 16) && g.stride_x * elem_size(g.dtype) % 16 == 0;
 }
 
 LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
@@ -192,7 +214,21 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   // there, w may have anything.
   p.pad_x = !p.quantize && (g.hidden % 16 != 0 || !codes_aligned(g.x, g.stride_x));
   p.pad_w = (g.hidden % 16 != 0 && !readable) || !codes_aligned(g.w, g.stride_w);
-  p.cut = choose_cut(1, g.features, g.rows, p.padded, true);
+  // In us, one launch for few rows of codes / the product's tiles: 5000 channels of 512 6.4 and 7.0
+  // for a row, 8.1 and 7.2 for 32; 2048 of 2048 6.6 and 10.6, 7.6 and 10.4; 8192 of 2048 8.4 and
+  // 13.4, 10.5 and 15.8; 50000 of 2048 22.8 and 23.6, 32 and 25.  With x quantised there / before it:
+  // 16 rows of 512 10.6 and 10.9, 4 of 2048 9.5 and 10.8, 16 of 2048 11.7 and 11.0.
+  const int64_t values = (int64_t)g.rows * up(p.padded, 64);
+  p.few = g.rows <= (p.padded >= 1024 ? 32 : 16) && values <= kFewCodes && !p.pad_w &&
+          g.features <= 64 * kCUs;
+  if (p.few) {
+    p.pad_x = false;
+    const int per = 16 / elem_size(g.dtype);
+    const bool pieces = g.hidden <= kFewPieces * (g.hidden % per || !rows_aligned(g) ? 1 : per);
+    p.quantize = p.quantize && (values > kFewValues || !pieces);
+  } else {
+    p.cut = choose_cut(1, g.features, g.rows, p.padded, true);
+  }
   p.pitch = (int32_t)up(g.features, 4);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -211,8 +247,8 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
 
 int check_linear8(const ctcpb_lm_linear8_args& g) {
   if (!elem_size(g.dtype)) return fail(CTCPB_ERR_INVALID, kBadType);
-  if (!code_size(g.x_dtype))
-    return fail(CTCPB_ERR_INVALID, "x_dtype must be a type or CTCPB_LM_CODES");
+  if (g.x_dtype != g.dtype && g.x_dtype != CTCPB_LM_CODES)
+    return fail(CTCPB_ERR_INVALID, "x_dtype must be dtype or CTCPB_LM_CODES");
   if (g.flags & ~CTCPB_LM_READABLE) return fail(CTCPB_ERR_INVALID, "flags has unknown bits");
   if (g.rows < 0 || g.features < 1 || g.hidden < 1)
     return fail(CTCPB_ERR_INVALID, "need rows >= 0, features >= 1 and hidden >= 1");
@@ -269,8 +305,60 @@ Operand codes_of(const void* data, int64_t stride, int32_t rows, int32_t hidden,
   return Operand{copy, padded, rows, false};
 }
 
+template <typename T, typename X, int N, int NT>
+void launch_few(const FewArgs& a, hipStream_t st) {
+  const int tiles = ceil_div(a.features, 16);
+  const size_t lds =
+      (size_t)a.rows * (up(a.padded, 64) + 16) + 16 * NT * 1024 + a.rows * sizeof(float);
+  // Four waves to a tile, and four tiles at a time to a workgroup, where rows are too short for 16
+  // and there are tiles enough
+  if (tiles <= kCUs || a.padded >= 1024)
+    launch_with_lds(linear8_few_kernel<T, X, N, NT, 16>, (unsigned)std::min(tiles, kCUs), 1024, lds,
+                    a, st);
+  else
+    launch_with_lds(linear8_few_kernel<T, X, N, NT, 4>, (unsigned)std::min(ceil_div(tiles, 4), kCUs),
+                    1024, lds, a, st);
+}
+
+template <typename T, typename X, int N>
+void launch_few(const FewArgs& a, hipStream_t st) {
+  if (a.rows <= 16)
+    launch_few<T, X, N, 1>(a, st);
+  else
+    launch_few<T, X, N, 2>(a, st);
+}
+
+// x of type X, in pieces of 16 bytes or single values.
+template <typename T, typename X>
+void launch_few(FewArgs& a, const void* x, int64_t stride, hipStream_t st) {
+  constexpr int N = 16 / (int)sizeof(X);
+  a.x = static_cast<const char*>(x);
+  a.x_row = stride * (int)sizeof(X);
+  const bool wide = a.hidden % N == 0 && aligned(x, 16) && a.x_row % 16 == 0;
+  a.per = wide ? a.hidden / N : a.hidden;
+  if (wide)
+    launch_few<T, X, N>(a, st);
+  else
+    launch_few<T, X, 1>(a, st);
+}
+
+template <typename T>
+void run_few(const LinearPlan& p, const ctcpb_lm_linear8_args& g, char* ws, hipStream_t st) {
+  FewArgs a{nullptr, 0, g.x_scale, g.w, g.stride_w, g.w_scale, g.bias, static_cast<char*>(g.out),
+            g.stride_out, g.rows, g.hidden, g.features, p.padded, 0};
+  if (g.x_dtype == CTCPB_LM_CODES) return launch_few<T, int8_t>(a, g.x, g.stride_x, st);
+  if (!p.quantize) return launch_few<T, T>(a, g.x, g.stride_x, st);   // (out has x's type)
+  float* scales = reinterpret_cast<float*>(ws + p.o_scale);
+  launch_quantize(g.x_dtype, g.x, g.stride_x, reinterpret_cast<int8_t*>(ws + p.o_x), p.padded,
+                  scales, g.rows, g.hidden, p.padded, st);
+  a.x_scale = scales;
+  a.hidden = p.padded;   // zeros behind
+  launch_few<T, int8_t>(a, ws + p.o_x, p.padded, st);
+}
+
 template <typename T>
 void run_linear8(const LinearPlan& p, const ctcpb_lm_linear8_args& g, char* ws, hipStream_t st) {
+  if (p.few) return run_few<T>(p, g, ws, st);
   const float* x_scale = g.x_scale;
   Operand x;
   if (p.quantize) {

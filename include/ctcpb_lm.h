@@ -310,8 +310,8 @@ enum { CTCPB_LM_READABLE = 1 };
  *   out[n, m] = (sum_k xc[n, k] w[m, k]) * xs[n] * w_scale[m] + bias[m]
  * with codes xc and scales xs of x as ctcpb_lm_quantize_rows makes them, or as given.  The sum
  * is exact, the rest float32 with one rounding to out's type.
- *   x        device, x_dtype, row stride stride_x >= 0;  x_scale: device float32 [rows], with
- *            CTCPB_LM_CODES only
+ *   x        device, row stride stride_x >= 0; x_dtype is dtype, or CTCPB_LM_CODES, with x_scale:
+ *            device float32 [rows]
  *   w        device int8 [features][hidden], row stride stride_w >= 0;  w_scale: device
  *            float32 [features];  bias: device float32 [features] or NULL
  *   out      device, typed (dtype), row stride stride_out >= features

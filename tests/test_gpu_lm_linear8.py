@@ -112,6 +112,29 @@ def test_sizes(dtype, N, M, H):
     check(x, w, ws, bias)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,M,H", [
+    (1, 1, 1), (1, 100, 32768), (1, 50000, 40), (2, 77, 16000), (4, 129, 8192), (5, 33, 5003),
+    (16, 20000, 64), (16, 48, 2048), (17, 1000, 100), (31, 333, 1000), (32, 5000, 512),
+    (32, 65, 1024), (32, 65, 1025),
+    (32, 4100, 4000), (32, 4111, 2048), (20, 50, 6553), (3, 300, 43000)])
+def test_few_rows(dtype, N, M, H):
+    """Rows on both sides of what one launch does, with weights in rows that can be read past
+    their ends, where anything may lie; as values and as codes."""
+    x = rows(N, H, dtype, N)
+    w, ws = weight(M, H)
+    wide = torch.full((M, -(-H // 16) * 16 + 16), 99, dtype=torch.int8, device="cuda")[:, :H]
+    wide.copy_(w)
+    bias = torch.randn(M).cuda()
+    want = check(x, w, ws, bias)
+    assert torch.equal(check(x, wide, ws, bias), want)
+    codes, s = lm.quantize_rows(x)
+    assert torch.equal(lm.linear8(codes, wide, ws, bias, x_scale=s, dtype=dtype), want)
+    apart = torch.zeros((N, H + 3), dtype=dtype, device="cuda")[:, 1:H + 1]
+    apart.copy_(x)
+    assert torch.equal(lm.linear8(apart, wide, ws, bias), want)
+
+
 @pytest.mark.parametrize("N,M,H", [(1, 40, 131071), (3, 70, 100000), (300, 40, 65536)])
 def test_long_sums_stay_whole(N, M, H):
     """Sums of up to 2^31 - 128^2, exact in 32 bits."""
@@ -125,6 +148,20 @@ def test_long_sums_stay_whole(N, M, H):
     out = lm.linear8(w[:1].expand(N, H), w, one, x_scale=xs, dtype=torch.float32)
     assert (out.double() == 128.0 * 128 * H).all() or H % 2   # (131071: 2^31 - 2^14, 17 bits)
     assert ((out.double() - 128.0 * 128 * H).abs() <= 2.0 ** -23 * 128.0 * 128 * H).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_row_is_the_same_among_others(dtype):
+    """Whatever kernels the number of rows takes: sums are exact, and what follows is alike."""
+    M, H = 777, 1032
+    x = rows(2500, H, dtype)
+    w, ws = lm.quantize_rows(torch.randn(M, H, device="cuda"))
+    bias = torch.randn(M, device="cuda")
+    want = lm.linear8(x, w, ws, bias)
+    for n in (1, 5, 16, 17, 31, 40, 100, 300, 1100):
+        assert torch.equal(lm.linear8(x[7:7 + n], w, ws, bias), want[7:7 + n]), n
+        some = lm.linear8(x[7:7 + n], w[:500], ws[:500], bias[:500])
+        assert torch.equal(some, want[7:7 + n, :500]), n
 
 
 def test_large_tiles_against_products_in_pieces():

@@ -98,7 +98,7 @@ def test_quantize_refusals(L):
     assert quantize(rows=0, x=N, codes=N, s=N) == 0
 
 
-def linear(L, x=P, xs=N, w=P, wscale=P, out=P, sx=64, sw=64, so=100, xt=0, dtype=0, rows=3, M=100,
+def linear(L, x=P, xs=N, w=P, wscale=P, out=P, sx=64, sw=64, so=100, xt=0, dtype=0, rows=90, M=100,
            H=64, flags=0, ws=P, ws_bytes=1 << 40):
     return L.ctcpb_lm_linear8(lm._LINEAR8.pack(x, xs, w, wscale, N, out, sx, sw, so, xt, dtype, rows,
                                                M, H, flags), ws, ws_bytes, None)
@@ -106,7 +106,7 @@ def linear(L, x=P, xs=N, w=P, wscale=P, out=P, sx=64, sw=64, so=100, xt=0, dtype
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=N), 1), (dict(w=N), 1), (dict(wscale=N), 1), (dict(out=N), 1), (dict(xt=3), 1),
-    (dict(xt=4), 1), (dict(xt=-1), 1), (dict(dtype=3), 1), (dict(rows=-1), 1), (dict(M=0), 1),
+    (dict(xt=4), 1), (dict(xt=1), 1), (dict(xt=-1), 1), (dict(dtype=3), 1), (dict(rows=-1), 1), (dict(M=0), 1),
     (dict(H=0), 1), (dict(sx=-1), 1), (dict(sw=-1), 1), (dict(so=99), 1), (dict(flags=2), 1),
     (dict(H=131072), 3), (dict(rows=1 << 30, M=1 << 30, so=1 << 30), 3), (dict(ws=N), 1),
     (dict(ws=264), 1), (dict(ws_bytes=8), 2)])
@@ -121,6 +121,7 @@ def test_linear_workspace(L):
         assert L.ctcpb_lm_linear8_workspace(lm._LINEAR8.pack(
             x, N, w, N, N, N, sx, sw, M, xt, 0, rows, M, H, flags), out) == 0
         return out.value
+    assert size(rows=16, H=512, sx=512, sw=512) == 0   # few rows: one launch
     codes, one = -(-1000 * 64 // 256) * 256, -(-4000 // 256) * 256
     assert size() == codes + one                       # x as codes, and their scales
     assert size(xt=3) == 0                             # everything in place
