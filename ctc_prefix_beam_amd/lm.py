@@ -461,12 +461,14 @@ def _codes(t, name):
 def _cache8(k_cache, v_cache, k_scale, v_scale, index, written):
     """(code, (pages, page_size, heads, dim), the caches' and scales' addresses and strides)."""
     _gpu(k_cache, "k_cache")
+    dtype = k_cache.dtype
     code = _codes(k_cache, "k_cache")
-    kc = _cache(k_cache, index, "k_cache", k_cache.dtype)
+    kc = _cache(k_cache, index, "k_cache", dtype)
     shape = k_cache.shape
-    vc = _cache(v_cache, index, "v_cache", k_cache.dtype, shape)
-    _like(k_scale, index, "k_scale", torch.float32, (shape[0], shape[2]))
-    _like(v_scale, index, "v_scale", torch.float32, (shape[0], shape[2]))
+    vc = _cache(v_cache, index, "v_cache", dtype, shape)
+    each = (shape[0], shape[2])
+    _like(k_scale, index, "k_scale", torch.float32, each)
+    _like(v_scale, index, "v_scale", torch.float32, each)
     ks, vs = k_scale.stride(), v_scale.stride()
     if written:
         _apart(k_cache, kc[1:], "k_cache")
@@ -476,9 +478,9 @@ def _cache8(k_cache, v_cache, k_scale, v_scale, index, written):
     return code, shape, kc + vc, (k_scale.data_ptr(), *ks, v_scale.data_ptr(), *vs)
 
 
-def _no_gradient(name, *tensors):
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in tensors):
+def _no_gradient(name):
+    """Raise ValueError for a call with tensors that ask for gradients, which it cannot give."""
+    if torch.is_grad_enabled():
         raise ValueError(f"{name} carries no gradients: call it under torch.no_grad() or on "
                          "detached tensors")
 
@@ -493,10 +495,11 @@ def cache_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     ones less than one; one that is not finite makes its page's scale NaN, until the page
     begins anew."""
     dev = _gpu(k, "k")
-    _no_gradient("cache_store8", k, v)
     dt = _type(k, "k")
     kt, kh, shape = _rows(k, "k")
     _like(v, dev, "v", k.dtype, shape)
+    if k.requires_grad or v.requires_grad:
+        _no_gradient("cache_store8")
     vt, vh, _ = _rows(v, "v")
     T, H, D = shape
     _i32(slots, dev, "slots", (T,))
@@ -537,7 +540,8 @@ def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: fl
     (pages, kv_heads) >= 0: keys and values are code times scale of their page and head.  q and
     out are bfloat16, float16 or float32; head_dim is a multiple of 16."""
     dev = _gpu(q, "q")
-    _no_gradient("attention8", q)
+    if q.requires_grad:
+        _no_gradient("attention8")
     dt = _type(q, "q")
     qr, qh, shape = _rows(q, "q")
     R, Hq, D = shape
@@ -586,7 +590,8 @@ def quantize_rows(x, stream=None):
     with a value that is not finite has the scale NaN.  Rows of codes begin on 16 bytes, with
     zeros behind them, as ``linear8`` reads them best."""
     dev = _gpu(x, "x")
-    _no_gradient("quantize_rows", x)
+    if x.requires_grad:
+        _no_gradient("quantize_rows")
     dt = _type(x, "x")
     sx, N, H = _matrix(x, "x")
     if H == 0:
@@ -615,18 +620,21 @@ def linear8(x, w, w_scale, bias=None, x_scale=None, dtype=None, out=None, stream
     x_scale float32 (rows,), and `dtype` (default bfloat16) is that of out.  bias: float32
     (features,) or None.  Sums of codes are exact; hidden is at most 131071."""
     dev = _gpu(x, "x")
-    _no_gradient("linear8", x, w_scale, bias, x_scale)
     sx, N, H = _matrix(x, "x")
     _like(w, dev, "w", torch.int8)
     sw, M, _ = _matrix(w, "w", H)
     _floats(w_scale, dev, "w_scale", M)
     if bias is not None:
         _floats(bias, dev, "bias", M)
+    if x.requires_grad or w_scale.requires_grad or (bias is not None and bias.requires_grad):
+        _no_gradient("linear8")
     flags = _READABLE if _readable(w, sw, M, H) else 0
     if x.dtype is torch.int8:
         if x_scale is None:
             raise ValueError("x of int8 codes needs x_scale")
         _floats(x_scale, dev, "x_scale", N)
+        if x_scale.requires_grad:
+            _no_gradient("linear8")
         xt, dtype = _CODES_X, dtype or torch.bfloat16
     else:
         if x_scale is not None:
