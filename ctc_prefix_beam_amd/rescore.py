@@ -2,7 +2,7 @@
 decoder token by token, with a paged key/value cache, and its output layer is
 trained on the best ones.
 
-    python -m ctc_prefix_beam_amd.rescore
+    python -m ctc_prefix_beam_amd.rescore [--bits 8]
 
 decodes seeded synthetic utterances, rescores their 8-best lists with a small
 randomly initialised model, takes training steps on its output layer with the
@@ -11,11 +11,13 @@ operators of ``ctc_prefix_beam_amd.lm`` together as a user would: pages and
 slots from the hypotheses' lengths (of which only the longest is read back), the
 store of new keys and values, attention over the cache, and token losses with
 gradients.
-Projections and normalisations are plain torch.
+Projections and normalisations are plain torch.  With 8 bits, the cache holds int8 codes with
+a scale for each page and head, and the projections are products of int8 weights with
+activations quantised by token (the embedding and the output layer stay as they are).
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -32,6 +34,8 @@ class ModelConfig:
     head_dim: int = 64
     max_len: int = 1024
     dtype: torch.dtype = torch.bfloat16
+    cache_dtype: torch.dtype | None = None   # torch.int8 or torch.float8_e4m3fn: an 8-bit cache
+    weights8: bool = False                   # projections of int8 weights, scaled by channel
 
 
 class LanguageModel:
@@ -44,20 +48,24 @@ class LanguageModel:
 
         def weight(rows, cols):
             return (torch.randn((rows, cols), generator=g) / cols ** 0.5).to(c.dtype).to(device)
+
+        def projection(rows, cols):
+            w = weight(rows, cols)
+            return lm.quantize_rows(w) if c.weights8 else w
         self.embed = weight(c.vocab, c.hidden)
         self.position = weight(c.max_len + 1, c.hidden)
         heads = c.q_heads + 2 * c.kv_heads
-        self.qkv = [weight(heads * c.head_dim, c.hidden) for _ in range(c.layers)]
-        self.o = [weight(c.hidden, c.q_heads * c.head_dim) for _ in range(c.layers)]
-        self.up = [weight(4 * c.hidden, c.hidden) for _ in range(c.layers)]
-        self.down = [weight(c.hidden, 4 * c.hidden) for _ in range(c.layers)]
+        self.qkv = [projection(heads * c.head_dim, c.hidden) for _ in range(c.layers)]
+        self.o = [projection(c.hidden, c.q_heads * c.head_dim) for _ in range(c.layers)]
+        self.up = [projection(4 * c.hidden, c.hidden) for _ in range(c.layers)]
+        self.down = [projection(c.hidden, 4 * c.hidden) for _ in range(c.layers)]
         self.out = weight(c.vocab, c.hidden)
         self.bias = torch.zeros(c.vocab, device=device)
 
     def cache(self, rows: int, max_len: int, num_pages: int = 0, page_size: int = 16):
         c = self.cfg
-        return lm.PagedCache(rows, max_len, c.kv_heads, c.head_dim, c.dtype, page_size, num_pages,
-                             self.embed.device, layers=c.layers)
+        return lm.PagedCache(rows, max_len, c.kv_heads, c.head_dim, c.cache_dtype or c.dtype,
+                             page_size, num_pages, self.embed.device, layers=c.layers)
 
     def step(self, tokens, alive, cache, max_len: int = 0):
         """Hidden states (rows, hidden) after one more token of every row with
@@ -72,18 +80,23 @@ class LanguageModel:
         slots = torch.where(alive, plan.slots[at], -1)
         x = self.embed[tokens] + self.position[before.long()]
         for i in range(c.layers):
-            qkv = (_norm(x) @ self.qkv[i].t()).view(rows, -1, c.head_dim)
+            qkv = _project(_norm(x), self.qkv[i]).view(rows, -1, c.head_dim)
             q, k, v = qkv.split((c.q_heads, c.kv_heads, c.kv_heads), 1)
             cache.store(k, v, slots, layer=i)
             a, _ = cache.attend(q, layer=i, max_len=max_len)
-            x = x + a.reshape(rows, -1) @ self.o[i].t()
-            x = x + torch.nn.functional.gelu(_norm(x) @ self.up[i].t()) @ self.down[i].t()
+            x = x + _project(a.reshape(rows, -1), self.o[i])
+            x = x + _project(torch.nn.functional.gelu(_project(_norm(x), self.up[i])), self.down[i])
         return _norm(x)
 
 
 def _norm(x):
     f = x.float()
     return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
+
+
+def _project(x, w):
+    """x times a projection's weight, which is a tensor or (codes, scales)."""
+    return x @ w.t() if isinstance(w, torch.Tensor) else lm.linear8(x, *w)
 
 
 def _longest(model: LanguageModel, toks, lens) -> int:
@@ -174,12 +187,18 @@ def utterances(rows: int, frames: int, vocab: int, seed: int = 0):
     return z.log_softmax(-1), torch.full((rows,), frames, dtype=torch.int32)
 
 
-def main():
+def in_8_bits(cfg: ModelConfig) -> ModelConfig:
+    """The same model with an int8 cache and int8 projections."""
+    return replace(cfg, cache_dtype=torch.int8, weights8=True)
+
+
+def main(bits: int = 16):
     from . import DecoderConfig, OfflineDecoder
     lp, lens = utterances(8, 200, 256)
     dec = OfflineDecoder(DecoderConfig(beam=8, nbest=8, blank_threshold=0.999, max_out_len=100))
     tokens, lengths, scores = dec.decode(lp.cuda(), lens.cuda())
-    model = LanguageModel(ModelConfig(vocab=256))
+    cfg = ModelConfig(vocab=256)
+    model = LanguageModel(in_8_bits(cfg) if bits == 8 else cfg)
     order, _ = rescore(model, tokens, lengths, scores)
     print("order before training:", order[0].tolist())
     losses = train_output(model, tokens[:, :1], lengths[:, :1])
@@ -191,4 +210,7 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    import argparse
+    parser = argparse.ArgumentParser(description="second pass over N-best lists")
+    parser.add_argument("--bits", type=int, choices=(8, 16), default=16)
+    main(parser.parse_args().bits)
