@@ -38,13 +38,15 @@ __device__ inline uint32_t wave_magnitude(uint32_t most) {
 // where old is 0 if a token goes to slot 0 of the page, which begins it anew, else what the
 // page has.  Where a page's scale grows, its codes are multiplied by old / new first.
 //
-// A wave makes a page's scale and codes by itself, so nothing crosses waves: tokens of one
-// page follow one another in the call, and the wave that has the first of them in its chunk
-// of `chunk` tokens (the one before with a slot lies in another page) does the page's whole
+// W waves make a page's scale and codes by themselves, so nothing crosses workgroups: tokens of
+// one page follow one another in the call, and the waves that have the first of them in their chunk
+// of `chunk` tokens (the one before with a slot lies in another page) do the page's whole
 // run, for one head of the keys or of the values.  A run's values stay in registers
-// between the two passes (maximum, codes) up to kHeld pieces a lane.
+// between the two passes (maximum, codes) up to kStoreHeld pieces a lane; W is chosen so that
+// those of a page do.
 //
-// Bound by memory for prompts and by latency for a step of single tokens.
+// Bound by memory for prompts (131072 tokens of 8 x 128 bf16, pages of 16: 167 us, 4.8 TB/s) and by
+// latency for a step of single tokens.
 constexpr int kStoreHeld = 4;
 
 // The page of the nearest token with a slot before token t, -1 if there is none.
@@ -58,9 +60,9 @@ __device__ inline int32_t page_before(const Cache8Args& a, int32_t t, int lane) 
   return -1;
 }
 
-template <typename T, typename C, int N>
+template <typename T, typename C, int N, int W>
 struct StoreRun {
-  static constexpr int U = kStoreHeld;
+  static constexpr int U = kStoreHeld, kLanes = 64 * W;
   const char* src;          // the head's row of token 0
   int64_t src_t;
   char* page;               // the head's row of slot 0
@@ -75,8 +77,8 @@ struct StoreRun {
   };
   __device__ At first() const { return At{lane / per, lane % per}; }
   __device__ void next(At& at) const {
-    at.t += 64 / per;
-    at.j += 64 % per;
+    at.t += kLanes / per;
+    at.j += kLanes % per;
     if (at.j >= per) {
       at.j -= per;
       ++at.t;
@@ -165,11 +167,14 @@ struct StoreRun {
 };
 
 // N: values of a piece, 8 (16-bit types) or 4 (f32) where rows and strides allow, else 1.
-template <typename T, typename C, int N>
-__global__ __launch_bounds__(256) void store8_kernel(Cache8Args a) {
+// W: waves of a workgroup that do a run together; with one, a workgroup's four have four runs.
+template <typename T, typename C, int N, int W>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Args a) {
+  __shared__ uint32_t part[2][W];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;   // (chunk, head, keys or values)
+  // (chunk, head, keys or values)
+  const int64_t unit = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   const int64_t chunk = unit / (2 * a.heads);
   const int64_t begin = chunk * a.chunk;
   if (begin >= a.tokens) return;
@@ -195,7 +200,7 @@ __global__ __launch_bounds__(256) void store8_kernel(Cache8Args a) {
   const CacheView& c = values ? a.vc : a.kc;
   const ScaleView& sc = values ? a.vs : a.ks;
   const int32_t mask = (1 << a.page_log) - 1;
-  while (leaders) {
+  for (int parity = 0; leaders; parity ^= 1) {
     const int first = __builtin_ctzll(leaders);
     leaders &= leaders - 1;
     const int32_t page = __builtin_amdgcn_readlane(mine, first);
@@ -219,7 +224,7 @@ __global__ __launch_bounds__(256) void store8_kernel(Cache8Args a) {
         if (other) break;
       }
     }
-    StoreRun<T, C, N> run;
+    StoreRun<T, C, N, W> run;
     const int32_t from = t0 + first;
     run.src_t = values ? a.v_t : a.k_t;
     run.src = (values ? a.v + head * a.v_h : a.k + head * a.k_h) + from * run.src_t;
@@ -230,26 +235,33 @@ __global__ __launch_bounds__(256) void store8_kernel(Cache8Args a) {
     run.num_slots = a.num_slots;
     run.mask = mask;
     run.per = a.per;
-    run.lane = lane;
+    run.lane = W == 1 ? lane : (int)threadIdx.x;
     float* scale = sc.data + page * sc.page + head * sc.head;
     const float old = begun ? 0.0f : *scale;
-    // lane 0's pieces are the first of each load: the loop is the same for all lanes
     const int64_t pieces = (int64_t)run.count * a.per;
-    const int64_t batches = (pieces + 64 * run.U - 1) / (64 * run.U);
-    typename StoreRun<T, C, N>::At at = run.first();
+    const int64_t batches = (pieces + run.kLanes * run.U - 1) / (run.kLanes * run.U);
+    typename StoreRun<T, C, N, W>::At at = run.first();
     const auto at0 = at;
     uint32_t most = 0;
     for (int64_t b = 0; b < batches; ++b) {
       run.load(at);
       run.raise(most);
     }
-    const float need = bits_f32(unit_bits<C>(wave_magnitude<T>(most)));
+    most = wave_magnitude<T>(most);
+    if constexpr (W > 1) {
+      if (lane == 0) part[parity][wave] = most;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) most = max(most, part[parity][w]);
+    }
+    const float need = bits_f32(unit_bits<C>(most));
     // (a NaN stays, whichever of the two it is)
     const float now = old != old ? old : need != need || need > old ? need : old;
     if (now > old && old > 0.0f) {
       run.rescale(old / now);
       // the new codes go over some of these
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if constexpr (W > 1) __syncthreads();
     }
     const float inverse = inverse_unit(now);
     if (batches == 1) {
@@ -262,7 +274,7 @@ __global__ __launch_bounds__(256) void store8_kernel(Cache8Args a) {
         run.write(here, inverse);
       }
     }
-    if (lane == 0) *scale = now;
+    if (run.lane == 0) *scale = now;
   }
 }
 

@@ -172,7 +172,8 @@ __device__ inline float finish(int32_t sum, const TwoFactors& x, float w, float 
   return y;
 }
 
-template <typename T>
+// WIDE: rows of out begin on 16 bytes and have whole pieces of them.
+template <typename T, bool WIDE>
 struct Linear8Epilogue {
   T* out;
   int64_t ld;
@@ -180,7 +181,6 @@ struct Linear8Epilogue {
   int32_t* planes;     // parts of k: [part][n][pitch], or null
   int32_t pitch;       // of m in a plane, a multiple of 4
   int32_t M, N;
-  bool wide;           // rows of out can be written 16 bytes at a time
 
   static constexpr bool kJoins = false;
   template <int BM, int BN>
@@ -214,6 +214,9 @@ struct Linear8Epilogue {
       }
       return;
     }
+    // rows of 32 values on 8 bytes, and not all in the same banks
+    constexpr int kPitch = 32 + 8 / (int)sizeof(T);
+    __shared__ __align__(16) T stage[WIDE ? 1 : WM * WN][WIDE ? 1 : 16 * kPitch];
     const float* mine = got + wm * TM * 16 + g * 4;
 #pragma unroll
     for (int i = 0; i < TM; i += 2) {
@@ -233,25 +236,37 @@ struct Linear8Epilogue {
 #pragma unroll
           for (int r = 0; r < 4; ++r) y[h][r] = finish(acc[i + h][j][r], sx, sw[h][r], b[h][r]);
         T* to = out + n * ld;
-        if (sizeof(T) == 2 && wide) {
-          if constexpr (sizeof(T) == 2) {
-            const TilePair<T> t(y[0], y[1]);
-            const int m = mb + i * 16 + TilePair<T>::at(g);
-            if (n < N && m < M) t.store(to + m);
-          }
-          continue;
-        }
-        if (n >= N) continue;
+        const int m = mb + i * 16;
+        if constexpr (sizeof(T) == 2 && WIDE) {
+          const TilePair<T> t(y[0], y[1]);
+          const int at = m + TilePair<T>::at(g);
+          if (n < N && at < M) t.store(to + at);
+        } else if constexpr (WIDE) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int m = mb + (i + h) * 16 + g * 4;
-          if (sizeof(T) == 4 && wide) {
-            if (m < M) *reinterpret_cast<f32x4*>(to + m) = y[h];
-          } else {
+          for (int h = 0; h < 2; ++h)
+            if (n < N && m + h * 16 + g * 4 < M)
+              *reinterpret_cast<f32x4*>(to + m + h * 16 + g * 4) = y[h];
+        } else {
+          // Rows that begin anywhere: the tile goes through LDS, so that a store has neighbouring
+          // values of a few rows, not a few of many (8192 x 8191 x 2048 bf16 219 -> 161 us)
+          T* at = stage[wm * WN + wn];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (m + r < M) to[m + r] = (T)y[h][r];
+          for (int h = 0; h < 2; ++h) {
+            typedef T T4 __attribute__((ext_vector_type(4)));
+            T4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = (T)y[h][r];
+            *reinterpret_cast<T4*>(at + c * kPitch + h * 16 + g * 4) = v;
           }
+          __builtin_amdgcn_wave_barrier();
+          const int first = n - c;   // of the tile's 16 rows
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int row = q * 2 + (lane >> 5), mm = lane & 31;
+            const T v = at[row * kPitch + mm];
+            if (first + row < N && m + mm < M) out[(int64_t)(first + row) * ld + m + mm] = v;
+          }
+          __builtin_amdgcn_wave_barrier();
         }
       }
     }
@@ -260,7 +275,8 @@ struct Linear8Epilogue {
 
 // Adds the planes of parts of k (whole numbers: in any order) and finishes the result.
 template <typename T>
-__global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T> ep, int32_t parts) {
+__global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T, false> ep,
+                                                           int32_t parts) {
   const int32_t quads = ep.pitch / 4;
   const int64_t step = (int64_t)gridDim.x * 256, all = (int64_t)ep.N * quads;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {

@@ -373,12 +373,20 @@ void run_linear8(const LinearPlan& p, const ctcpb_lm_linear8_args& g, char* ws, 
   const Operand w =
       codes_of(g.w, g.stride_w, g.features, g.hidden, p.padded, p.pad_w, ws + p.o_w, st);
   constexpr int per = 16 / (int)sizeof(T);
-  Linear8Epilogue<T> ep{static_cast<T*>(g.out), g.stride_out, g.w_scale, g.bias, x_scale, nullptr,
-                        p.pitch, g.features, g.rows, false};
-  ep.wide = g.features % per == 0 && g.stride_out % per == 0 && aligned(g.out, 16);
-  if (p.cut.splits > 1) ep.planes = reinterpret_cast<int32_t*>(ws + p.o_planes);
-  launch_cut<int8_t, true, true>(w, x, p.padded, p.cut, 0, ep, st);
-  if (p.cut.splits > 1) {
+  int32_t* planes = p.cut.splits > 1 ? reinterpret_cast<int32_t*>(ws + p.o_planes) : nullptr;
+  const bool wide = g.features % per == 0 && g.stride_out % per == 0 && aligned(g.out, 16);
+  const auto run = [&](auto ep) {
+    ep = decltype(ep){static_cast<T*>(g.out), g.stride_out, g.w_scale, g.bias, x_scale, planes,
+                      p.pitch, g.features, g.rows};
+    launch_cut<int8_t, true, true>(w, x, p.padded, p.cut, 0, ep, st);
+  };
+  if (wide)
+    run(Linear8Epilogue<T, true>{});
+  else
+    run(Linear8Epilogue<T, false>{});
+  if (planes) {
+    const Linear8Epilogue<T, false> ep{static_cast<T*>(g.out), g.stride_out, g.w_scale, g.bias,
+                                       x_scale, planes, p.pitch, g.features, g.rows};
     const int64_t blocks = ((int64_t)g.rows * (p.pitch / 4) + 255) / 256;
     linear8_join_kernel<T><<<(unsigned)std::min<int64_t>(blocks, 4096), 256, 0, st>>>(ep,
                                                                                       p.cut.splits);
@@ -396,15 +404,26 @@ int ctcpb_lm_cache_store8(const ctcpb_lm_cache8_args* args, void* stream) {
     if (args->tokens == 0) return ok();
     bool wide;
     Cache8Args a = cache8_args(*args, wide);
-    // a wave to each token while that makes no more than some waves to each place on the card
-    const int64_t one = (int64_t)a.tokens * a.heads * 2;
-    a.chunk = one <= 1 << 16 ? 1 : 16;
-    const int64_t blocks = ((int64_t)ceil_div(a.tokens, a.chunk) * a.heads * 2 + 3) / 4;
+    // A wave to each token while that makes no more than some waves to each place on the card, else
+    // as many as hold the values of a page in registers, to as many tokens
+    const int64_t one = (int64_t)a.tokens * a.heads * 2, pieces = (int64_t)args->page_size * a.per;
+    const bool many = one > 1 << 16;
+    const int waves = !many || pieces <= 64 * kStoreHeld ? 1 : pieces <= 128 * kStoreHeld ? 2 : 4;
+    a.chunk = !many ? 1 : std::min(std::max(args->page_size, 16), 64);
+    const int64_t units = (int64_t)ceil_div(a.tokens, a.chunk) * a.heads * 2;
+    const int64_t blocks = waves == 1 ? (units + 3) / 4 : units;
     if (blocks > INT_MAX) return fail(CTCPB_ERR_UNSUPPORTED, "too many tokens for one launch");
     hipStream_t st = static_cast<hipStream_t>(stream);
     for_types(args->dtype, args->code, wide, [&](auto t, auto c, auto n) {
-      store8_kernel<decltype(t), decltype(c), decltype(n)::value>
-          <<<(unsigned)blocks, 256, 0, st>>>(a);
+      typedef decltype(t) T;
+      typedef decltype(c) C;
+      constexpr int N = decltype(n)::value;
+      if (waves == 1)
+        store8_kernel<T, C, N, 1><<<(unsigned)blocks, 256, 0, st>>>(a);
+      else if (waves == 2)
+        store8_kernel<T, C, N, 2><<<(unsigned)blocks, 128, 0, st>>>(a);
+      else
+        store8_kernel<T, C, N, 4><<<(unsigned)blocks, 256, 0, st>>>(a);
     });
     return launched("store8_kernel");
   });

@@ -201,6 +201,26 @@ def test_many_tokens():
           *cache(pages, 16, 2, 64, torch.int8, seed=1))
 
 
+@pytest.mark.parametrize("page,D,dtype,code", [
+    (32, 128, torch.bfloat16, torch.int8), (64, 128, torch.float16, torch.float8_e4m3fn),
+    (16, 128, torch.float32, torch.int8), (256, 64, torch.bfloat16, torch.float8_e4m3fn),
+    (256, 256, torch.float32, torch.int8), (32, 20, torch.bfloat16, torch.int8),
+    (64, 36, torch.float32, torch.float8_e4m3fn), (128, 13, torch.float16, torch.int8)])
+def test_many_tokens_in_larger_pages(page, D, dtype, code):
+    """Pages whose values take several waves' registers, or more; begun, gone on with and filled
+    over in one call, among single tokens and tokens without a slot."""
+    H = 40
+    g = torch.Generator().manual_seed(page + D)
+    counts = torch.randint(0, 130, (12,), generator=g).tolist() + [1] * 9
+    held = torch.randint(0, page, (21,), generator=g).tolist()
+    slots, pages = slots_of(counts, held, page)
+    slots[torch.rand(slots.numel(), generator=g) < 0.05] = -1
+    assert slots.numel() * H * 2 > 1 << 16   # not a wave to each token
+    x, y = random(slots, H, D, dtype)
+    check(x, y, slots.cuda(), *cache(pages, page, H, D, code, "htd"),
+          *cache(pages, page, H, D, code, "thd", seed=1))
+
+
 def test_no_tokens_and_a_stream_of_its_own():
     kc, ks = cache(3, 16, 2, 64, torch.int8)
     vc, vs = cache(3, 16, 2, 64, torch.int8)
