@@ -209,7 +209,7 @@ def test_many_tokens():
 def test_many_tokens_in_larger_pages(page, D, dtype, code):
     """Pages whose values take several waves' registers, or more; begun, gone on with and filled
     over in one call, among single tokens and tokens without a slot."""
-    H = 40
+    H = 60
     g = torch.Generator().manual_seed(page + D)
     counts = torch.randint(0, 130, (12,), generator=g).tolist() + [1] * 9
     held = torch.randint(0, page, (21,), generator=g).tolist()
