@@ -37,6 +37,12 @@ __device__ inline float inverse_unit(float u) {
   return u >= bits_f32(1u << 23) && u < bits_f32(kInfBits) ? 1.0f / u : 0.0f;
 }
 
+// The low bytes of four words.
+__device__ inline uint32_t low_bytes(float a, float b, float c, float d) {
+  const uint32_t lo = __builtin_amdgcn_perm(f32_bits(b), f32_bits(a), 0x0c0c0400u);
+  return lo | __builtin_amdgcn_perm(f32_bits(d), f32_bits(c), 0x04000c0cu);
+}
+
 struct Int8 {
   static constexpr uint32_t kTopFraction = 0x7e0000u;   // 127 = 1.984375 * 2^6
   static constexpr int kTopExponent = 6;
@@ -45,9 +51,7 @@ struct Int8 {
   // 1.5 * 2^23 leaves them in the low bits.
   static __device__ uint32_t round4(float a, float b, float c, float d) {
     constexpr float M = 12582912.0f;
-    const uint32_t lo = __builtin_amdgcn_perm(f32_bits(b + M), f32_bits(a + M), 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(f32_bits(d + M), f32_bits(c + M), 0x04000c0cu);
-    return lo | hi;
+    return low_bytes(a + M, b + M, c + M, d + M);
   }
   static __device__ void values4(uint32_t w, float (&v)[4]) {
 #pragma unroll

@@ -25,47 +25,6 @@ struct QuantArgs {
   int32_t per;            // pieces of a row
 };
 
-// Codes of N values: times `up` (a power of two), then over `unit`.
-template <typename T, int N>
-__device__ inline void quantize_piece(const Values<T, N>& x, float up, float unit, float inverse,
-                                      int8_t* to) {
-  constexpr float M = 12582912.0f;   // 1.5 * 2^23: sums with it are whole
-  float v[N], n[N];
-  bool near = false;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = x.at(i) * up;
-    n[i] = __builtin_fmaf(v[i], inverse, M) - M;
-    near = near || fabsf(__builtin_fmaf(v[i], inverse, -n[i])) > 0.4999f;
-  }
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      // what is left of v: exact where it matters, a multiple of half the unit's last bit
-      const float left = __builtin_fmaf(-n[i], unit, v[i]), half = 0.5f * unit;
-      const bool odd = (int)n[i] & 1;
-      if (left > half || (left == half && odd))
-        n[i] += 1.0f;
-      else if (left < -half || (left == -half && odd))
-        n[i] -= 1.0f;
-    }
-  }
-  uint32_t w[N > 4 ? N / 4 : 1];
-#pragma unroll
-  for (int i = 0; i < N; ++i) n[i] = fminf(fmaxf(n[i], -127.0f), 127.0f);
-  if constexpr (N == 1) {
-    *to = (int8_t)(int)n[0];
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-      w[i] = Int8::round4(n[4 * i], n[4 * i + 1], n[4 * i + 2], n[4 * i + 3]);
-    if constexpr (N == 8)
-      *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
-    else
-      *reinterpret_cast<uint32_t*>(to) = w[0];
-  }
-}
-
 // What a row's largest magnitude (as bits) makes of it.
 struct RowScale {
   float scale, up, unit, inverse;
@@ -80,6 +39,54 @@ struct RowScale {
     inverse = some ? 1.0f / unit : 0.0f;
   }
 };
+
+// Codes of N values of a row.  1.5 * 2^23 added to a quotient leaves its nearest whole number in
+// the sum's low bits, which are the code.  The reciprocal puts a quotient on the wrong side of a half
+// only where it is within 2^-16 of one: then what is left of the value tells.
+template <typename T, int N>
+__device__ inline void quantize_piece(const Values<T, N>& x, const RowScale& r, int8_t* to) {
+  constexpr float M = 12582912.0f;
+  float v[N], y[N], most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = x.at(i);
+  const bool small = r.up != 1.0f;   // the same for the whole row
+  if (small) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= r.up;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    y[i] = __builtin_fmaf(v[i], r.inverse, M);
+    most = fmaxf(most, fabsf(__builtin_fmaf(v[i], r.inverse, M - y[i])));
+  }
+  if (most > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      // what is left of v: exact where it matters, a multiple of half the unit's last bit
+      const float n = y[i] - M, left = __builtin_fmaf(-n, r.unit, v[i]), half = 0.5f * r.unit;
+      const bool odd = (int)n & 1;
+      if (left > half || (left == half && odd))
+        y[i] += 1.0f;
+      else if (left < -half || (left == -half && odd))
+        y[i] -= 1.0f;
+    }
+  }
+  if (small) {   // a subnormal scale may be much less than 1/127 of the largest value
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = fminf(fmaxf(y[i], M - 127.0f), M + 127.0f);
+  }
+  if constexpr (N == 1) {
+    *to = (int8_t)f32_bits(y[0]);
+  } else {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = low_bytes(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    if constexpr (N == 8)
+      *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+    else
+      *reinterpret_cast<uint32_t*>(to) = w[0];
+  }
+}
 
 // A row's pieces lane, lane + LANES, .. : their largest magnitude, of which a caller with several
 // waves to a row makes the row's.  The last kQuantHeld of them are kept for write().
@@ -122,7 +129,7 @@ struct RowPieces {
 #pragma unroll
           for (uint32_t& w : held[u].w) w = 0;
         }
-        quantize_piece<T, N>(held[u], r.up, r.unit, r.inverse, codes + p * N);
+        quantize_piece<T, N>(held[u], r, codes + p * N);
       }
   }
 };
@@ -303,7 +310,7 @@ __global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T, fa
 // its own).  Then KW waves share the k of a tile of 16 channels, 16 / KW tiles at a time; the next
 // tiles' first weights are on their way while the waves' sums are added.  Weights go from
 // memory straight into the registers of the matrix instruction, kFewHeld of them a lane at a time.
-constexpr int32_t kFewValues = 8192, kFewCodes = 131072;
+constexpr int32_t kFewValues = 16384, kFewCodes = 131072;
 constexpr int kFewHeld = 8;
 constexpr int kFewPieces = 256;   // of a row that is quantised here
 
@@ -321,12 +328,12 @@ struct FewArgs {
   int32_t per;             // pieces of a row of x
 };
 
-// Codes and scales of rows first, first + step, .. below a.rows, several of them at a time: P pieces a
-// lane to each, and 8 / P rows, so that their loads and reductions overlap.
+// Codes and scales of rows first, first + step, .. below a.rows (up to 32 rows over 16 waves: two at
+// a time, whose loads and reductions overlap), P pieces a lane to each.
 template <typename X, int N, int P>
 __device__ inline void quantize_few(const FewArgs& a, int first, int step, int lane, int8_t* codes,
                                     int pitch, float* sx) {
-  constexpr int R = kQuantHeld / P;
+  constexpr int R = 2;
   for (int n0 = first; n0 < a.rows; n0 += R * step) {
     Values<X, N> held[R][P];
     uint32_t most[R];
@@ -366,8 +373,7 @@ __device__ inline void quantize_few(const FewArgs& a, int first, int step, int l
             for (uint32_t& w : held[r][p].w) w = 0;
           }
           if (p * 64 + lane < a.per)
-            quantize_piece<X, N>(held[r][p], q.up, q.unit, q.inverse,
-                                 codes + n * pitch + (p * 64 + lane) * N);
+            quantize_piece<X, N>(held[r][p], q, codes + n * pitch + (p * 64 + lane) * N);
         }
       }
     }

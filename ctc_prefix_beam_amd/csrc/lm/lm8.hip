@@ -214,18 +214,20 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   // there, w may have anything.
   p.pad_x = !p.quantize && (g.hidden % 16 != 0 || !codes_aligned(g.x, g.stride_x));
   p.pad_w = (g.hidden % 16 != 0 && !readable) || !codes_aligned(g.w, g.stride_w);
-  // In us, one launch for few rows of codes / the product's tiles: 5000 channels of 512 6.4 and 7.0
-  // for a row, 8.1 and 7.2 for 32; 2048 of 2048 6.6 and 10.6, 7.6 and 10.4; 8192 of 2048 8.4 and
-  // 13.4, 10.5 and 15.8; 50000 of 2048 22.8 and 23.6, 32 and 25.  With x quantised there / before it:
-  // 16 rows of 512 10.6 and 10.9, 4 of 2048 9.5 and 10.8, 16 of 2048 11.7 and 11.0.
+  // In us, one launch for few rows of codes / the product's tiles: 5000 channels of 512 6.6 and 7.0
+  // for a row, 8.3 and 7.1 for 32; 2048 of 2048 6.6 and 10.6, 8.0 and 10.4; 8192 of 2048 9.5 and 13.4,
+  // 10.8 and 15.8; 50000 of 2048 22.8 and 23.6, 32 and 25.  With x quantised there / before it: 16 rows
+  // of 512 8.6 and 10.6, 32 10.8 and 10.9 (and a launch less), 16 of 1024 10.5 and 11.5, 8 of 2048
+  // 10.0 and 10.8, 16 of them 11.3 and 11.0.
   const int64_t values = (int64_t)g.rows * up(p.padded, 64);
-  p.few = g.rows <= (p.padded >= 1024 ? 32 : 16) && values <= kFewCodes && !p.pad_w &&
+  const int per = 16 / elem_size(g.dtype);
+  const bool pieces = g.hidden <= kFewPieces * (g.hidden % per || !rows_aligned(g) ? 1 : per);
+  const bool there = p.quantize && values <= kFewValues && pieces;   // quantised by the same launch
+  p.few = g.rows <= (there || p.padded >= 1024 ? 32 : 16) && values <= kFewCodes && !p.pad_w &&
           g.features <= 64 * kCUs;
   if (p.few) {
     p.pad_x = false;
-    const int per = 16 / elem_size(g.dtype);
-    const bool pieces = g.hidden <= kFewPieces * (g.hidden % per || !rows_aligned(g) ? 1 : per);
-    p.quantize = p.quantize && (values > kFewValues || !pieces);
+    p.quantize = p.quantize && !there;
   } else {
     p.cut = choose_cut(1, g.features, g.rows, p.padded, true);
   }
