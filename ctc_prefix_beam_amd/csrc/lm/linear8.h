@@ -310,7 +310,8 @@ __global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T, fa
 // its own).  Then KW waves share the k of a tile of 16 channels, 16 / KW tiles at a time; the next
 // tiles' first weights are on their way while the waves' sums are added.  Weights go from
 // memory straight into the registers of the matrix instruction, kFewHeld of them a lane at a time.
-constexpr int32_t kFewValues = 16384, kFewCodes = 131072;
+constexpr int32_t kFewValues = 16384;
+constexpr int32_t kFewCodes = 124 * 1024;   // of a CU's 160 KB of LDS; the waves' sums take 32 KB
 constexpr int kFewHeld = 8;
 constexpr int kFewPieces = 256;   // of a row that is quantised here
 

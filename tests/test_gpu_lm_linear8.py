@@ -117,7 +117,7 @@ def test_sizes(dtype, N, M, H):
     (1, 1, 1), (1, 100, 32768), (1, 50000, 40), (2, 77, 16000), (4, 129, 8192), (5, 33, 5003),
     (16, 20000, 64), (16, 48, 2048), (17, 1000, 100), (31, 333, 1000), (32, 5000, 512),
     (32, 65, 1024), (32, 65, 1025),
-    (32, 4100, 4000), (32, 4111, 2048), (20, 50, 6553), (3, 300, 43000)])
+    (32, 4100, 4000), (31, 60, 4096), (32, 60, 4096), (3, 60, 42000), (32, 4111, 2048), (20, 50, 6553), (3, 300, 43000)])
 def test_few_rows(dtype, N, M, H):
     """Rows on both sides of what one launch does, with weights in rows that can be read past
     their ends, where anything may lie; as values and as codes."""
