@@ -5,7 +5,7 @@
 // is read is half of a 16-bit cache, so what each value costs beside its load counts twice:
 //
 // - Both products are f16 ones.  Every code is an f16 value (of whole numbers, 1/512 of it), so
-//   the cache enters them without a rounding; widening a pair costs 1 or 2.5 instructions.
+//   the cache enters them without a rounding; widening a pair costs 1 (e4m3) or 2.5 instructions.
 // - q enters as f16 too.  bf16 and f32 ones are first multiplied by the power of two that takes
 //   the largest of the head to 2^14 .. 2^15: what of a bf16 value is then lost lies 2^-39 below the
 //   largest, less than its float32 product's rounding.  f32 ones are the sum of two f16 values.
@@ -17,9 +17,23 @@
 //   (`top`, which shrinks as m grows) to 2^14 .. 2^15, so that pages of very different scales, and
 //   long tails, keep their digits.  The sums acc carry the same factor.
 //
-// Layout of a tile of 32 tokens: as for 16-bit types, but a lane (g, c) has 16 bytes of a key's row at
-// d = 64 k + 16 g (which two k-steps of the product take in that order, q alike) and, of the
-// values of tokens 8g .. 8g+7, DP / 16 bytes at d = c DP / 16.
+// - A wave looks pages and scales up for eight tiles at a time, well before it needs them; what
+//   is left to a tile is one multiplication for each group of four tokens' address.  With a
+//   lookup for each tile, and addresses multiplied out in 64 bits, 4096 requests of up to 512
+//   tokens took 155 us, not 131.
+//
+// What bounds it, measured: memory.  256 requests of 1..4095 tokens, 32 query and 8 key/value
+// heads of 128, int8, bf16: 1.08 GB in 209 us, 5.2 TB/s (a copy: 5.0; 16-bit caches 420 us), the
+// matrix units busy in 11 % of the cycles; three requests of up to 131071 tokens, e4m3: 604 MB in
+// 119 us, 5.1 TB/s; 4096 requests of up to 512 tokens, 4 heads of 64, e4m3, f16: 542 MB in 131 us
+// token by token and 121 head by head (full rows: 5.1 TB/s; the rest is the start and end of
+// short ones).  Four waves a SIMD for heads of 128 spill (302 us for the 256 requests), five for
+// heads of 64 too (156 for the 4096); two sets of registers for tiles, to fetch two ahead, leave
+// two waves and take 225.
+//
+// Layout of a tile of 32 tokens: as for 16-bit types, but a lane (g, c) has 16 bytes of a key's
+// row at d = 64 k + 16 g (which two k-steps of the product take in that order, q alike) and, of
+// the values of tokens 8g .. 8g+7, DP / 16 bytes at d = c DP / 16.
 #pragma once
 #include <type_traits>
 
@@ -180,12 +194,13 @@ struct Tile8 {
       for (int i = 0; i < 8; ++i) x[k][i] = (T)0.0f;
       if (live && d < a.D) {
         if (a.wide_q) {
-          typedef T TN __attribute__((ext_vector_type(16 / sizeof(T))));
+          constexpr int M = 16 / (int)sizeof(T);
+          typedef T TM __attribute__((ext_vector_type(M)));
 #pragma unroll
-          for (int v = 0; v < (int)sizeof(T) / 2; ++v) {
-            const TN y = reinterpret_cast<const TN*>(src + d)[v];
+          for (int v = 0; v < 8 / M; ++v) {
+            const TM y = reinterpret_cast<const TM*>(src + d)[v];
 #pragma unroll
-            for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[k][v * (16 / (int)sizeof(T)) + i] = y[i];
+            for (int i = 0; i < M; ++i) x[k][v * M + i] = y[i];
           }
         } else {
 #pragma unroll

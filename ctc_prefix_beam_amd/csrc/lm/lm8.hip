@@ -214,11 +214,11 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   // there, w may have anything.
   p.pad_x = !p.quantize && (g.hidden % 16 != 0 || !codes_aligned(g.x, g.stride_x));
   p.pad_w = (g.hidden % 16 != 0 && !readable) || !codes_aligned(g.w, g.stride_w);
-  // In us, one launch for few rows of codes / the product's tiles: 5000 channels of 512 6.6 and 7.0
-  // for a row, 8.3 and 7.1 for 32; 2048 of 2048 6.6 and 10.6, 8.0 and 10.4; 8192 of 2048 9.5 and 13.4,
-  // 10.8 and 15.8; 50000 of 2048 22.8 and 23.6, 32 and 25.  With x quantised there / before it: 16 rows
-  // of 512 8.6 and 10.6, 32 10.8 and 10.9 (and a launch less), 16 of 1024 10.5 and 11.5, 8 of 2048
-  // 10.0 and 10.8, 16 of them 11.3 and 11.0.
+  // In us, one launch for few rows of codes / the product's tiles: 5000 channels of 512 6.6 and
+  // 7.0 for a row, 8.3 and 7.1 for 32; 2048 of 2048 6.6 and 10.6, 8.0 and 10.4; 8192 of 2048 9.5
+  // and 13.4, 10.8 and 15.8; 50000 of 2048 22.8 and 23.6, 32 and 25.  With x quantised there /
+  // before it: 16 rows of 512 8.6 and 10.6, 32 10.8 and 10.9 (and a launch less), 16 of 1024 10.5
+  // and 11.5, 8 of 2048 10.0 and 10.8, 16 of them 11.3 and 11.0.
   const int64_t values = (int64_t)g.rows * up(p.padded, 64);
   const int per = 16 / elem_size(g.dtype);
   const bool pieces = g.hidden <= kFewPieces * (g.hidden % per || !rows_aligned(g) ? 1 : per);
@@ -319,8 +319,8 @@ void launch_few(const FewArgs& a, hipStream_t st) {
     launch_with_lds(linear8_few_kernel<T, X, N, NT, 16>, (unsigned)std::min(tiles, kCUs), 1024, lds,
                     a, st);
   else
-    launch_with_lds(linear8_few_kernel<T, X, N, NT, 4>, (unsigned)std::min(ceil_div(tiles, 4), kCUs),
-                    1024, lds, a, st);
+    launch_with_lds(linear8_few_kernel<T, X, N, NT, 4>,
+                    (unsigned)std::min(ceil_div(tiles, 4), kCUs), 1024, lds, a, st);
 }
 
 template <typename T, typename X, int N>
@@ -475,8 +475,9 @@ int ctcpb_lm_attention8(const ctcpb_lm_attention8_args* args, void* workspace,
     if (g.rows == 0) return ok();
     a.ks = view(args->k_scale);
     a.vs = view(args->v_scale);
-    const int64_t page = std::max(std::max(a.kc.page, a.vc.page), 4 * std::max(a.ks.page, a.vs.page));
-    if (page > UINT32_MAX || std::max(a.kc.token, a.vc.token) > 1 << 23)
+    if (std::max(a.kc.page, a.vc.page) > UINT32_MAX ||
+        std::max(a.ks.page, a.vs.page) > UINT32_MAX / 4 ||
+        std::max(a.kc.token, a.vc.token) > 1 << 23)
       return fail(CTCPB_ERR_UNSUPPORTED, "pages 4 GiB apart, or tokens of a page more than 8 MiB");
     a.k_page = (uint32_t)a.kc.page;
     a.v_page = (uint32_t)a.vc.page;

@@ -529,8 +529,8 @@ def cache_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloat16,
     both = empty((2, T, H, D), dtype=dtype, device=slots.device)
     at = both.data_ptr()
     _check(lib().ctcpb_lm_cache_load8(_pack(
-        _CACHE8, at, at + both.stride(0) * both.element_size(), slots.data_ptr(), H * D, D, H * D, D,
-        *caches, *scales, dt, code, T, pages, page_size, H, D), raw))
+        _CACHE8, at, at + T * H * D * dtype.itemsize, slots.data_ptr(), H * D, D, H * D, D, *caches,
+        *scales, dt, code, T, pages, page_size, H, D), raw))
     return both.unbind(0)
 
 
@@ -654,8 +654,8 @@ def linear8(x, w, w_scale, bias=None, x_scale=None, dtype=None, out=None, stream
         _like(out, dev, "out", dtype, (N, M))
     so, _, _ = _matrix(out, "out")
     _apart(out, out.stride(), "out")
-    args = _pack(_LINEAR8, x.data_ptr(), _ptr(x_scale), w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
-                 out.data_ptr(), sx, sw, so, xt, dt, N, M, H, flags)
+    args = _pack(_LINEAR8, x.data_ptr(), _ptr(x_scale), w.data_ptr(), w_scale.data_ptr(),
+                 _ptr(bias), out.data_ptr(), sx, sw, so, xt, dt, N, M, H, flags)
     need = ctypes.c_size_t()
     _check(L.ctcpb_lm_linear8_workspace(args, need))
     size = need.value

@@ -181,8 +181,8 @@ typedef struct {
  * old is 0 where a token goes to the page's slot 0, which begins the page anew (its
  * other slots then hold nothing), else the page's scale, which has to have been
  * set.  Codes of a page whose scale grows are multiplied by old / new and rounded
- * again, which with scales from here leaves them less than one step off their value (e4m3: half a step
- * as ever, and less than one of the smallest codes').  A value that is not finite
+ * again, which with scales from here leaves them less than one step off their value
+ * (e4m3: half a step as ever, and less than one of the smallest codes).  A value that is not finite
  * makes the scale NaN, which the page keeps until it begins anew.
  *   k, v     device, typed: element (t, head, d) at t*stride_t + head*stride_h + d;
  *            read by the store, written by the load (code * scale, rounded)
@@ -209,7 +209,8 @@ int ctcpb_lm_cache_load8(const ctcpb_lm_cache8_args* args, void* stream);
  * scale: `base` as there (its dtype that of q and out, its caches' strides in codes), but
  * head_dim is a multiple of 16.  Scales are any finite numbers >= 0.  Codes and scales of slots
  * past a row's length, or before its window in another page, are never used, whatever
- * they hold.  Nothing is rounded on the way to fewer than 22 bits. */
+ * they hold.  Nothing is rounded on the way to fewer than 22 bits.  Pages lie less than
+ * 4 GiB apart (their scales too), tokens of a page up to 8 MiB. */
 typedef struct {
   ctcpb_lm_attention_args base;
   ctcpb_lm_scales k_scale, v_scale;

@@ -66,7 +66,9 @@ def attend(L, dtype=0, code=0, q=P, sr=128, sh=64, kc=cache(), vc=cache(), ks=sc
     (dict(vc=cache(0)), 1), (dict(kc=cache(264)), 1), (dict(vc=cache(token=72)), 1),
     (dict(ks=scales(0)), 1), (dict(vs=scales(0)), 1), (dict(vs=scales(page=-2)), 1),
     (dict(width=4096, stride=4096, ws=N), 1), (dict(width=4096, stride=4096, ws_bytes=16), 2),
-    (dict(rows=1 << 30, Hq=64, Hkv=64), 3)])
+    (dict(rows=1 << 30, Hq=64, Hkv=64), 3), (dict(kc=cache(page=1 << 32)), 3),
+    (dict(vc=cache(token=(1 << 23) + 16)), 3), (dict(ks=scales(page=1 << 30)), 3),
+    (dict(vs=scales(page=1 << 62)), 3)])
 def test_attention_refusals(L, kw, code):
     assert attend(L, **kw) == code
     assert L.ctcpb_lm_last_error().decode() != ""
