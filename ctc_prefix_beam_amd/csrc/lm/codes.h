@@ -141,6 +141,26 @@ struct Values {
     }
   }
 
+  // The same from an address that is a multiple of a value's size only; `count` of them, then
+  // zeros.
+  __device__ void load_some(const void* p, int count) {
+    if (count >= N) {
+      __builtin_memcpy(w, p, sizeof(w));
+      return;
+    }
+#pragma unroll
+    for (uint32_t& x : w) x = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i < count) {
+        if constexpr (sizeof(T) == 2)
+          w[i / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[i] << (i % 2 * 16);
+        else
+          w[i] = static_cast<const uint32_t*>(p)[i];
+      }
+    }
+  }
+
   // Raises `most`, which holds magnitudes as bits: two 16-bit ones, or one of 32.  As whole
   // numbers they order as the values do, infinities and NaN above all.
   __device__ void raise(uint32_t& most) const {

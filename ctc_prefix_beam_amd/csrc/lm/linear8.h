@@ -43,8 +43,10 @@ struct RowScale {
 // Codes of N values of a row.  1.5 * 2^23 added to a quotient leaves its nearest whole number in
 // the sum's low bits, which are the code.  The reciprocal puts a quotient on the wrong side of a
 // half only where it is within 2^-16 of one: then what is left of the value tells.
-template <typename T, int N>
-__device__ inline void quantize_piece(const Values<T, N>& x, const RowScale& r, int8_t* to) {
+// ANY: `count` of them are there, and `to` may be any address.
+template <typename T, int N, bool ANY>
+__device__ inline void quantize_piece(const Values<T, N>& x, const RowScale& r, int8_t* to,
+                                      int count) {
   constexpr float M = 12582912.0f;
   float v[N], y[N], most = 0.0f;
 #pragma unroll
@@ -75,36 +77,52 @@ __device__ inline void quantize_piece(const Values<T, N>& x, const RowScale& r, 
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = fminf(fmaxf(y[i], M - 127.0f), M + 127.0f);
   }
-  if constexpr (N == 1) {
-    *to = (int8_t)f32_bits(y[0]);
-  } else {
-    uint32_t w[N / 4];
+  uint32_t w[N / 4];
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-      w[i] = low_bytes(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    if constexpr (N == 8)
-      *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
-    else
-      *reinterpret_cast<uint32_t*>(to) = w[0];
+  for (int i = 0; i < N / 4; ++i)
+    w[i] = low_bytes(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+  if constexpr (ANY) {
+    if (count >= N) {
+      __builtin_memcpy(to, w, N);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < count) to[i] = (int8_t)(w[i / 4] >> (i % 4 * 8));
+    }
+  } else if constexpr (N == 8) {
+    *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+  } else {
+    *reinterpret_cast<uint32_t*>(to) = w[0];
   }
 }
 
+// Values of piece p of a row of `hidden`.
+template <bool ANY, typename T, int N>
+__device__ inline void load_piece(Values<T, N>& v, const char* x, int32_t p, int32_t hidden) {
+  const char* at = x + (int64_t)p * (N * (int)sizeof(T));
+  if constexpr (ANY)
+    v.load_some(at, hidden - p * N);
+  else
+    v.load(at);
+}
+
 // A row's pieces lane, lane + LANES, .. : their largest magnitude, of which a caller with several
-// waves to a row makes the row's.  The last kQuantHeld of them are kept for write().
+// waves to a row makes the row's.  The last kQuantHeld of them are kept for write().  ANY: rows
+// begin on a value's size only, and the last piece may not be whole.
 constexpr int kQuantHeld = 8;
-template <typename T, int N, int LANES>
+template <typename T, int N, bool ANY, int LANES>
 struct RowPieces {
   static constexpr int U = kQuantHeld;
   Values<T, N> held[U];
 
-  __device__ uint32_t largest(const char* x, int32_t per, int lane) {
+  __device__ uint32_t largest(const char* x, int32_t hidden, int32_t per, int lane) {
     uint32_t most = 0;
     for (int32_t p0 = 0; p0 < per; p0 += U * LANES) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int32_t p = p0 + u * LANES + lane;
         if (p < per) {
-          held[u].load(x + (int64_t)p * (N * (int)sizeof(T)));
+          load_piece<ANY>(held[u], x, p, hidden);
         } else {
 #pragma unroll
           for (uint32_t& w : held[u].w) w = 0;
@@ -118,27 +136,29 @@ struct RowPieces {
     return most;
   }
 
-  __device__ void write(const char* x, int32_t per, int lane, const RowScale& r, int8_t* codes) {
+  __device__ void write(const char* x, int32_t hidden, int32_t per, int lane, const RowScale& r,
+                        int8_t* codes) {
     const bool again = per > U * LANES;
     for (int32_t p0 = 0; p0 < per; p0 += U * LANES)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int32_t p = p0 + u * LANES + lane;
         if (p >= per) continue;
-        if (again) held[u].load(x + (int64_t)p * (N * (int)sizeof(T)));
+        if (again) load_piece<ANY>(held[u], x, p, hidden);
         if (!r.some) {
 #pragma unroll
           for (uint32_t& w : held[u].w) w = 0;
         }
-        quantize_piece<T, N>(held[u], r, codes + p * N);
+        quantize_piece<T, N, ANY>(held[u], r, codes + p * N, hidden - p * N);
       }
   }
 };
 
 // W waves to a row: one, and four rows to a workgroup, or four.  Bound by memory: 20000 rows of
 // 4096 f16 51 us, 4.8 TB/s; 8192 of 2048 bf16 16 us, of which moving the 50 MB takes 10; 875 of
-// 387 f32, which are not aligned and go value by value, 3.8 us.
-template <typename T, int N, int W>
+// 387 f32 3.9 us.  Pieces that begin anywhere (ANY): 4000 rows of 2047 bf16 14.5 us a call, 20.4
+// value by value.
+template <typename T, int N, bool ANY, int W>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
   constexpr int kLanes = 64 * W;
   __shared__ uint32_t part[4];
@@ -147,8 +167,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
   if (row >= a.rows) return;   // (of W = 4, no workgroup)
   const int lane = threadIdx.x % kLanes;
   const char* x = a.x + row * a.x_row;
-  RowPieces<T, N, kLanes> pieces;
-  uint32_t most = pieces.largest(x, a.per, lane);
+  RowPieces<T, N, ANY, kLanes> pieces;
+  uint32_t most = pieces.largest(x, a.hidden, a.per, lane);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) part[wave] = most;
     __syncthreads();
@@ -158,7 +178,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
   const RowScale r(most);
   if (lane == 0) a.scales[row] = r.scale;
   int8_t* codes = a.codes + row * a.codes_row;
-  pieces.write(x, a.per, lane, r, codes);
+  pieces.write(x, a.hidden, a.per, lane, r, codes);
   for (int32_t k = a.hidden + lane; k < a.padded; k += kLanes) codes[k] = 0;
 }
 
@@ -343,7 +363,7 @@ struct FewArgs {
 
 // Codes and scales of rows first, first + step, .. below a.rows (up to 32 rows over 16 waves: two
 // at a time, whose loads and reductions overlap), P pieces a lane to each.
-template <typename X, int N, int P>
+template <typename X, int N, bool ANY, int P>
 __device__ inline void quantize_few(const FewArgs& a, int first, int step, int lane, int8_t* codes,
                                     int pitch, float* sx) {
   constexpr int R = 2;
@@ -356,7 +376,7 @@ __device__ inline void quantize_few(const FewArgs& a, int first, int step, int l
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         if (p * 64 + lane < a.per) {
-          held[r][p].load(a.x + n * a.x_row + (p * 64 + lane) * (N * (int)sizeof(X)));
+          load_piece<ANY>(held[r][p], a.x + n * a.x_row, p * 64 + lane, a.hidden);
         } else {
 #pragma unroll
           for (uint32_t& w : held[r][p].w) w = 0;
@@ -386,17 +406,18 @@ __device__ inline void quantize_few(const FewArgs& a, int first, int step, int l
             for (uint32_t& w : held[r][p].w) w = 0;
           }
           if (p * 64 + lane < a.per)
-            quantize_piece<X, N>(held[r][p], q, codes + n * pitch + (p * 64 + lane) * N);
+            quantize_piece<X, N, ANY>(held[r][p], q, codes + n * pitch + (p * 64 + lane) * N,
+                                      a.hidden - (p * 64 + lane) * N);
         }
       }
     }
   }
 }
 
-// X: type of x (int8_t: codes), N: its values to a piece; KW: 4, or 16 for few channels.
-template <typename T, typename X, int N, int NT, int KW>
+// X: type of x (int8_t: codes), of which a piece of N is 16 bytes; KW: 4, or 16 for few channels.
+template <typename T, typename X, bool ANY, int NT, int KW>
 __global__ __launch_bounds__(1024) void linear8_few_kernel(FewArgs a) {
-  constexpr int U = kFewHeld, G = 16 / KW;
+  constexpr int U = kFewHeld, G = 16 / KW, N = 16 / (int)sizeof(X);
   extern __shared__ __align__(16) char few_lds[];
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -425,19 +446,24 @@ __global__ __launch_bounds__(1024) void linear8_few_kernel(FewArgs a) {
       const char* x = a.x + n * a.x_row;
 #pragma unroll 4
       for (int p = lane; p < a.per; p += 64) {
-        if constexpr (N == 16)
-          reinterpret_cast<u32x4*>(codes + n * pitch)[p] = reinterpret_cast<const u32x4*>(x)[p];
-        else
-          codes[n * pitch + p] = static_cast<int8_t>(x[p]);
+        int8_t* to = codes + n * pitch + p * N;
+        if constexpr (ANY) {
+          if (a.hidden - p * N >= N)
+            __builtin_memcpy(to, x + p * N, N);
+          else
+            for (int k = p * N; k < a.hidden; ++k) codes[n * pitch + k] = (int8_t)x[k];
+        } else {
+          *reinterpret_cast<u32x4*>(to) = reinterpret_cast<const u32x4*>(x)[p];
+        }
       }
       if (lane == 0) sx[n] = a.x_scale[n];
     }
   } else if (a.per <= 64) {
-    quantize_few<X, N, 1>(a, wave, 16, lane, codes, pitch, sx);
+    quantize_few<X, N, ANY, 1>(a, wave, 16, lane, codes, pitch, sx);
   } else if (a.per <= 128) {
-    quantize_few<X, N, 2>(a, wave, 16, lane, codes, pitch, sx);
+    quantize_few<X, N, ANY, 2>(a, wave, 16, lane, codes, pitch, sx);
   } else {
-    quantize_few<X, N, 4>(a, wave, 16, lane, codes, pitch, sx);
+    quantize_few<X, N, ANY, 4>(a, wave, 16, lane, codes, pitch, sx);
   }
   for (int n = wave; n < a.rows; n += 16)
     for (int k = a.hidden + lane; k < steps * 64; k += 64) codes[n * pitch + k] = 0;

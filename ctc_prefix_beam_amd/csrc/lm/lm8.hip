@@ -200,11 +200,6 @@ bool codes_aligned(const void* p, int64_t stride) {
   return aligned(p, 16) && stride % 16 == 0 && stride <= 1 << 23;
 }
 
-// Whether rows of values begin on 16 bytes.
-bool rows_aligned(const ctcpb_lm_linear8_args& g) {
-  return aligned(g.x, 16) && g.stride_x * elem_size(g.dtype) % 16 == 0;
-}
-
 LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   LinearPlan p{};
   const bool readable = g.flags & CTCPB_LM_READABLE;
@@ -220,9 +215,9 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   // before it: 16 rows of 512 8.6 and 10.6, 32 10.8 and 10.9 (and a launch less), 16 of 1024 10.5
   // and 11.5, 8 of 2048 10.0 and 10.8, 16 of them 11.3 and 11.0.
   const int64_t values = (int64_t)g.rows * up(p.padded, 64);
-  const int per = 16 / elem_size(g.dtype);
-  const bool pieces = g.hidden <= kFewPieces * (g.hidden % per || !rows_aligned(g) ? 1 : per);
-  const bool there = p.quantize && values <= kFewValues && pieces;   // quantised by the same launch
+  // quantised by the same launch
+  const bool there = p.quantize && values <= kFewValues &&
+                     g.hidden <= kFewPieces * (16 / elem_size(g.dtype));
   p.few = g.rows <= (there || p.padded >= 1024 ? 32 : 16) && values <= kFewCodes && !p.pad_w &&
           g.features <= 64 * kCUs;
   if (p.few) {
@@ -265,28 +260,28 @@ int check_linear8(const ctcpb_lm_linear8_args& g) {
   return CTCPB_OK;
 }
 
-template <typename T, int N>
+template <typename T, bool ANY>
 void launch_quantize(const QuantArgs& a, hipStream_t st) {
+  constexpr int N = 16 / (int)sizeof(T);
   // a wave to each row where there are enough to fill the card, and they fit its registers
   if (a.rows >= 1024 && a.per <= 64 * kQuantHeld)
-    quantize_kernel<T, N, 1><<<(unsigned)((a.rows + 3) / 4), 256, 0, st>>>(a);
+    quantize_kernel<T, N, ANY, 1><<<(unsigned)((a.rows + 3) / 4), 256, 0, st>>>(a);
   else
-    quantize_kernel<T, N, 4><<<(unsigned)a.rows, 256, 0, st>>>(a);
+    quantize_kernel<T, N, ANY, 4><<<(unsigned)a.rows, 256, 0, st>>>(a);
 }
 
 template <typename T>
 void launch_quantize(const void* x, int64_t stride, int8_t* codes, int64_t codes_row, float* scales,
                      int32_t rows, int32_t hidden, int32_t padded, hipStream_t st) {
   constexpr int N = 16 / (int)sizeof(T);
-  QuantArgs a{static_cast<const char*>(x), stride * (int)sizeof(T), codes, codes_row, scales, rows,
-              hidden, padded, 0};
-  const bool wide = hidden % N == 0 && aligned(x, 16) && a.x_row % 16 == 0 && aligned(codes, N) &&
-                    codes_row % N == 0;
-  a.per = wide ? hidden / N : hidden;
-  if (wide)
-    launch_quantize<T, N>(a, st);
+  const QuantArgs a{static_cast<const char*>(x), stride * (int)sizeof(T), codes, codes_row, scales,
+                    rows, hidden, padded, ceil_div(hidden, N)};
+  const bool whole = hidden % N == 0 && aligned(x, 16) && a.x_row % 16 == 0 && aligned(codes, N) &&
+                     codes_row % N == 0;
+  if (whole)
+    launch_quantize<T, false>(a, st);
   else
-    launch_quantize<T, 1>(a, st);
+    launch_quantize<T, true>(a, st);
 }
 
 void launch_quantize(int32_t dtype, const void* x, int64_t stride, int8_t* codes, int64_t codes_row,
@@ -307,7 +302,7 @@ Operand codes_of(const void* data, int64_t stride, int32_t rows, int32_t hidden,
   return Operand{copy, padded, rows, false};
 }
 
-template <typename T, typename X, int N, int NT>
+template <typename T, typename X, bool ANY, int NT>
 void launch_few(const FewArgs& a, hipStream_t st) {
   const int tiles = ceil_div(a.features, 16);
   const size_t lds =
@@ -316,33 +311,32 @@ void launch_few(const FewArgs& a, hipStream_t st) {
   // Four waves to a tile, and four tiles at a time to a workgroup, where rows are too short for 16
   // and there are tiles enough
   if (tiles <= kCUs || a.padded >= 1024)
-    launch_with_lds(linear8_few_kernel<T, X, N, NT, 16>, (unsigned)std::min(tiles, kCUs), 1024, lds,
-                    a, st);
+    launch_with_lds(linear8_few_kernel<T, X, ANY, NT, 16>, (unsigned)std::min(tiles, kCUs), 1024,
+                    lds, a, st);
   else
-    launch_with_lds(linear8_few_kernel<T, X, N, NT, 4>,
+    launch_with_lds(linear8_few_kernel<T, X, ANY, NT, 4>,
                     (unsigned)std::min(ceil_div(tiles, 4), kCUs), 1024, lds, a, st);
 }
 
-template <typename T, typename X, int N>
+template <typename T, typename X, bool ANY>
 void launch_few(const FewArgs& a, hipStream_t st) {
   if (a.rows <= 16)
-    launch_few<T, X, N, 1>(a, st);
+    launch_few<T, X, ANY, 1>(a, st);
   else
-    launch_few<T, X, N, 2>(a, st);
+    launch_few<T, X, ANY, 2>(a, st);
 }
 
-// x of type X, in pieces of 16 bytes or single values.
+// x of type X, in pieces of 16 bytes, which are whole and aligned or not.
 template <typename T, typename X>
 void launch_few(FewArgs& a, const void* x, int64_t stride, hipStream_t st) {
   constexpr int N = 16 / (int)sizeof(X);
   a.x = static_cast<const char*>(x);
   a.x_row = stride * (int)sizeof(X);
-  const bool wide = a.hidden % N == 0 && aligned(x, 16) && a.x_row % 16 == 0;
-  a.per = wide ? a.hidden / N : a.hidden;
-  if (wide)
-    launch_few<T, X, N>(a, st);
+  a.per = ceil_div(a.hidden, N);
+  if (a.hidden % N == 0 && aligned(x, 16) && a.x_row % 16 == 0)
+    launch_few<T, X, false>(a, st);
   else
-    launch_few<T, X, 1>(a, st);
+    launch_few<T, X, true>(a, st);
 }
 
 template <typename T>
