@@ -195,6 +195,24 @@ def _apart(t, strides, name):
         raise ValueError(f"{name} is written, and must not have expanded axes")
 
 
+def _off(out, t, name):
+    """Raise ValueError if `out`, which is written, may overlap the input `t`: what a part of the
+    kernel has written, another would read."""
+    ends = [(a, a + sum((n - 1) * s for n, s in zip(b.shape, b.stride())) * b.itemsize + b.itemsize)
+            for b in (out, t) for a in (b.data_ptr(),)]
+    (a, a_end), (b, b_end) = ends
+    if a >= b_end or b >= a_end or not out.numel() or not t.numel():
+        return
+    if out.dim() == t.dim() == 2:   # columns of one matrix, side by side
+        step = out.stride(0) * out.itemsize
+        if 0 < step == t.stride(0) * t.itemsize:
+            width = out.shape[1] * out.itemsize
+            at = (b - a) % step
+            if at >= width and at + t.shape[1] * t.itemsize <= step:
+                return
+    raise ValueError(f"out must not overlap {name}")
+
+
 def _type(t, name):
     dt = _TYPES.get(t.dtype)
     if dt is None:
@@ -538,7 +556,7 @@ def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: fl
                window: int = 0, max_len: int = 0, out=None, stream=None):
     """``attention`` over caches of 8-bit codes (int8 or float8_e4m3fn) with float32 scales
     (pages, kv_heads) >= 0: keys and values are code times scale of their page and head.  q and
-    out are bfloat16, float16 or float32; head_dim is a multiple of 16."""
+    out are bfloat16, float16 or float32; head_dim is a multiple of 16.  `out` may be q."""
     dev = _gpu(q, "q")
     if q.requires_grad:
         _no_gradient("attention8")
@@ -557,6 +575,8 @@ def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: fl
         out = empty(shape, dtype=q.dtype, device=q.device)
     else:
         _like(out, dev, "out", q.dtype, shape)
+        if out.data_ptr() != q.data_ptr() or out.stride() != q.stride():
+            _off(out, q, "q")
     outr, outh, _ = _rows(out, "out")
     _apart(out, (outr, outh), "out")
     lse = empty((R, Hq), dtype=torch.float32, device=q.device)
@@ -652,6 +672,10 @@ def linear8(x, w, w_scale, bias=None, x_scale=None, dtype=None, out=None, stream
         out = empty((N, M), dtype=dtype, device=x.device)
     else:
         _like(out, dev, "out", dtype, (N, M))
+        for t, name in ((x, "x"), (w, "w"), (w_scale, "w_scale"), (bias, "bias"),
+                        (x_scale, "x_scale")):
+            if t is not None:
+                _off(out, t, name)
     so, _, _ = _matrix(out, "out")
     _apart(out, out.stride(), "out")
     args = _pack(_LINEAR8, x.data_ptr(), _ptr(x_scale), w.data_ptr(), w_scale.data_ptr(),

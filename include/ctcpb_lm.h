@@ -209,8 +209,9 @@ int ctcpb_lm_cache_load8(const ctcpb_lm_cache8_args* args, void* stream);
  * scale: `base` as there (its dtype that of q and out, its caches' strides in codes), but
  * head_dim is a multiple of 16.  Scales are any finite numbers >= 0.  Codes and scales of slots
  * past a row's length, or before its window in another page, are never used, whatever
- * they hold.  Nothing is rounded on the way to fewer than 22 bits.  Pages lie less than
- * 4 GiB apart (their scales too), tokens of a page up to 8 MiB. */
+ * they hold.  out may be q, but not overlap it otherwise.  Nothing is rounded on the way to
+ * fewer than 22 bits.  Pages lie less than 4 GiB apart (their scales too), tokens of a page up
+ * to 8 MiB. */
 typedef struct {
   ctcpb_lm_attention_args base;
   ctcpb_lm_scales k_scale, v_scale;
@@ -288,8 +289,8 @@ int ctcpb_lm_loss_grad(const ctcpb_lm_grad_args* args, void* workspace, size_t w
  *   not finite;  codes[n, k] = x[n, k] / scales[n], the exact quotient rounded to the nearest
  *   whole number (ties to the even one; 0 where the scale is 0 or NaN)
  *   x        device, typed, row stride stride_x >= 0
- *   codes    device, row stride stride_codes >= hidden; of what a row has behind `hidden`, up to
- *            the next multiple of 16 is zeroed
+ *   codes    device, row stride stride_codes >= hidden; of what a row (the last one too) has
+ *            behind `hidden`, up to the next multiple of 16 is zeroed
  *   scales   device float32 [rows] */
 typedef struct {
   const void* x;
@@ -315,7 +316,8 @@ enum { CTCPB_LM_READABLE = 1 };
  *            device float32 [rows]
  *   w        device int8 [features][hidden], row stride stride_w >= 0;  w_scale: device
  *            float32 [features];  bias: device float32 [features] or NULL
- *   out      device, typed (dtype), row stride stride_out >= features
+ *   out      device, typed (dtype), row stride stride_out >= features; must not overlap the
+ *            inputs
  *   hidden   at most 131071
  *   workspace  device, 256-byte aligned, contents on entry do not matter; calls that share it
  *            must not overlap.  Its size depends on the addresses and strides of x and w too;

@@ -216,6 +216,18 @@ def test_strided_q_out_and_scales():
 
 
 @pytest.mark.parametrize("lens", [[300] * 3, [3000, 17, 0], [(9 * r) % 70 for r in range(900)]])
+def test_out_in_place_of_q(lens):
+    a = make(lens, 40, 2, 64, torch.bfloat16, torch.int8, 16)
+    want, _ = lm.attention8(*a)
+    q = a[0].clone()
+    lm.attention8(q, *a[1:], out=q)
+    assert torch.equal(q, want)
+    big = torch.zeros((q.shape[0] + 1, 40, 64), dtype=q.dtype, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        lm.attention8(big[:-1], *a[1:], out=big[1:])
+
+
+@pytest.mark.parametrize("lens", [[300] * 3, [3000, 17, 0], [(9 * r) % 70 for r in range(900)]])
 def test_repeated_replayed_and_on_another_stream(lens):
     """The same bits from every call: eager, on a side stream, and from graphs that are replayed in
     between (each with a workspace of its own)."""

@@ -49,6 +49,30 @@ def test_codes_and_scales(dtype, H):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [5, 8, 387, 512, 2047, 4100])
+def test_rows_that_begin_anywhere(dtype, H):
+    """Values and codes at addresses that are multiples of their own size only, a wave or a
+    workgroup to each row, and nothing written beside the rows."""
+    for N in (9, 1030):
+        big = rows(N, H + 9, dtype, H)
+        for at in range(4 if N < 100 else 2):
+            x = big[:, at:at + H]
+            want, s = lm_ref8.quantize(x)
+            codes, scales = lm.quantize_rows(x)
+            assert torch.equal(scales.cpu(), s) and torch.equal(codes.cpu().double(), want)
+            for step in (H, H + 3):
+                space = torch.full((N * step + 32,), 99, dtype=torch.int8, device="cuda")
+                part = space[16 + at:]
+                lm._check(lm.lib().ctcpb_lm_quantize_rows(lm._pack(
+                    lm._QUANTIZE, x.data_ptr(), part.data_ptr(), scales.data_ptr(), x.stride(0),
+                    step, lm._TYPES[dtype], N, H), torch.cuda.current_stream().cuda_stream))
+                got = part[:N * step].view(N, step)
+                assert torch.equal(got[:, :H].cpu().double(), want)
+                assert (got[:, H:min(step, -(-H // 16) * 16)] == 0).all()
+                assert (space[:16 + at] == 99).all() and (part[N * step:] == 99).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_quotients_next_to_a_half(dtype):
     """Every value is n + 1/2 steps, or a neighbour of that in the type: halves go to the even
     code, the others to their own side."""
@@ -268,3 +292,27 @@ def test_refusals():
     for bad in (x.double(), x[0], x[:, :0], x.t(), codes, x.clone().requires_grad_()):
         with pytest.raises(ValueError):
             lm.quantize_rows(bad)
+
+
+def test_out_does_not_overlap_its_inputs():
+    x = rows(40, 64, torch.float16)
+    w, ws = weight(64, 64)
+    want = lm.linear8(x, w, ws)
+    for bad in (x, x.as_strided((40, 64), (32, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            lm.linear8(x, w, ws, out=bad)
+    one = torch.empty((8192,), dtype=torch.uint8, device="cuda")
+    part = one[:4096].view(torch.int8).view(64, 64)
+    part.copy_(w)
+    with pytest.raises(ValueError, match="overlap"):
+        lm.linear8(x, part, ws, out=one[2048:2048 + 5120].view(torch.float16).view(40, 64))
+    # the halves of one matrix
+    both = torch.zeros((40, 128), dtype=torch.float16, device="cuda")
+    for a, b in ((0, 64), (64, 0)):
+        both[:, a:a + 64] = x
+        lm.linear8(both[:, a:a + 64], w, ws, out=both[:, b:b + 64])
+        assert torch.equal(both[:, b:b + 64], want) and torch.equal(both[:, a:a + 64], x)
+    with pytest.raises(ValueError, match="overlap"):
+        lm.linear8(both[:, :64], w, ws, out=both[:, 63:127])
+    with pytest.raises(ValueError, match="overlap"):
+        lm.linear8(both[:, 64:], w, ws, out=both[:, 1:65])
