@@ -47,7 +47,9 @@ __device__ inline uint32_t wave_magnitude(uint32_t most) {
 //
 // Bound by memory for prompts: 131072 tokens of 8 x 128 bf16, read and written 805 MB, 167 us in
 // pages of 16, 172 of 32, 169 of 64 (4.8 TB/s; a wave to each page: 167, 319, 527); by latency
-// for a step of single tokens, 6 us for 256.
+// for a step of single tokens, 6 us for 256.  Where half the registers hold a run, a wave does the
+// keys' and the values' (B = 2 below): 131072 tokens of 8 x 64 bf16 in pages of 16, stored and
+// read back, 175 us, against 195 with a wave to each; 16 x 32 204 and 268.
 constexpr int kStoreHeld = 4;
 
 // The page of the nearest token with a slot before token t, -1 if there is none.
@@ -61,9 +63,9 @@ __device__ inline int32_t page_before(const Cache8Args& a, int32_t t, int lane) 
   return -1;
 }
 
-template <typename T, typename C, int N, int W>
+template <typename T, typename C, int N, int W, int U>
 struct StoreRun {
-  static constexpr int U = kStoreHeld, kLanes = 64 * W;
+  static constexpr int kLanes = 64 * W, kHeld = U;
   const char* src;          // the head's row of token 0
   int64_t src_t;
   char* page;               // the head's row of slot 0
@@ -169,18 +171,20 @@ struct StoreRun {
 
 // N: values of a piece, 8 (16-bit types) or 4 (f32) where rows and strides allow, else 1.
 // W: waves of a workgroup that do a run together; with one, a workgroup's four have four runs.
-template <typename T, typename C, int N, int W>
+// B: 2 where half of kStoreHeld is enough: a wave then does the run's keys and values, whose loads
+// overlap.
+template <typename T, typename C, int N, int W, int B>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Args a) {
+  typedef StoreRun<T, C, N, W, kStoreHeld / B> Run;
   __shared__ uint32_t part[2][W];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // (chunk, head, keys or values)
-  const int64_t unit = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  // (chunk, head, keys or values; with B = 2 both)
+  const int64_t unit = (W == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x) * B;
   const int64_t chunk = unit / (2 * a.heads);
   const int64_t begin = chunk * a.chunk;
   if (begin >= a.tokens) return;
   const int32_t head = (int32_t)(unit % (2 * a.heads)) >> 1;
-  const bool values = unit & 1;
   const int32_t t0 = (int32_t)begin, n = min(a.chunk, a.tokens - t0);
 
   const int32_t slot = lane < n ? a.slots[t0 + lane] : -1;
@@ -198,8 +202,6 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Arg
   if (!below) before = outside;
   uint64_t leaders = __ballot(in && mine != before);
 
-  const CacheView& c = values ? a.vc : a.kc;
-  const ScaleView& sc = values ? a.vs : a.ks;
   const int32_t mask = (1 << a.page_log) - 1;
   for (int parity = 0; leaders; parity ^= 1) {
     const int first = __builtin_ctzll(leaders);
@@ -225,57 +227,81 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Arg
         if (other) break;
       }
     }
-    StoreRun<T, C, N, W> run;
+    Run run[B];
+    float* scale[B];
+    float old[B];
     const int32_t from = t0 + first;
-    run.src_t = values ? a.v_t : a.k_t;
-    run.src = (values ? a.v + head * a.v_h : a.k + head * a.k_h) + from * run.src_t;
-    run.page = c.data + page * c.page + head * c.head;
-    run.token = c.token;
-    run.slots = a.slots + from;
-    run.count = last - from + 1;
-    run.num_slots = a.num_slots;
-    run.mask = mask;
-    run.per = a.per;
-    run.lane = W == 1 ? lane : (int)threadIdx.x;
-    float* scale = sc.data + page * sc.page + head * sc.head;
-    const float old = begun ? 0.0f : *scale;
-    const int64_t pieces = (int64_t)run.count * a.per;
-    const int64_t batches = (pieces + run.kLanes * run.U - 1) / (run.kLanes * run.U);
-    typename StoreRun<T, C, N, W>::At at = run.first();
-    const auto at0 = at;
-    uint32_t most = 0;
-    for (int64_t b = 0; b < batches; ++b) {
-      run.load(at);
-      run.raise(most);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const bool values = B == 2 ? b : unit & 1;
+      const CacheView& c = values ? a.vc : a.kc;
+      const ScaleView& sc = values ? a.vs : a.ks;
+      Run& r = run[b];
+      r.src_t = values ? a.v_t : a.k_t;
+      r.src = (values ? a.v + head * a.v_h : a.k + head * a.k_h) + from * r.src_t;
+      r.page = c.data + page * c.page + head * c.head;
+      r.token = c.token;
+      r.slots = a.slots + from;
+      r.count = last - from + 1;
+      r.num_slots = a.num_slots;
+      r.mask = mask;
+      r.per = a.per;
+      r.lane = W == 1 ? lane : (int)threadIdx.x;
+      scale[b] = sc.data + page * sc.page + head * sc.head;
+      old[b] = begun ? 0.0f : *scale[b];
     }
-    most = wave_magnitude<T>(most);
+    const int64_t pieces = (int64_t)run[0].count * a.per;
+    const int64_t batches = (pieces + Run::kLanes * Run::kHeld - 1) / (Run::kLanes * Run::kHeld);
+    typename Run::At at = run[0].first();
+    const auto at0 = at;
+    uint32_t most[B] = {};
+    for (int64_t i = 0; i < batches; ++i) {
+      const auto here = at;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        at = here;
+        run[b].load(at);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) run[b].raise(most[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) most[b] = wave_magnitude<T>(most[b]);
     if constexpr (W > 1) {
-      if (lane == 0) part[parity][wave] = most;
+      static_assert(B == 1, "a wave's own");
+      if (lane == 0) part[parity][wave] = most[0];
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < W; ++w) most = max(most, part[parity][w]);
+      for (int w = 0; w < W; ++w) most[0] = max(most[0], part[parity][w]);
     }
-    const float need = bits_f32(unit_bits<C>(most));
-    // (a NaN stays, whichever of the two it is)
-    const float now = old != old ? old : need != need || need > old ? need : old;
-    if (now > old && old > 0.0f) {
-      run.rescale(old / now);
-      // the new codes go over some of these
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      if constexpr (W > 1) __syncthreads();
-    }
-    const float inverse = inverse_unit(now);
-    if (batches == 1) {
-      run.write(at0, inverse);
-    } else {
-      at = at0;
-      for (int64_t b = 0; b < batches; ++b) {
-        const auto here = at;
-        run.load(at);
-        run.write(here, inverse);
+    float now[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const float need = bits_f32(unit_bits<C>(most[b])), was = old[b];
+      // (a NaN stays, whichever of the two it is)
+      now[b] = was != was ? was : need != need || need > was ? need : was;
+      if (now[b] > was && was > 0.0f) {
+        run[b].rescale(was / now[b]);
+        // the new codes go over some of these
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if constexpr (W > 1) __syncthreads();
       }
     }
-    if (run.lane == 0) *scale = now;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const float inverse = inverse_unit(now[b]);
+      if (batches == 1) {
+        run[b].write(at0, inverse);
+      } else {
+        at = at0;
+        for (int64_t i = 0; i < batches; ++i) {
+          const auto here = at;
+          run[b].load(at);
+          run[b].write(here, inverse);
+        }
+      }
+      if (run[b].lane == 0) *scale[b] = now[b];
+    }
   }
 }
 

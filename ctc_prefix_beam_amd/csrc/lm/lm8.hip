@@ -402,12 +402,14 @@ int ctcpb_lm_cache_store8(const ctcpb_lm_cache8_args* args, void* stream) {
     bool wide;
     Cache8Args a = cache8_args(*args, wide);
     // A wave to each token while that makes no more than some waves to each place on the card, else
-    // as many as hold the values of a page in registers, to as many tokens
+    // as many as hold a page's keys or values in registers, or one that holds both, to as many
+    // tokens
     const int64_t one = (int64_t)a.tokens * a.heads * 2, pieces = (int64_t)args->page_size * a.per;
     const bool many = one > 1 << 16;
     const int waves = !many || pieces <= 64 * kStoreHeld ? 1 : pieces <= 128 * kStoreHeld ? 2 : 4;
+    const bool both = many && pieces <= 32 * kStoreHeld;
     a.chunk = !many ? 1 : std::min(std::max(args->page_size, 16), 64);
-    const int64_t units = (int64_t)ceil_div(a.tokens, a.chunk) * a.heads * 2;
+    const int64_t units = (int64_t)ceil_div(a.tokens, a.chunk) * a.heads * (both ? 1 : 2);
     const int64_t blocks = waves == 1 ? (units + 3) / 4 : units;
     if (blocks > INT_MAX) return fail(CTCPB_ERR_UNSUPPORTED, "too many tokens for one launch");
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -415,12 +417,14 @@ int ctcpb_lm_cache_store8(const ctcpb_lm_cache8_args* args, void* stream) {
       typedef decltype(t) T;
       typedef decltype(c) C;
       constexpr int N = decltype(n)::value;
-      if (waves == 1)
-        store8_kernel<T, C, N, 1><<<(unsigned)blocks, 256, 0, st>>>(a);
+      if (both)
+        store8_kernel<T, C, N, 1, 2><<<(unsigned)blocks, 256, 0, st>>>(a);
+      else if (waves == 1)
+        store8_kernel<T, C, N, 1, 1><<<(unsigned)blocks, 256, 0, st>>>(a);
       else if (waves == 2)
-        store8_kernel<T, C, N, 2><<<(unsigned)blocks, 128, 0, st>>>(a);
+        store8_kernel<T, C, N, 2, 1><<<(unsigned)blocks, 128, 0, st>>>(a);
       else
-        store8_kernel<T, C, N, 4><<<(unsigned)blocks, 256, 0, st>>>(a);
+        store8_kernel<T, C, N, 4, 1><<<(unsigned)blocks, 256, 0, st>>>(a);
     });
     return launched("store8_kernel");
   });

@@ -221,6 +221,33 @@ def test_many_tokens_in_larger_pages(page, D, dtype, code):
           *cache(pages, page, H, D, code, "thd", seed=1))
 
 
+@pytest.mark.parametrize("page,D,dtype,code", [
+    (16, 64, torch.bfloat16, torch.int8), (16, 64, torch.float16, torch.float8_e4m3fn),
+    (8, 128, torch.float16, torch.int8), (16, 32, torch.float32, torch.float8_e4m3fn),
+    (4, 256, torch.bfloat16, torch.float8_e4m3fn), (4, 20, torch.bfloat16, torch.int8),
+    (8, 13, torch.float32, torch.int8)])
+def test_many_tokens_in_small_pages(page, D, dtype, code):
+    """Pages whose keys and values one wave stores together: begun, gone on with, with tokens
+    without a slot between (a run of more tokens than the page has slots), and keys or values
+    alone that raise a scale or are not finite."""
+    H = 60
+    g = torch.Generator().manual_seed(page + D)
+    counts = torch.randint(0, 130, (16,), generator=g).tolist() + [1] * 30
+    held = torch.randint(0, page, (46,), generator=g).tolist()
+    slots, pages = slots_of(counts, held, page)
+    gaps = torch.rand(slots.numel(), generator=g) < 0.4
+    gaps[400:] = False
+    slots = torch.stack((slots, torch.full_like(slots, -1)), 1).flatten()[
+        torch.stack((torch.ones_like(gaps), gaps), 1).flatten()]
+    assert slots.numel() * H * 2 > 1 << 16   # not a wave to each token
+    x, y = (t.clone() for t in random(slots, H, D, dtype))
+    x[::7, 3] *= 512
+    y[::11, 4] *= 512
+    x[100, 5, D - 1], y[200, 6, 0] = math.nan, math.inf
+    check(x, y, slots.cuda(), *cache(pages, page, H, D, code, "htd"),
+          *cache(pages, page, H, D, code, "thd", seed=1))
+
+
 def test_no_tokens_and_a_stream_of_its_own():
     kc, ks = cache(3, 16, 2, 64, torch.int8)
     vc, vs = cache(3, 16, 2, 64, torch.int8)
