@@ -341,11 +341,11 @@ __global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T, fa
 // next tiles' first weights are on their way while the waves' sums are added.  Weights go from
 // memory straight into the registers of the matrix instruction, kFewHeld of them a lane at a
 // time. 32 rows x 5000 channels of 512, bf16: 8.2 us; a row of codes with 8192 channels of 2048
-// (16.8 MB) 7 us.
+// (16.8 MB) 7 us.  Long rows are quantised by several waves each: a call of a row of 4096 with 4096
+// channels 10.4 us (12.6 with a launch for that), of 16384 21.8 (29.1).
 constexpr int32_t kFewValues = 16384;
 constexpr int32_t kFewCodes = 124 * 1024;   // of a CU's 160 KB of LDS; the waves' sums take 32 KB
 constexpr int kFewHeld = 8;
-constexpr int kFewPieces = 256;   // of a row that is quantised here
 
 struct FewArgs {
   const char* x;
@@ -359,56 +359,62 @@ struct FewArgs {
   int32_t rows, hidden, features;
   int32_t padded;          // bytes of a row of w that can be read
   int32_t per;             // pieces of a row of x
+  int32_t ways_log;        // 2^this waves quantise a row: as many of the 16 as it has pieces for
 };
 
-// Codes and scales of rows first, first + step, .. below a.rows (up to 32 rows over 16 waves: two
-// at a time, whose loads and reductions overlap), P pieces a lane to each.
-template <typename X, int N, bool ANY, int P>
-__device__ inline void quantize_few(const FewArgs& a, int first, int step, int lane, int8_t* codes,
-                                    int pitch, float* sx) {
-  constexpr int R = 2;
-  for (int n0 = first; n0 < a.rows; n0 += R * step) {
-    Values<X, N> held[R][P];
-    uint32_t most[R];
+// Codes and scales of the rows, up to 16 * R: a wave has a part of row `wave >> ways_log`, or (R =
+// 2) rows `wave` and wave + 16, whose loads and reductions overlap.  P pieces a lane to each.
+// `most_of`: room for 16 waves' maxima.
+template <typename X, int N, bool ANY, int P, int R>
+__device__ inline void quantize_few(const FewArgs& a, int wave, int lane, int8_t* codes, int pitch,
+                                    float* sx, uint32_t* most_of) {
+  const int ways = R == 1 ? 1 << a.ways_log : 1, n0 = R == 1 ? wave >> a.ways_log : wave;
+  const int first = (wave & (ways - 1)) * 64 + lane, step = 64 * ways;   // of the lane's pieces
+  Values<X, N> held[R][P];
+  uint32_t most[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int n = min(n0 + r * step, a.rows - 1);   // (the last row again: not kept)
+  for (int r = 0; r < R; ++r) {
+    const int n = min(n0 + r * 16, a.rows - 1);   // (the last row again: not kept)
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (first + p * step < a.per) {
+        load_piece<ANY>(held[r][p], a.x + n * a.x_row, first + p * step, a.hidden);
+      } else {
+#pragma unroll
+        for (uint32_t& w : held[r][p].w) w = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    most[r] = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) held[r][p].raise(most[r]);
+    most[r] = Values<X, N>::magnitude(most[r]);
+  }
+  for (int s = 1; s < 64; s <<= 1)
+#pragma unroll
+    for (int r = 0; r < R; ++r) most[r] = max(most[r], (uint32_t)__shfl_xor((int)most[r], s));
+  if (R == 1 && ways > 1) {
+    if (lane == 0) most_of[wave] = most[0];
+    __syncthreads();
+    for (int w = 0; w < ways; ++w) most[0] = max(most[0], most_of[(wave & -ways) + w]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int n = n0 + r * 16;
+    const RowScale q(most[r]);
+    if (n < a.rows) {
+      if (first == 0) sx[n] = q.scale;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        if (p * 64 + lane < a.per) {
-          load_piece<ANY>(held[r][p], a.x + n * a.x_row, p * 64 + lane, a.hidden);
-        } else {
+        const int k = (first + p * step) * N;
+        if (!q.some) {
 #pragma unroll
           for (uint32_t& w : held[r][p].w) w = 0;
         }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      most[r] = 0;
-#pragma unroll
-      for (int p = 0; p < P; ++p) held[r][p].raise(most[r]);
-      most[r] = Values<X, N>::magnitude(most[r]);
-    }
-    for (int s = 1; s < 64; s <<= 1)
-#pragma unroll
-      for (int r = 0; r < R; ++r) most[r] = max(most[r], (uint32_t)__shfl_xor((int)most[r], s));
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int n = n0 + r * step;
-      const RowScale q(most[r]);
-      if (n < a.rows) {
-        if (lane == 0) sx[n] = q.scale;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          if (!q.some) {
-#pragma unroll
-            for (uint32_t& w : held[r][p].w) w = 0;
-          }
-          if (p * 64 + lane < a.per)
-            quantize_piece<X, N, ANY>(held[r][p], q, codes + n * pitch + (p * 64 + lane) * N,
-                                      a.hidden - (p * 64 + lane) * N);
-        }
+        if (first + p * step < a.per)
+          quantize_piece<X, N, ANY>(held[r][p], q, codes + n * pitch + k, a.hidden - k);
       }
     }
   }
@@ -458,12 +464,21 @@ __global__ __launch_bounds__(1024) void linear8_few_kernel(FewArgs a) {
       }
       if (lane == 0) sx[n] = a.x_scale[n];
     }
-  } else if (a.per <= 64) {
-    quantize_few<X, N, ANY, 1>(a, wave, 16, lane, codes, pitch, sx);
-  } else if (a.per <= 128) {
-    quantize_few<X, N, ANY, 2>(a, wave, 16, lane, codes, pitch, sx);
   } else {
-    quantize_few<X, N, ANY, 4>(a, wave, 16, lane, codes, pitch, sx);
+    // Pieces a lane, if there is more than one: rows * hidden is at most kFewValues, and more than 8
+    // waves have a part, so up to 32 / N of them
+    static_assert(kFewValues <= 16384, "more pieces than that");
+    uint32_t* most_of = reinterpret_cast<uint32_t*>(parts);
+    const int lanes = NT == 1 ? 64 << a.ways_log : 64;
+    if (a.per <= lanes)
+      quantize_few<X, N, ANY, 1, NT>(a, wave, lane, codes, pitch, sx, most_of);
+    else if (a.per <= 2 * lanes)
+      quantize_few<X, N, ANY, 2, NT>(a, wave, lane, codes, pitch, sx, most_of);
+    else if (N == 8 || a.per <= 4 * lanes)
+      quantize_few<X, N, ANY, 4, NT>(a, wave, lane, codes, pitch, sx, most_of);
+    else
+      quantize_few<X, N, ANY, N == 4 && NT == 1 ? 8 : 4, NT>(a, wave, lane, codes, pitch, sx,
+                                                             most_of);
   }
   for (int n = wave; n < a.rows; n += 16)
     for (int k = a.hidden + lane; k < steps * 64; k += 64) codes[n * pitch + k] = 0;

@@ -216,8 +216,7 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   // and 11.5, 8 of 2048 10.0 and 10.8, 16 of them 11.3 and 11.0.
   const int64_t values = (int64_t)g.rows * up(p.padded, 64);
   // quantised by the same launch
-  const bool there = p.quantize && values <= kFewValues &&
-                     g.hidden <= kFewPieces * (16 / elem_size(g.dtype));
+  const bool there = p.quantize && values <= kFewValues;
   p.few = g.rows <= (there || p.padded >= 1024 ? 32 : 16) && values <= kFewCodes && !p.pad_w &&
           g.features <= 64 * kCUs;
   if (p.few) {
@@ -333,6 +332,7 @@ void launch_few(FewArgs& a, const void* x, int64_t stride, hipStream_t st) {
   a.x = static_cast<const char*>(x);
   a.x_row = stride * (int)sizeof(X);
   a.per = ceil_div(a.hidden, N);
+  while (64 << a.ways_log < a.per && (2 << a.ways_log) * a.rows <= 16) ++a.ways_log;
   if (a.hidden % N == 0 && aligned(x, 16) && a.x_row % 16 == 0)
     launch_few<T, X, false>(a, st);
   else
@@ -342,7 +342,7 @@ void launch_few(FewArgs& a, const void* x, int64_t stride, hipStream_t st) {
 template <typename T>
 void run_few(const LinearPlan& p, const ctcpb_lm_linear8_args& g, char* ws, hipStream_t st) {
   FewArgs a{nullptr, 0, g.x_scale, g.w, g.stride_w, g.w_scale, g.bias, static_cast<char*>(g.out),
-            g.stride_out, g.rows, g.hidden, g.features, p.padded, 0};
+            g.stride_out, g.rows, g.hidden, g.features, p.padded, 0, 0};
   if (g.x_dtype == CTCPB_LM_CODES) return launch_few<T, int8_t>(a, g.x, g.stride_x, st);
   if (!p.quantize) return launch_few<T, T>(a, g.x, g.stride_x, st);   // (out has x's type)
   float* scales = reinterpret_cast<float*>(ws + p.o_scale);

@@ -159,6 +159,28 @@ def test_few_rows(dtype, N, M, H):
     assert torch.equal(lm.linear8(apart, wide, ws, bias), want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,M,H", [
+    (1, 77, 16000), (1, 29, 16384), (2, 40, 8192), (3, 65, 5001), (4, 5000, 1100), (5, 65, 3200),
+    (7, 33, 2300), (8, 20, 2048), (9, 40, 1800), (13, 33, 1250), (16, 70, 1024), (17, 40, 960)])
+def test_few_long_rows(dtype, N, M, H):
+    """Rows that several waves quantise, with one of zeros, one of a single value and one that is
+    not finite among them."""
+    x = rows(N, H, dtype, N)
+    if N > 3:
+        x[0], x[1, 1:] = 0, 0
+        x[3, H - 1] = math.inf
+    w, ws = weight(M, -(-H // 16) * 16)
+    w = w[:, :H]
+    out = lm.linear8(x, w, ws)
+    codes, s = lm_ref8.quantize(x)
+    if N > 3:
+        assert torch.isnan(out[3]).all() and (out[0] == 0).all()
+        codes, s, x, out = (t[torch.arange(N) != 3] for t in (codes, s, x, out.cpu()))
+    want, tol = lm_ref8.linear(codes, s, w, ws, None, dtype)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("N,M,H", [(1, 40, 131071), (3, 70, 100000), (300, 40, 65536)])
 def test_long_sums_stay_whole(N, M, H):
     """Sums of up to 2^31 - 128^2, exact in 32 bits."""
