@@ -156,7 +156,7 @@ struct RowPieces {
 
 // W waves to a row: one, and four rows to a workgroup, or four.  Bound by memory: 20000 rows of
 // 4096 f16 51 us, 4.8 TB/s; 8192 of 2048 bf16 16 us, of which moving the 50 MB takes 10; 875 of
-// 387 f32 3.9 us.  Pieces that begin anywhere (ANY): 4000 rows of 2047 bf16 14.5 us a call, 20.4
+// 387 f32 4.7 us.  Pieces that begin anywhere (ANY): 4000 rows of 2047 bf16 14.5 us a call, 20.4
 // value by value.
 template <typename T, int N, bool ANY, int W>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
