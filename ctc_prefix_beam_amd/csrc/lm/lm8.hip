@@ -15,6 +15,8 @@ namespace {
 
 constexpr const char* kBadCode = "code must be CTCPB_LM_INT8 or CTCPB_LM_E4M3";
 
+constexpr int64_t kMostBlocks = 1 << 24;   // of 256 threads: a launch has less than 2^32
+
 bool code_ok(int32_t code) { return code == CTCPB_LM_INT8 || code == CTCPB_LM_E4M3; }
 
 int check_scales(const ctcpb_lm_scales& s) {
@@ -288,7 +290,10 @@ void launch_quantize(int32_t dtype, const void* x, int64_t stride, int8_t* codes
   const auto f = dtype == CTCPB_LM_BF16  ? launch_quantize<__bf16>
                  : dtype == CTCPB_LM_F16 ? launch_quantize<_Float16>
                                          : launch_quantize<float>;
-  f(x, stride, codes, codes_row, scales, rows, hidden, padded, st);
+  constexpr int32_t most = 1 << 22;   // rows of a launch, which has 2^32 threads at most
+  for (int64_t r = 0; r < rows; r += most)
+    f(static_cast<const char*>(x) + r * stride * elem_size(dtype), stride, codes + r * codes_row,
+      codes_row, scales + r, (int32_t)std::min<int64_t>(rows - r, most), hidden, padded, st);
 }
 
 Operand codes_of(const void* data, int64_t stride, int32_t rows, int32_t hidden, int32_t padded,
@@ -411,7 +416,8 @@ int ctcpb_lm_cache_store8(const ctcpb_lm_cache8_args* args, void* stream) {
     a.chunk = !many ? 1 : std::min(std::max(args->page_size, 16), 64);
     const int64_t units = (int64_t)ceil_div(a.tokens, a.chunk) * a.heads * (both ? 1 : 2);
     const int64_t blocks = waves == 1 ? (units + 3) / 4 : units;
-    if (blocks > INT_MAX) return fail(CTCPB_ERR_UNSUPPORTED, "too many tokens for one launch");
+    if (blocks >= kMostBlocks)
+      return fail(CTCPB_ERR_UNSUPPORTED, "too many tokens for one launch");
     hipStream_t st = static_cast<hipStream_t>(stream);
     for_types(args->dtype, args->code, wide, [&](auto t, auto c, auto n) {
       typedef decltype(t) T;
@@ -471,6 +477,9 @@ int ctcpb_lm_attention8(const ctcpb_lm_attention8_args* args, void* workspace,
                                 "workspace smaller than ctcpb_lm_attention8_workspace", a))
       return rc;
     if (g.rows == 0) return ok();
+    // (a wave to an item, four to a workgroup; four heads or more to a workgroup that joins)
+    if ((int64_t)g.rows * g.q_heads >= 4 * kMostBlocks)
+      return fail(CTCPB_ERR_UNSUPPORTED, "too many rows for one launch");
     a.ks = view(args->k_scale);
     a.vs = view(args->v_scale);
     if (std::max(a.kc.page, a.vc.page) > UINT32_MAX ||

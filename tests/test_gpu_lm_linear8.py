@@ -72,6 +72,19 @@ def test_rows_that_begin_anywhere(dtype, H):
                 assert (space[:16 + at] == 99).all() and (part[N * step:] == 99).all()
 
 
+def test_more_rows_than_one_launch_takes():
+    N = (1 << 22) + 70
+    x = rows(100, 9, torch.float16).repeat(N // 100 + 1, 1)[:N]
+    codes, scales = lm.quantize_rows(x)
+    want, s = lm_ref8.quantize(x[:100])
+    for a in (0, (1 << 22) - 300, N - 300):
+        at = a // 100 * 100
+        assert torch.equal(codes[at:at + 100].cpu().double(), want)
+        assert torch.equal(scales[at:at + 100].cpu(), s)
+    assert torch.equal(codes, codes[:100].repeat(N // 100 + 1, 1)[:N])
+    assert torch.equal(scales, scales[:100].repeat(N // 100 + 1)[:N])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_quotients_next_to_a_half(dtype):
     """Every value is n + 1/2 steps, or a neighbour of that in the type: halves go to the even

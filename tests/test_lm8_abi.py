@@ -45,6 +45,13 @@ def test_store_and_load_refusals(L, kw):
         assert L.ctcpb_lm_last_error().decode() != ""
 
 
+def test_more_tokens_than_a_launch_has_threads_for(L):
+    wide = dict(k=1 << 20, v=1 << 20, D=128, st=8192, sh=128)
+    for kw in (dict(page=16), dict(page=32), dict(page=256), dict(page=16, D=64)):
+        assert cache8(L.ctcpb_lm_cache_store8, T=(1 << 27), H=64, **{**wide, **kw}) == 3
+        assert "too many tokens" in L.ctcpb_lm_last_error().decode()
+
+
 def test_no_tokens(L):
     for call in (L.ctcpb_lm_cache_store8, L.ctcpb_lm_cache_load8):
         assert cache8(call, T=0, k=N, v=N, slots=N) == 0
@@ -66,7 +73,7 @@ def attend(L, dtype=0, code=0, q=P, sr=128, sh=64, kc=cache(), vc=cache(), ks=sc
     (dict(vc=cache(0)), 1), (dict(kc=cache(264)), 1), (dict(vc=cache(token=72)), 1),
     (dict(ks=scales(0)), 1), (dict(vs=scales(0)), 1), (dict(vs=scales(page=-2)), 1),
     (dict(width=4096, stride=4096, ws=N), 1), (dict(width=4096, stride=4096, ws_bytes=16), 2),
-    (dict(rows=1 << 30, Hq=64, Hkv=64), 3), (dict(kc=cache(page=1 << 32)), 3),
+    (dict(rows=1 << 30, Hq=64, Hkv=64), 3), (dict(rows=1 << 24), 3), (dict(kc=cache(page=1 << 32)), 3),
     (dict(vc=cache(token=(1 << 23) + 16)), 3), (dict(ks=scales(page=1 << 30)), 3),
     (dict(vs=scales(page=1 << 62)), 3)])
 def test_attention_refusals(L, kw, code):
