@@ -1,6 +1,8 @@
 // A paged key/value cache held in 8 bits, with a scale for each page and head: keys and
 // values quantised as they are stored, and read back.
 #pragma once
+#include <type_traits>
+
 #include "codes.h"
 
 namespace ctcpb_lm {
@@ -310,6 +312,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Arg
 // k[t, h] = code * scale of the token's slot, in T; zeros for a token without a slot.  A copy,
 // bound by memory: 131072 tokens of 8 x 128 to bf16 147 us, 5.4 TB/s; 500 of 8 x 64 to f32 3.2
 // us. A thread makes 16 bytes of a key's row and the same of the value's.
+//
+// What is finite is read as such: the nearest code to a value next to the type's largest one may
+// stand for more (f16 65504 in int8 is 64 * 1024), and is read as the largest.  No code reaches
+// 512, so only scales above a 512th of that have to be looked at, in a branch of the whole wave
+// (the limits cost 24 of 185 us where every value is compared).
 template <typename T, typename C, int N>
 __global__ __launch_bounds__(256) void load8_kernel(Cache8Args a) {
   const int64_t step = (int64_t)gridDim.x * 256;
@@ -321,44 +328,60 @@ __global__ __launch_bounds__(256) void load8_kernel(Cache8Args a) {
     const int32_t slot = a.slots[t];
     const bool in = (uint32_t)slot < (uint32_t)a.num_slots;
     const int64_t page = in ? slot >> a.page_log : 0, at = slot & ((1 << a.page_log) - 1);
+    // (0 times a scale of 0 without a slot)
+    constexpr int W = N == 1 ? 1 : N / 4;
+    uint32_t w[2][W] = {};
+    float scale[2] = {0.0f, 0.0f};
+    if (in) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const CacheView& c = half ? a.vc : a.kc;
-      const ScaleView& sc = half ? a.vs : a.ks;
-      T* to = reinterpret_cast<T*>((half ? a.v + t * a.v_t + h * a.v_h
-                                         : a.k + t * a.k_t + h * a.k_h)) + p * N;
-      T out[N];
-#pragma unroll
-      for (int j = 0; j < N; ++j) out[j] = (T)0.0f;
-      if (in) {
+      for (int half = 0; half < 2; ++half) {
+        const CacheView& c = half ? a.vc : a.kc;
+        const ScaleView& sc = half ? a.vs : a.ks;
         const char* from = c.data + page * c.page + at * c.token + h * c.head + p * N;
-        const float scale = sc.data[page * sc.page + h * sc.head];
-        float v[4];
+        scale[half] = sc.data[page * sc.page + h * sc.head];
         if constexpr (N == 1) {
-          C::values4(*reinterpret_cast<const uint8_t*>(from), v);
-          out[0] = (T)(v[0] * scale);
+          w[half][0] = *reinterpret_cast<const uint8_t*>(from);
+        } else if constexpr (N == 8) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(from);
+          w[half][0] = x[0];
+          w[half][1] = x[1];
         } else {
-          uint32_t w[N / 4];
-          if constexpr (N == 8) {
-            const u32x2 x = *reinterpret_cast<const u32x2*>(from);
-            w[0] = x[0];
-            w[1] = x[1];
-          } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(from);
-          }
+          w[half][0] = *reinterpret_cast<const uint32_t*>(from);
+        }
+      }
+    }
+    constexpr float most = kLargest<T>;
+    T out[2][N];
+    const auto read = [&](auto limit) {
 #pragma unroll
-          for (int b = 0; b < N / 4; ++b) {
-            C::values4(w[b], v);
+      for (int half = 0; half < 2; ++half) {
+        const bool finite = scale[half] < bits_f32(kInfBits);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) out[4 * b + r] = (T)(v[r] * scale);
+        for (int b = 0; b < W; ++b) {
+          float v[4];
+          C::values4(w[half][b], v);
+#pragma unroll
+          for (int r = 0; r < 4 && r < N; ++r) {
+            float x = v[r] * scale[half];
+            if (limit && finite) x = x > most ? most : x < -most ? -most : x;   // (a NaN stays)
+            out[half][4 * b + r] = (T)x;
           }
         }
       }
+    };
+    if (__any(fmaxf(scale[0], scale[1]) > most / 512.0f))
+      read(std::true_type{});
+    else
+      read(std::false_type{});
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      T* to = reinterpret_cast<T*>((half ? a.v + t * a.v_t + h * a.v_h
+                                         : a.k + t * a.k_t + h * a.k_h)) + p * N;
       if constexpr (N == 1) {
-        *to = out[0];
+        *to = out[half][0];
       } else {
         static_assert(N * sizeof(T) == 16, "a piece is 16 bytes");
-        *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, out);
+        *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, out[half]);
       }
     }
   }

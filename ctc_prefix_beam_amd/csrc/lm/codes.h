@@ -31,6 +31,12 @@ __device__ inline uint32_t unit_bits(uint32_t most) {
   return (uint32_t)(e < 1 ? 1 : e) << 23;
 }
 
+// The largest finite value of a type.
+template <typename T>
+constexpr float kLargest = __is_same(T, _Float16) ? 65504.0f
+                           : __is_same(T, __bf16) ? 0x1.fep127f
+                                                  : 0x1.fffffep127f;
+
 // What values are multiplied by to become codes: 1 / u, or 0 for a scale that is 0 or not
 // finite, whose codes are 0.
 __device__ inline float inverse_unit(float u) {

@@ -534,7 +534,8 @@ def cache_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
 
 def cache_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloat16, stream=None):
     """(k, v), both (tokens, kv_heads, head_dim) of `dtype`: what the slots (int32 (tokens,)) of
-    an 8-bit cache hold, code times scale; zeros for a token without a slot (-1)."""
+    an 8-bit cache hold, code times scale, as the largest value of `dtype` where a finite product
+    is past it; zeros for a token without a slot (-1)."""
     dev = _gpu(slots, "slots")
     T = slots.numel()
     _i32(slots, dev, "slots", (T,))

@@ -185,7 +185,9 @@ typedef struct {
  * (e4m3: half a step as ever, and less than one of the smallest codes).  A value that is not finite
  * makes the scale NaN, which the page keeps until it begins anew.
  *   k, v     device, typed: element (t, head, d) at t*stride_t + head*stride_h + d;
- *            read by the store, written by the load (code * scale, rounded)
+ *            read by the store, written by the load (code * scale, rounded; the type's
+ *            largest value where a finite product is past it, as the nearest code to a value
+ *            next to that may make it)
  *   slots    device int32 [tokens]; tokens whose slot is outside
  *            [0, num_pages*page_size) are left out by the store, zeros by the
  *            load.  For the store they are distinct, and tokens of one page
