@@ -162,6 +162,7 @@ struct Tile {
   static constexpr int kRangeOnSimd = DP == 64 ? 4 : DP == 128 ? 3 : 1;   // and ranges
   static constexpr int kTokens = 32;
   static constexpr bool kWalks = false;   // has a loop over tiles of its own
+  static constexpr bool kLimit = false;   // values may be past the type's largest
   static constexpr int kK = DP / 32;            // k-steps of the score product
   static constexpr int kV = DP >= 128 ? 8 : 4;  // values a lane loads at once
   static constexpr int kH = DP / 16 / kV;       // such loads per token
@@ -330,6 +331,7 @@ struct Tile<float, DP> {
   static constexpr int kRangeOnSimd = DP == 64 ? 4 : 1;
   static constexpr int kTokens = 16;
   static constexpr bool kWalks = false;
+  static constexpr bool kLimit = false;
   static constexpr int kK = DP / 16;
   static constexpr int kH = DP / 64;
   static constexpr int kAcc = DP / 16;
@@ -449,8 +451,9 @@ struct Tile<float, DP> {
   }
 };
 
-// Stores N neighbouring values of a head's output, rounded.
-template <typename T, int N>
+// Stores N neighbouring values of a head's output, rounded.  LIMIT: a finite one past f16's largest
+// becomes that.
+template <typename T, int N, bool LIMIT>
 __device__ inline void store_run(const AttnArgs& a, int row, int head, int d, const float (&v)[N]) {
   if (d >= a.D) return;
   T* to = reinterpret_cast<T*>(a.out) + row * a.out_r + head * a.out_h + d;
@@ -460,7 +463,11 @@ __device__ inline void store_run(const AttnArgs& a, int row, int head, int d, co
   for (int x = 0; x < N; x += M) {
     TM t;
 #pragma unroll
-    for (int i = 0; i < M; ++i) t[i] = (T)v[x + i];
+    for (int i = 0; i < M; ++i) {
+      float y = v[x + i];
+      if (LIMIT && fabsf(y) < __builtin_huge_valf()) y = fminf(fmaxf(y, -65504.0f), 65504.0f);
+      t[i] = (T)y;
+    }
     if (a.wide_out) {
       *reinterpret_cast<TM*>(to + x) = t;
     } else {
@@ -575,7 +582,7 @@ struct Attend {
       } else {
         const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
         const float v[4] = {o[0] * scale, o[1] * scale, o[2] * scale, o[3] * scale};
-        store_run<T, 4>(a, row, head0 + h, d, v);
+        store_run<T, 4, TL::kLimit>(a, row, head0 + h, d, v);
         if (d == 0) store_lse(a, row, head0 + h, m, sum);
       }
     }
@@ -638,7 +645,7 @@ void attn_kernel(typename TL::Args a) {
         float v[A::kRun];
 #pragma unroll
         for (int j = 0; j < A::kRun; ++j) v[j] = at.s.acc[b * A::kRun + j][r] * scale;
-        store_run<typename TL::Type, A::kRun>(a, row, at.head0 + c, TL::run_of(b, r), v);
+        store_run<typename TL::Type, A::kRun, TL::kLimit>(a, row, at.head0 + c, TL::run_of(b, r), v);
       }
     if (lane < 16) store_lse(a, row, at.head0 + c, at.s.m, l);
   }
@@ -803,7 +810,7 @@ __global__ __launch_bounds__(256) void join_kernel(typename TL::Args a, int ways
   if (!in) return;
   const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
   const float v[4] = {o[0] * scale, o[1] * scale, o[2] * scale, o[3] * scale};
-  store_run<T, 4>(a, row, head, d, v);
+  store_run<T, 4, TL::kLimit>(a, row, head, d, v);
   if (lane == 0) store_lse(a, row, head, m, sum);
 }
 

@@ -80,6 +80,8 @@ struct Tile8 {
   static constexpr int kRangeOnSimd = DP == 64 ? 4 : DP == 128 ? 3 : 2;
   static constexpr int kTokens = 32;
   static constexpr bool kWalks = true;
+  // code times scale may be 65536 where 65504 was stored
+  static constexpr bool kLimit = __is_same(T, _Float16);
   static constexpr int kK = DP / 64;       // 16-byte loads of a key's row for a lane
   static constexpr int kV = DP / 16;       // bytes of a value's row
   static constexpr int kAcc = DP / 16;

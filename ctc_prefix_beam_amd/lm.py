@@ -557,7 +557,8 @@ def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: fl
                window: int = 0, max_len: int = 0, out=None, stream=None):
     """``attention`` over caches of 8-bit codes (int8 or float8_e4m3fn) with float32 scales
     (pages, kv_heads) >= 0: keys and values are code times scale of their page and head.  q and
-    out are bfloat16, float16 or float32; head_dim is a multiple of 16.  `out` may be q."""
+    out are bfloat16, float16 or float32 (finite results past float16's end become its largest
+    value); head_dim is a multiple of 16.  `out` may be q."""
     dev = _gpu(q, "q")
     if q.requires_grad:
         _no_gradient("attention8")

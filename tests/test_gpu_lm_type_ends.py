@@ -86,3 +86,31 @@ def test_what_is_not_finite_stays_so(D):
     cache[2].fill_(math.inf)
     k, _ = lm.cache_load8(slots, *cache, dtype=torch.float16)
     assert not torch.isfinite(k).any()
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows,n", [(4, 8), (3000, 8), (2, 6000)])   # each launch form
+def test_attention_over_values_at_the_end_of_f16(code, D, rows, n):
+    """Every token's values lie between 0.99 and 1 of the largest one, with the same signs: so do the
+    results.  Codes are half a step off (u / 2, and 1/16 for e4m3's), never past the end."""
+    page, kept = 8, -(-n // 8)
+    g = torch.Generator().manual_seed(D)
+    v = (65504 * (0.99 + 0.01 * torch.rand((kept * page, 1, D), generator=g))).to(torch.float16)
+    v[0] = 65504
+    v[..., ::2] *= -1
+    v = v.cuda()
+    kc = torch.zeros((kept, page, 1, D), dtype=torch.int8, device="cuda").view(code)
+    vc, ks, vs = kc.clone(), torch.zeros((kept, 1), device="cuda"), torch.zeros((kept, 1), device="cuda")
+    slots = torch.arange(kept * page, dtype=torch.int32, device="cuda")
+    lm.cache_store8(torch.zeros_like(v), v, slots, kc, vc, ks, vs)
+    tables = torch.arange(kept, dtype=torch.int32, device="cuda").repeat(rows, 1)
+    lens = torch.full((rows,), n, dtype=torch.int32, device="cuda")
+    lens[0] = 1
+    q = torch.randn((rows, 2, D), device="cuda").to(torch.float16)
+    out, _ = lm.attention8(q, kc, vc, ks, vs, tables, lens)
+    assert torch.isfinite(out).all()
+    sign = v[0, 0].sign().float()
+    assert (out.float() * sign <= 65504).all()
+    assert (out.float() * sign >= 65504 * 0.99 * (1 - 1 / 16 - 2.0 ** -10)).all()
+    assert (out[0].float() == 65504 * sign).all()
