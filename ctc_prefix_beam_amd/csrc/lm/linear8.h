@@ -250,8 +250,10 @@ struct Linear8Epilogue {
       }
       return;
     }
-    // rows of 32 values on 8 bytes, and not all in the same banks
-    constexpr int kPitch = 32 + 8 / (int)sizeof(T);
+    // rows of 32 values, not all in the same banks, that begin where four can be stored at once
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    constexpr int kPitch = 32 + 4;
+    static_assert(kPitch * sizeof(T) % sizeof(T4) == 0, "rows begin between two stores");
     __shared__ __align__(16) T stage[WIDE ? 1 : WM * WN][WIDE ? 1 : 16 * kPitch];
     const float* mine = got + wm * TM * 16 + g * 4;
 #pragma unroll
@@ -289,7 +291,6 @@ struct Linear8Epilogue {
           T* at = stage[wm * WN + wn];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            typedef T T4 __attribute__((ext_vector_type(4)));
             T4 v;
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = (T)y[h][r];
