@@ -250,9 +250,10 @@ struct Linear8Epilogue {
       }
       return;
     }
-    // rows of 32 values, not all in the same banks, that begin where four can be stored at once
+    // kWide channels of 16 rows, which lie in different banks and begin where four values can be
+    // stored at once.  Of f32 half as many, so that as many workgroups share a CU as without.
     typedef T T4 __attribute__((ext_vector_type(4)));
-    constexpr int kPitch = 32 + 4;
+    constexpr int kHalves = sizeof(T) == 2 ? 2 : 1, kWide = kHalves * 16, kPitch = kWide + 4;
     static_assert(kPitch * sizeof(T) % sizeof(T4) == 0, "rows begin between two stores");
     __shared__ __align__(16) T stage[WIDE ? 1 : WM * WN][WIDE ? 1 : 16 * kPitch];
     const float* mine = got + wm * TM * 16 + g * 4;
@@ -289,22 +290,26 @@ struct Linear8Epilogue {
           // values of a few rows, not a few of many (8192 x 8191 x 2048 bf16 169 us a call, 222
           // without)
           T* at = stage[wm * WN + wn];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            T4 v;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = (T)y[h][r];
-            *reinterpret_cast<T4*>(at + c * kPitch + h * 16 + g * 4) = v;
-          }
-          __builtin_amdgcn_wave_barrier();
           const int first = n - c;   // of the tile's 16 rows
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int row = q * 2 + (lane >> 5), mm = lane & 31;
-            const T v = at[row * kPitch + mm];
-            if (first + row < N && m + mm < M) out[(int64_t)(first + row) * ld + m + mm] = v;
+          for (int part = 0; part < 2; part += kHalves) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              T4 v;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = (T)y[part + h][r];
+              *reinterpret_cast<T4*>(at + c * kPitch + h * 16 + g * 4) = v;
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int q = 0; q < kWide / 4; ++q) {
+              const int row = (q * 64 + lane) / kWide, mm = lane % kWide;
+              const T v = at[row * kPitch + mm];
+              const int ch = m + part * 16 + mm;
+              if (first + row < N && ch < M) out[(int64_t)(first + row) * ld + ch] = v;
+            }
+            __builtin_amdgcn_wave_barrier();
           }
-          __builtin_amdgcn_wave_barrier();
         }
       }
     }
