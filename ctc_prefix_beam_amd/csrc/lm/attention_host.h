@@ -92,13 +92,21 @@ inline int attention_args(const ctcpb_lm_attention_args& g, const AttnPlan& p, i
   return CTCPB_OK;
 }
 
+// A CU's LDS, of which kernels that are given theirs at the launch have none of their own.
+constexpr int kLds = 160 * 1024;
+
+// Whether `kernel` was launched; if not, the error is the thread's last one.  How much LDS a kernel
+// may be given is noted for the kernel, not for the call: always the same, so that calls of
+// several threads do not take it from each other.
 template <typename K, typename Args>
-void launch_with_lds(K kernel, unsigned blocks, int threads, size_t lds, const Args& a,
+bool launch_with_lds(K kernel, unsigned blocks, int threads, size_t lds, const Args& a,
                      hipStream_t st) {
-  if (lds > 65536)   // more dynamic LDS than a kernel has unasked
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (lds > 65536 &&   // more than a kernel has unasked
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds) != hipSuccess)
+    return false;
   kernel<<<blocks, threads, lds, st>>>(a);
+  return true;
 }
 
 template <typename TL>
@@ -110,10 +118,10 @@ void launch_tiles_of(const typename TL::Args& a, const AttnPlan& p, hipStream_t 
     constexpr int NW = TL::kDP <= 128 ? 8 : 4;
     launch_with_lds(attn_kernel<TL, NW>, (unsigned)p.items, 64 * NW, NW * state, a, st);
   } else {
-    launch_with_lds(attn_range_kernel<TL>,
-                    (unsigned)((int64_t)p.ranges * a.kv_heads * a.head_tiles), 64 * kRangeWaves,
-                    kRangeWaves * state, a, st);
-    if (p.ranges == 1) return;   // no row is split
+    const bool done = launch_with_lds(
+        attn_range_kernel<TL>, (unsigned)((int64_t)p.ranges * a.kv_heads * a.head_tiles),
+        64 * kRangeWaves, kRangeWaves * state, a, st);
+    if (!done || p.ranges == 1) return;   // (one range: no row is split)
     constexpr int kGroups = 256 / (TL::kDP / 4);
     const int64_t heads = (int64_t)a.rows * a.heads;
     // a workgroup to each head while that does not make more than a few to a CU

@@ -311,7 +311,7 @@ void launch_few(const FewArgs& a, hipStream_t st) {
   const int tiles = ceil_div(a.features, 16);
   const size_t lds =
       (size_t)a.rows * (up(a.padded, 64) + 16) + 16 * NT * 1024 + a.rows * sizeof(float);
-  static_assert(kFewCodes + 32 * 16 + 32 * 1024 + 32 * 4 <= 160 * 1024, "more LDS than there is");
+  static_assert(kFewCodes + 32 * 16 + 32 * 1024 + 32 * 4 <= kLds, "more LDS than there is");
   // Four waves to a tile, and four tiles at a time to a workgroup, where rows are too short for 16
   // and there are tiles enough
   if (tiles <= kCUs || a.padded >= 1024)
