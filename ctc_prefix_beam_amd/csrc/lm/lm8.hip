@@ -404,6 +404,9 @@ int ctcpb_lm_cache_store8(const ctcpb_lm_cache8_args* args, void* stream) {
     if (!args) return fail(CTCPB_ERR_INVALID, kNoArgs);
     if (int rc = check_cache8(*args)) return rc;
     if (args->tokens == 0) return ok();
+    // (as many as a plan has; a chunk's waves look up to 127 tokens past it, in 32 bits)
+    if (args->tokens > 1 << 30)
+      return fail(CTCPB_ERR_UNSUPPORTED, "too many tokens: above 2^30");
     bool wide;
     Cache8Args a = cache8_args(*args, wide);
     // A wave to each token while that makes no more than some waves to each place on the card, else

@@ -190,7 +190,7 @@ typedef struct {
  *            next to that may make it)
  *   slots    device int32 [tokens]; tokens whose slot is outside
  *            [0, num_pages*page_size) are left out by the store, zeros by the
- *            load.  For the store they are distinct, and tokens of one page
+ *            load.  For the store they are at most 2^30, distinct, and tokens of one page
  *            follow one another, as ctcpb_lm_cache_plan lays them out (in any order within
  *            the page, and with tokens without a slot between them): a page that comes
  *            twice, with another one between, gets either scale and mixed codes.

@@ -23,6 +23,12 @@ def linear(rows, hidden, features=64, dtype=0):
     return L.ctcpb_lm_linear8(lm._LINEAR8.pack(P, P, P, P, 0, P, hidden, hidden, features, 3, dtype,
                                                rows, features, hidden, 0), P, 1 << 40, None)
 
+def store(tokens, heads=1, D=1, page=16, name="cache_store8"):
+    cache = (P, page * D * heads, D * heads, D)
+    return getattr(L, "ctcpb_lm_" + name)(lm._CACHE8.pack(
+        P, P, P, 0, 0, 0, 0, *cache, *cache, P, 1, 1, P, 1, 1, 0, 0, tokens, (1 << 30) // page, page,
+        heads, D), None)
+
 def attend(rows, n, D, group, eight, dtype=0):
     width = n // 16
     args = (P, P, P, P, 0, group * D, D, group * D, D, width, *(P, 16 * D, D, 16 * D) * 2, dtype, rows,
@@ -90,3 +96,14 @@ def test_a_kernel_that_cannot_have_its_lds_is_not_launched(run):
         assert rc == 4 and "invalid" in error
         assert [n[0] for n in notes] == ["set"]
         assert again == 0 and none == "" and any(n[0] == "launch" for n in after)
+
+
+def test_a_store_counts_its_tokens_in_32_bits(run):
+    """The search for the end of a page's tokens looks up to 64 + 63 past the last one of a chunk:
+    as cache_plan, a store takes 2^30 tokens at most."""
+    most = 1 << 30
+    got = run(*[(0, "store", (n, 1, 1, 64)) for n in (most, most + 1, 2 ** 31 - 1)],
+              (0, "store", (2 ** 31 - 1, 1, 1, 64, "cache_load8")))
+    assert [g[0] for g in got] == [0, 3, 3, 0]
+    assert [len(g[2]) for g in got] == [1, 0, 0, 1]
+    assert "too many tokens" in got[1][1]
