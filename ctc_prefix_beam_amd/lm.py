@@ -195,22 +195,34 @@ def _apart(t, strides, name):
         raise ValueError(f"{name} is written, and must not have expanded axes")
 
 
+def _meet(a, b, d):
+    """Whether two strided sets of bytes may share some.  a, b: (bytes from the first one to
+    behind the last, item size, ((stride, count), ...) by descending stride); the second begins `d`
+    behind the first.  False is certain."""
+    if d >= a[0] or -d >= b[0]:
+        return False
+    if not a[2] or not b[2] or a[2][0][0] != b[2][0][0]:
+        return True
+    # both lie in strips `step` apart: a strip of the second beside each one of the first
+    step = a[2][0][0]
+    a, b = ((sum(s * (n - 1) for s, n in x[2][1:]) + x[1], x[1], x[2][1:]) for x in (a, b))
+    if a[0] > step or b[0] > step:
+        return True
+    return _meet(a, b, d % step) or _meet(a, b, d % step - step)
+
+
 def _off(out, t, name):
     """Raise ValueError if `out`, which is written, may overlap the input `t`: what a part of the
     kernel has written, another would read."""
-    ends = [(a, a + sum((n - 1) * s for n, s in zip(b.shape, b.stride())) * b.itemsize + b.itemsize)
-            for b in (out, t) for a in (b.data_ptr(),)]
-    (a, a_end), (b, b_end) = ends
-    if a >= b_end or b >= a_end or not out.numel() or not t.numel():
+    if not out.numel() or not t.numel():
         return
-    if out.dim() == t.dim() == 2:   # columns of one matrix, side by side
-        step = out.stride(0) * out.itemsize
-        if 0 < step == t.stride(0) * t.itemsize:
-            width = out.shape[1] * out.itemsize
-            at = (b - a) % step
-            if at >= width and at + t.shape[1] * t.itemsize <= step:
-                return
-    raise ValueError(f"out must not overlap {name}")
+    sets = []
+    for x in (out, t):
+        axes = sorted(((s * x.itemsize, n) for s, n in zip(x.stride(), x.shape) if s and n > 1),
+                      reverse=True)
+        sets.append((sum(s * (n - 1) for s, n in axes) + x.itemsize, x.itemsize, axes))
+    if _meet(*sets, t.data_ptr() - out.data_ptr()):
+        raise ValueError(f"out must not overlap {name}")
 
 
 def _type(t, name):
