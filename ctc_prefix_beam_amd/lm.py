@@ -488,7 +488,7 @@ def _codes(t, name):
     return code
 
 
-def _cache8(k_cache, v_cache, k_scale, v_scale, index, written):
+def _cache8(k_cache, v_cache, k_scale, v_scale, index, written, caller):
     """(code, (pages, page_size, heads, dim), the caches' and scales' addresses and strides)."""
     _gpu(k_cache, "k_cache")
     dtype = k_cache.dtype
@@ -499,6 +499,9 @@ def _cache8(k_cache, v_cache, k_scale, v_scale, index, written):
     each = (shape[0], shape[2])
     _like(k_scale, index, "k_scale", torch.float32, each)
     _like(v_scale, index, "v_scale", torch.float32, each)
+    if (k_cache.requires_grad or v_cache.requires_grad or k_scale.requires_grad or
+            v_scale.requires_grad):
+        _no_gradient(caller)
     ks, vs = k_scale.stride(), v_scale.stride()
     if written:
         _apart(k_cache, kc[1:], "k_cache")
@@ -534,7 +537,7 @@ def cache_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     T, H, D = shape
     _i32(slots, dev, "slots", (T,))
     code, (pages, page_size, heads, dim), caches, scales = _cache8(
-        k_cache, v_cache, k_scale, v_scale, dev, True)
+        k_cache, v_cache, k_scale, v_scale, dev, True, "cache_store8")
     if heads != H or dim != D:
         raise ValueError(f"caches must have {H} heads of {D}, got {(heads, dim)}")
     if T == 0:
@@ -555,7 +558,7 @@ def cache_load8(slots, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloat16,
     if dt is None:
         raise ValueError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     code, (pages, page_size, H, D), caches, scales = _cache8(
-        k_cache, v_cache, k_scale, v_scale, dev, False)
+        k_cache, v_cache, k_scale, v_scale, dev, False, "cache_load8")
     raw, empty = _on(stream, dev)
     both = empty((2, T, H, D), dtype=dtype, device=slots.device)
     at = both.data_ptr()
@@ -578,7 +581,7 @@ def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: fl
     qr, qh, shape = _rows(q, "q")
     R, Hq, D = shape
     code, (pages, page_size, Hkv, Dk), caches, scales = _cache8(
-        k_cache, v_cache, k_scale, v_scale, dev, False)
+        k_cache, v_cache, k_scale, v_scale, dev, False, "attention8")
     if Dk != D:
         raise ValueError(f"caches must have heads of {D}, got {Dk}")
     stride, width = _tables(tables, dev, R)
@@ -589,6 +592,8 @@ def attention8(q, k_cache, v_cache, k_scale, v_scale, tables, lengths, scale: fl
         out = empty(shape, dtype=q.dtype, device=q.device)
     else:
         _like(out, dev, "out", q.dtype, shape)
+        if out.requires_grad:
+            _no_gradient("attention8")
         if out.data_ptr() != q.data_ptr() or out.stride() != q.stride():
             _off(out, q, "q")
     outr, outh, _ = _rows(out, "out")
@@ -686,6 +691,8 @@ def linear8(x, w, w_scale, bias=None, x_scale=None, dtype=None, out=None, stream
         out = empty((N, M), dtype=dtype, device=x.device)
     else:
         _like(out, dev, "out", dtype, (N, M))
+        if out.requires_grad:
+            _no_gradient("linear8")
         for t, name in ((x, "x"), (w, "w"), (w_scale, "w_scale"), (bias, "bias"),
                         (x_scale, "x_scale")):
             if t is not None:
