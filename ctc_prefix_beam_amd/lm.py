@@ -723,7 +723,7 @@ class PagedCache:
     flagged in the plan's status and holds only the tokens that have a slot.  Use
     one PagedCache per stream, or order its calls.
 
-    With `dtype` int8 or float8_e4m3fn the cache holds codes, and ``k_scale`` and ``v_scale``
+    With `dtype` int8 or float8_e4m3fn (head_dim a multiple of 16) the cache holds codes, and ``k_scale`` and ``v_scale``
     (layers, num_pages, kv_heads) their scales: ``store`` quantises (``cache_store8``), ``attend``
     is ``attention8``, and ``load(slots, layer)`` reads tokens back in 16 or 32 bits.
 
@@ -738,6 +738,9 @@ class PagedCache:
             raise ValueError("page_size must be a power of two in 4..256")
         if min(rows, max_len, num_pages) < 0:
             raise ValueError("rows, max_len and num_pages must be >= 0")
+        if dtype in _CODES and (head_dim % 16 or not 0 < head_dim <= 256):   # what attend takes
+            raise ValueError("head_dim must be a multiple of 16 up to 256 with a dtype of codes, "
+                             f"got {head_dim}")
         width = -(-max_len // page_size)
         num_pages = num_pages or max(1, rows * width)
         self.page_size, self.max_len = page_size, width * page_size
