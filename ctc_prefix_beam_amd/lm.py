@@ -523,8 +523,8 @@ def cache_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     kv_heads, head_dim)) with float32 scales (pages, kv_heads).  A page's scale is the least
     power of two with which the largest code (127 or 448) reaches all that was written to it; it
     starts with the token of slot 0, which begins the page anew, and later tokens can only raise
-    it: what the page holds is then rescaled.  Slots are distinct, and the tokens of a page follow
-    one another, as ``cache_plan`` lays them out.  Values are at most half a step off, rescaled
+    it: what the page holds is then rescaled.  Slots are distinct, 2^30 at most, and the tokens of
+    a page follow one another, as ``cache_plan`` lays them out (``cache_store`` takes any order).  Values are at most half a step off, rescaled
     ones less than one; one that is not finite makes its page's scale NaN, until the page
     begins anew."""
     dev = _gpu(k, "k")
@@ -725,7 +725,11 @@ class PagedCache:
 
     With `dtype` int8 or float8_e4m3fn (head_dim a multiple of 16) the cache holds codes, and ``k_scale`` and ``v_scale``
     (layers, num_pages, kv_heads) their scales: ``store`` quantises (``cache_store8``), ``attend``
-    is ``attention8``, and ``load(slots, layer)`` reads tokens back in 16 or 32 bits.
+    is ``attention8``, and ``load(slots, layer)`` reads tokens back in 16 or 32 bits.  A page's
+    tokens share a scale, so ``store`` then needs what ``append`` gives: the tokens of a page one
+    after another in the call.  (In 16 and 32 bits tokens may come in any order.)  Tokens of a page
+    with those of another one between them would be done at the same time, and leave the page
+    with either scale and codes of both.
 
     An append goes on to the plan's new lengths, so a captured one repeats the same
     step when it is replayed.  To capture a step that moves on, call ``cache_plan``
