@@ -524,9 +524,9 @@ def cache_store8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     power of two with which the largest code (127 or 448) reaches all that was written to it; it
     starts with the token of slot 0, which begins the page anew, and later tokens can only raise
     it: what the page holds is then rescaled.  Slots are distinct, 2^30 at most, and the tokens of
-    a page follow one another, as ``cache_plan`` lays them out (``cache_store`` takes any order).  Values are at most half a step off, rescaled
-    ones less than one; one that is not finite makes its page's scale NaN, until the page
-    begins anew."""
+    a page follow one another, as ``cache_plan`` lays them out (``cache_store`` takes any order).
+    Values are at most half a step off, rescaled ones less than one; one that is not finite makes
+    its page's scale NaN, until the page begins anew."""
     dev = _gpu(k, "k")
     dt = _type(k, "k")
     kt, kh, shape = _rows(k, "k")
