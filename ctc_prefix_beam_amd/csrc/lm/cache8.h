@@ -310,79 +310,86 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Arg
 // ------------------------------------------------------------------ load --
 //
 // k[t, h] = code * scale of the token's slot, in T; zeros for a token without a slot.  A copy,
-// bound by memory: 131072 tokens of 8 x 128 to bf16 147 us, 5.4 TB/s; 500 of 8 x 64 to f32 3.2
-// us. A thread makes 16 bytes of a key's row and the same of the value's.
+// bound by memory: 131072 tokens of 8 x 128 to bf16 162 us, 5.0 TB/s, to f32 320 (4.2); 500 of 8 x
+// 64 to f32 3.4 us.  A thread makes 16 bytes of a key's row, then the same of the value's: with both
+// rows' codes asked for before either is stored, times hang on where the tensors lie (155 or 171 us
+// to bf16, 267 or 342 to f32).  A thread's first piece is found by divisions in 32 bits; in 64 they
+// cost as much as the loads (172 us).
 //
 // What is finite is read as such: the nearest code to a value next to the type's largest one may
 // stand for more (f16 65504 in int8 is 64 * 1024), and is read as the largest.  No code reaches
-// 512, so only scales above a 512th of that have to be looked at, in a branch of the whole wave
-// (the limits cost 24 of 185 us where every value is compared).
+// 512, so only scales above a 512th of that have to be looked at, in a branch of the whole wave.
 template <typename T, typename C, int N>
 __global__ __launch_bounds__(256) void load8_kernel(Cache8Args a) {
-  const int64_t step = (int64_t)gridDim.x * 256;
-  const int32_t row = a.heads * a.per;
-  const int64_t pieces = (int64_t)a.tokens * row;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += step) {
-    const int32_t t = (int32_t)(i / row), rest = (int32_t)(i % row);
-    const int32_t h = rest / a.per, p = rest % a.per;
+  const uint32_t row = (uint32_t)(a.heads * a.per), step = gridDim.x * 256;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;   // (2^28 threads at most)
+  uint32_t t = i / row, rest = i % row;
+  for (; t < (uint32_t)a.tokens; t += step / row, rest += step % row) {
+    if (rest >= row) {
+      rest -= row;
+      if (++t >= (uint32_t)a.tokens) break;
+    }
+    const int32_t h = (int32_t)(rest / (uint32_t)a.per), p = (int32_t)(rest % (uint32_t)a.per);
     const int32_t slot = a.slots[t];
     const bool in = (uint32_t)slot < (uint32_t)a.num_slots;
     const int64_t page = in ? slot >> a.page_log : 0, at = slot & ((1 << a.page_log) - 1);
-    // (0 times a scale of 0 without a slot)
     constexpr int W = N == 1 ? 1 : N / 4;
-    uint32_t w[2][W] = {};
+    constexpr float most = kLargest<T>;
+    // (0 times a scale of 0 without a slot)
     float scale[2] = {0.0f, 0.0f};
     if (in) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const CacheView& c = half ? a.vc : a.kc;
-        const ScaleView& sc = half ? a.vs : a.ks;
-        const char* from = c.data + page * c.page + at * c.token + h * c.head + p * N;
-        scale[half] = sc.data[page * sc.page + h * sc.head];
-        if constexpr (N == 1) {
-          w[half][0] = *reinterpret_cast<const uint8_t*>(from);
-        } else if constexpr (N == 8) {
-          const u32x2 x = *reinterpret_cast<const u32x2*>(from);
-          w[half][0] = x[0];
-          w[half][1] = x[1];
-        } else {
-          w[half][0] = *reinterpret_cast<const uint32_t*>(from);
-        }
-      }
+      scale[0] = a.ks.data[page * a.ks.page + h * a.ks.head];
+      scale[1] = a.vs.data[page * a.vs.page + h * a.vs.head];
     }
-    constexpr float most = kLargest<T>;
-    T out[2][N];
-    const auto read = [&](auto limit) {
+    const auto load = [&](int half, uint32_t (&w)[W]) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const bool finite = scale[half] < bits_f32(kInfBits);
-#pragma unroll
-        for (int b = 0; b < W; ++b) {
-          float v[4];
-          C::values4(w[half][b], v);
-#pragma unroll
-          for (int r = 0; r < 4 && r < N; ++r) {
-            float x = v[r] * scale[half];
-            if (limit && finite) x = x > most ? most : x < -most ? -most : x;   // (a NaN stays)
-            out[half][4 * b + r] = (T)x;
-          }
-        }
+      for (uint32_t& x : w) x = 0;
+      if (!in) return;
+      const CacheView& c = half ? a.vc : a.kc;
+      const char* from = c.data + page * c.page + at * c.token + h * c.head + p * N;
+      if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint8_t*>(from);
+      } else if constexpr (N == 8) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(from);
+        w[0] = x[0];
+        w[1] = x[1];
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(from);
       }
     };
-    if (__any(fmaxf(scale[0], scale[1]) > most / 512.0f))
-      read(std::true_type{});
-    else
-      read(std::false_type{});
+    const auto store = [&](int half, const uint32_t (&w)[W], auto limit) {
+      T out[N];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+      for (int b = 0; b < W; ++b) {
+        float v[4];
+        C::values4(w[b], v);
+#pragma unroll
+        for (int r = 0; r < 4 && r < N; ++r) {
+          float x = v[r] * scale[half];
+          if (limit && scale[half] < bits_f32(kInfBits))
+            x = x > most ? most : x < -most ? -most : x;   // (a NaN stays)
+          out[4 * b + r] = (T)x;
+        }
+      }
       T* to = reinterpret_cast<T*>((half ? a.v + t * a.v_t + h * a.v_h
                                          : a.k + t * a.k_t + h * a.k_h)) + p * N;
       if constexpr (N == 1) {
-        *to = out[half][0];
+        *to = out[0];
       } else {
         static_assert(N * sizeof(T) == 16, "a piece is 16 bytes");
-        *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, out[half]);
+        *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, out);
       }
+    };
+    uint32_t w[W];
+    load(0, w);
+    if (__any(fmaxf(scale[0], scale[1]) > most / 512.0f)) {
+      store(0, w, std::true_type{});
+      load(1, w);
+      store(1, w, std::true_type{});
+    } else {
+      store(0, w, std::false_type{});
+      load(1, w);
+      store(1, w, std::false_type{});
     }
   }
 }
