@@ -24,12 +24,17 @@
 //
 // What bounds it, measured: memory.  256 requests of 1..4095 tokens, 32 query and 8 key/value
 // heads of 128, int8, bf16: 1.08 GB in 209 us, 5.2 TB/s (a copy: 5.0; 16-bit caches 420 us), the
-// matrix units busy in 11 % of the cycles; three requests of up to 131071 tokens, e4m3: 604 MB in
+// matrix units busy in 10 % of the cycles; three requests of up to 131071 tokens, e4m3: 604 MB in
 // 119 us, 5.1 TB/s; 4096 requests of up to 512 tokens, 4 heads of 64, e4m3, f16: 542 MB in 131 us
 // token by token and 121 head by head (full rows: 5.1 TB/s; the rest is the start and end of
 // short ones).  Four waves a SIMD for heads of 128 spill (302 us for the 256 requests), five for
 // heads of 64 too (156 for the 4096); two sets of registers for tiles, to fetch two ahead, leave
-// two waves and take 225.
+// two waves and take 225.  Some of what is kept spills as well, mostly outside the loop over tiles:
+// ranges of int8 codes with heads of 64 seven registers; all ranges with f32 q, of which there are
+// two halves, 8 to 23; and f32 heads of 256 with a wave to an item 4 and 9.  Inside the loop are up
+// to four of 885 instructions, for f32 heads of 256.  256 requests of up to 1024 tokens, 8 heads of
+// 64, f32: 51 us for 134 MB, half of a copy's rate.  A tile costs as many vector instructions for
+// one query head as for 16.
 //
 // Layout of a tile of 32 tokens: as for 16-bit types, but a lane (g, c) has 16 bytes of a key's
 // row at d = 64 k + 16 g (which two k-steps of the product take in that order, q alike) and, of

@@ -44,14 +44,17 @@ __device__ inline uint32_t wave_magnitude(uint32_t most) {
 // one page follow one another in the call, and the waves that have the first of them in their chunk
 // of `chunk` tokens (the one before with a slot lies in another page) do the page's whole
 // run, for one head of the keys or of the values.  A run's values stay in registers
-// between the two passes (maximum, codes) up to kStoreHeld pieces a lane; W is chosen so that
-// those of a page do.
+// between the two passes (maximum, codes) up to kStoreHeld pieces a lane.  W is chosen so that
+// those of a page do, up to four waves' 1024 pieces (16 KB of a head); of longer pages, and of those
+// that single waves do in calls of few tokens, values that do not fit are read twice.
 //
-// Bound by memory for prompts: 131072 tokens of 8 x 128 bf16, read and written 805 MB, 167 us in
-// pages of 16, 172 of 32, 169 of 64 (4.8 TB/s; a wave to each page: 167, 319, 527); by latency
-// for a step of single tokens, 6 us for 256.  Where half the registers hold a run, a wave does the
-// keys' and the values' (B = 2 below): 131072 tokens of 8 x 64 bf16 in pages of 16, stored and
-// read back, 175 us, against 195 with a wave to each; 16 x 32 204 and 268.
+// Bound by memory for prompts: 131072 tokens of 8 x 128 bf16, read and written 805 MB, 163 us in
+// pages of 16 (4.9 TB/s; 176 to 186 behind a load), 182 of 32, 176 of 64, 352 of 256, which are
+// read twice; a wave to each page of 32 or 64 took 319 and 527.  f32: 292 us in pages of 4, 306 of
+// 16, 324 of 64 (1.34 GB, 4.2 to 4.6 TB/s), 556 of 256.  By latency for a step of single tokens, 6
+// us for 256.  Where half the registers hold a run, a wave does the keys' and the values' (B = 2
+// below): 131072 tokens of 8 x 64 bf16 in pages of 16 91 us; stored and read back 175, against 195
+// with a wave to each, and 16 x 32 204 and 268.
 constexpr int kStoreHeld = 4;
 
 // The page of the nearest token with a slot before token t, -1 if there is none.
@@ -313,8 +316,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void store8_kernel(Cache8Arg
 // bound by memory: 131072 tokens of 8 x 128 to bf16 162 us, 5.0 TB/s, to f32 320 (4.2); 500 of 8 x
 // 64 to f32 3.4 us.  A thread makes 16 bytes of a key's row, then the same of the value's: with both
 // rows' codes asked for before either is stored, times hang on where the tensors lie (155 or 171 us
-// to bf16, 267 or 342 to f32).  A thread's first piece is found by divisions in 32 bits; in 64 they
-// cost as much as the loads (172 us).
+// to bf16, 267 or 342 to f32).  A thread's first piece is found by divisions in 32 bits: in 64 they
+// took 7 us more.
 //
 // What is finite is read as such: the nearest code to a value next to the type's largest one may
 // stand for more (f16 65504 in int8 is 64 * 1024), and is read as the largest.  No code reaches

@@ -30,7 +30,8 @@ inline size_t up(size_t v, size_t n) { return (v + n - 1) / n * n; }
 // f32 on products of 10^8 to 10^12 multiplications, for each shape: the time that
 // a k-tile of an item takes of its CU when CUs are full (`unit`; 256x256: 1430
 // TFLOP/s with bf16, 145 with f32), and when the item is alone on it (`alone`: its
-// fetches' latency), and a launch's beginning and end (`ends`).
+// fetches' latency), and a launch's beginning and end (`ends`).  int8 takes the figures of
+// bf16, whose k-tiles are as many bytes: they were not measured for it.
 inline double cut_time(int es, const Cut& c, int64_t m, int64_t n) {
   constexpr double unit[2][3] = {{0.26, 0.56, 1.5}, {0.56, 2.05, 0}};
   constexpr double alone[2][3] = {{0.5, 0.73, 1.5}, {0.73, 2.28, 0}};

@@ -155,7 +155,7 @@ struct RowPieces {
 };
 
 // W waves to a row: one, and four rows to a workgroup, or four.  Bound by memory: 20000 rows of
-// 4096 f16 51 us, 4.8 TB/s; 8192 of 2048 bf16 16 us, of which moving the 50 MB takes 10; 875 of
+// 4096 f16 50 to 56 us, up to 4.9 TB/s; 8192 of 2048 bf16 16 us, of which moving the 50 MB takes 10; 875 of
 // 387 f32 4.7 us.  Pieces that begin anywhere (ANY): 4000 rows of 2047 bf16 14.5 us a call, 20.4
 // value by value.
 template <typename T, int N, bool ANY, int W>
@@ -193,9 +193,9 @@ struct TwoFactors {
 };
 
 // The product is that of gemm.h, with its tiles: 128 bytes of k are 128 codes.  Bound by the LDS
-// that feeds the matrix units, which are busy in 48 % of the cycles: 8192 x 8192 x 2048 bf16 126
-// us, 2180 TOP/s, and 8192^3 2440 (the library's int8 product: 1740 and 2080); 20000 x 1024 x
-// 4096 82 us, 2050. One wave to a SIMD with a tile of 128 x 128, which reads a third less from
+// that feeds the matrix units, which are busy in 50 % of the cycles: of codes, 8192 x 8192 x 2048
+// bf16 120 to 127 us, up to 2300 TOP/s, and 8192^3 407 to 411, 2700 (the library's int8 product: 1740
+// and 2080); 20000 x 1024 x 4096 83 us, 2020. One wave to a SIMD with a tile of 128 x 128, which reads a third less from
 // LDS, took 2.3 times as long.
 //
 // What follows a sum: scales and bias, in float32.  Every kernel rounds alike (no product is
@@ -346,9 +346,10 @@ __global__ __launch_bounds__(256) void linear8_join_kernel(Linear8Epilogue<T, fa
 // of its own).  Then KW waves share the k of a tile of 16 channels, 16 / KW tiles at a time; the
 // next tiles' first weights are on their way while the waves' sums are added.  Weights go from
 // memory straight into the registers of the matrix instruction, kFewHeld of them a lane at a
-// time. 32 rows x 5000 channels of 512, bf16: 8.2 us; a row of codes with 8192 channels of 2048
-// (16.8 MB) 7 us.  Long rows are quantised by several waves each: a call of a row of 4096 with 4096
-// channels 10.4 us (12.6 with a launch for that), of 16384 21.8 (29.1).
+// time.  On the GPU, with weights that its caches hold: 32 rows x 5000 channels of 512, bf16, 8.1
+// us; a row of codes with 8192 channels of 2048 (16.8 MB) 5.7.  Long rows are quantised by several
+// waves each: a row of 4096 with 4096 channels 6.4 us (8.3 with a launch for that), of 16384 17.5
+// (24.9).
 constexpr int32_t kFewValues = 16384;
 constexpr int32_t kFewCodes = 124 * 1024;   // of a CU's 160 KB of LDS; the waves' sums take 32 KB
 constexpr int kFewHeld = 8;

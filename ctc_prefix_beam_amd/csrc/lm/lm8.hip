@@ -211,11 +211,13 @@ LinearPlan plan_linear8(const ctcpb_lm_linear8_args& g) {
   // there, w may have anything.
   p.pad_x = !p.quantize && (g.hidden % 16 != 0 || !codes_aligned(g.x, g.stride_x));
   p.pad_w = (g.hidden % 16 != 0 && !readable) || !codes_aligned(g.w, g.stride_w);
-  // In us, one launch for few rows of codes / the product's tiles: 5000 channels of 512 6.6 and
-  // 7.0 for a row, 8.3 and 7.1 for 32; 2048 of 2048 6.6 and 10.6, 8.0 and 10.4; 8192 of 2048 9.5
-  // and 13.4, 10.8 and 15.8; 50000 of 2048 22.8 and 23.6, 32 and 25.  With x quantised there /
-  // before it: 16 rows of 512 8.6 and 10.6, 32 10.8 and 10.9 (and a launch less), 16 of 1024 10.5
-  // and 11.5, 8 of 2048 10.0 and 10.8, 16 of them 11.3 and 11.0.
+  // On the GPU in us, with weights that its caches hold, one launch for few rows of codes / the
+  // product's tiles: 5000 channels of 512 4.2 and 4.3 for a row, 4.8 and 4.3 for 16, 6.0 and 4.5 for
+  // 32; 2048 of 2048 4.4 and 7.7, 4.7 and 7.2, 5.8 and 7.6; 8192 of 2048 5.7 and 8.4, 6.1 and 9.3,
+  // 7.6 and 7.3; 50000 of 2048 25 and 18, 27 and 20 for 32.  x quantised there / before it, then one
+  // launch / before it, then tiles, 5000 channels: 16 rows of 512 6.1, 7.9, 7.8; 32 8.4, 9.6, 8.1
+  // (and a launch less for the host); 16 of 1024 7.3, 8.6, 9.5; 8 of 2048 7.9, 9.0, 11.4; 16 of
+  // them before it 9.5, tiles 12.0.
   const int64_t values = (int64_t)g.rows * up(p.padded, 64);
   // quantised by the same launch
   const bool there = p.quantize && values <= kFewValues;

@@ -723,13 +723,13 @@ class PagedCache:
     flagged in the plan's status and holds only the tokens that have a slot.  Use
     one PagedCache per stream, or order its calls.
 
-    With `dtype` int8 or float8_e4m3fn (head_dim a multiple of 16) the cache holds codes, and ``k_scale`` and ``v_scale``
-    (layers, num_pages, kv_heads) their scales: ``store`` quantises (``cache_store8``), ``attend``
-    is ``attention8``, and ``load(slots, layer)`` reads tokens back in 16 or 32 bits.  A page's
-    tokens share a scale, so ``store`` then needs what ``append`` gives: the tokens of a page one
-    after another in the call.  (In 16 and 32 bits tokens may come in any order.)  Tokens of a page
-    with those of another one between them would be done at the same time, and leave the page
-    with either scale and codes of both.
+    With `dtype` int8 or float8_e4m3fn (head_dim a multiple of 16) the cache holds codes, and
+    ``k_scale`` and ``v_scale`` (layers, num_pages, kv_heads) their scales: ``store`` quantises
+    (``cache_store8``), ``attend`` is ``attention8``, and ``load(slots, layer)`` reads tokens back
+    in 16 or 32 bits.  A page's tokens share a scale, so ``store`` then needs what ``append`` gives:
+    the tokens of a page one after another in the call.  (In 16 and 32 bits tokens may come in any
+    order.)  Tokens of a page with those of another one between them would be done at the same
+    time, and leave the page with either scale and codes of both.
 
     An append goes on to the plan's new lengths, so a captured one repeats the same
     step when it is replayed.  To capture a step that moves on, call ``cache_plan``

@@ -213,8 +213,8 @@ int ctcpb_lm_cache_load8(const ctcpb_lm_cache8_args* args, void* stream);
  * past a row's length, or before its window in another page, are never used, whatever
  * they hold.  out may be q, but not overlap it otherwise.  Nothing is rounded on the way to
  * fewer than 22 bits; sums are float32 numbers, which values next to 2^128 take past their
- * end.  A finite result past the end of f16 is 65504.  Pages lie less than 4 GiB apart (their scales too), tokens of a page up
- * to 8 MiB. */
+ * end.  A finite result past the end of f16 is 65504.  Pages lie less than 4 GiB apart (their
+ * scales too), tokens of a page up to 8 MiB. */
 typedef struct {
   ctcpb_lm_attention_args base;
   ctcpb_lm_scales k_scale, v_scale;
