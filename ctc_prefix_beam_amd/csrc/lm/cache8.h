@@ -369,7 +369,7 @@ __global__ __launch_bounds__(256) void load8_kernel(Cache8Args a) {
 #pragma unroll
         for (int r = 0; r < 4 && r < N; ++r) {
           float x = v[r] * scale[half];
-          if (limit && scale[half] < bits_f32(kInfBits))
+          if (limit && fabsf(scale[half]) < bits_f32(kInfBits))
             x = x > most ? most : x < -most ? -most : x;   // (a NaN stays)
           out[4 * b + r] = (T)x;
         }
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256) void load8_kernel(Cache8Args a) {
     };
     uint32_t w[W];
     load(0, w);
-    if (__any(fmaxf(scale[0], scale[1]) > most / 512.0f)) {
+    if (__any(fmaxf(fabsf(scale[0]), fabsf(scale[1])) > most / 512.0f)) {
       store(0, w, std::true_type{});
       load(1, w);
       store(1, w, std::true_type{});

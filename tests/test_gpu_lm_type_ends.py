@@ -88,6 +88,15 @@ def test_what_is_not_finite_stays_so(D):
     assert not torch.isfinite(k).any()
 
 
+@pytest.mark.parametrize("D", [64, 5])
+def test_scales_below_zero_turn_the_signs(D):
+    """A store makes none, but a load takes any."""
+    slots, cache = stored(ends(torch.float16, D), torch.int8)
+    k, v = lm.cache_load8(slots, *cache, dtype=torch.float16)
+    got = lm.cache_load8(slots, cache[0], cache[1], -cache[2], -cache[3], dtype=torch.float16)
+    assert torch.equal(got[0], -k) and torch.equal(got[1], -v) and torch.isfinite(k).all()
+
+
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("rows,n", [(4, 8), (3000, 8), (2, 6000)])   # each launch form
